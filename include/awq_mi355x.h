@@ -254,6 +254,113 @@ int awq_w4a16_matmul(const void* X, int64_t n_tokens, int64_t in_features, int64
                      void* stream);
 
 /* ------------------------------------------------------------------------
+ * Packed-weight operators: the layer as awq_pack leaves it, for every group
+ * size it packs, served and trained.  With g(k) = k / group_size,
+ *   W[o, k] = (q[o, k] - zero[o, g(k)]) * step[o, g(k)]
+ * taken without rounding where not said otherwise.
+ *
+ * Common arguments:
+ *   dtype:      the activations' and gradients' type, AWQ_F16 or AWQ_BF16
+ *   n_tokens:   rows of the activations, 1..2^20
+ *   in_features, out_features: as for awq_pack (in_features a multiple of 128)
+ *   half_features: the width of one half of a gated block: the packed matrix
+ *               has 2 * half_features rows, the gate's rows first, then the up
+ *               projection's (a fused layer, as awq_search_layer takes it)
+ *   group_size: 32, 64 or 128
+ *   qweight:    [rows, in_features / 8] int32, nibble j of word w = column 8w + j
+ *   step16, zero16: [rows, in_features / group_size] fp16; zero may be any
+ *               finite fp16 value (awq_pack writes integers).  q - zero is
+ *               rounded once to fp16, which is exact for integer zeros of
+ *               magnitude up to 2032
+ *   workspace:  scratch of at least the matching *_workspace_size bytes; its
+ *               contents on entry do not matter.  A size of 0 means that none
+ *               is used and workspace may be NULL; (size_t)-1 means that the
+ *               arguments are refused (awq_last_error says why)
+ * All pointers are 16-byte aligned, all arrays dense and row-major; an output
+ * or the workspace must not overlap an input or another output.  Sums are
+ * held in binary32 from exact products of 16-bit values; outputs are rounded
+ * once, to nearest even.  bf16 rows are brought to fp16 by a power of two per
+ * row where a product needs it: values below 2^-32 of their row's largest
+ * finite magnitude are then rounded at 2^-40 of it, others stay exact.
+ * Infinities and NaN in a token's row follow IEEE arithmetic on the formula
+ * and stay in that token's outputs.  Results do not depend on what runs
+ * beside a call: sums have a fixed order and no atomics are used.
+ * Errors: AWQ_ERR_INVALID_ARG for NULL, misaligned or overlapping pointers and
+ * sizes out of range; AWQ_ERR_UNSUPPORTED for another group size, type or
+ * activation; AWQ_ERR_WORKSPACE for a short workspace (nothing is enqueued);
+ * AWQ_ERR_HIP for a launch failure.
+ * Source: dev.to page, "What do you actually deploy" (4-bit weights, 16-bit
+ * activations, group size) and quant_config; esaholic.com page, INT4 in INT32
+ * containers and W4A16 GEMM kernels.
+ * ---------------------------------------------------------------------- */
+typedef enum awq_dtype { AWQ_F16 = 0, AWQ_BF16 = 1, AWQ_F32 = 2 } awq_dtype;
+
+/* Gates of the gated block: AWQ_ACT_SILU g / (1 + e^-g);
+ * AWQ_ACT_GELU_TANH g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))). */
+typedef enum awq_activation { AWQ_ACT_SILU = 0, AWQ_ACT_GELU_TANH = 1 } awq_activation;
+
+/* Y[t, o] = sum_k X[t, k] W[o, k].
+ *   X: [n_tokens, in_features] dtype; Y: [n_tokens, out_features] y_dtype,
+ *   which is dtype or AWQ_F32. */
+size_t awq_w4a16_linear_workspace_size(int64_t n_tokens, int64_t in_features, int64_t out_features,
+                                       int group_size, int dtype);
+int awq_w4a16_linear(const void* X, int dtype, int64_t n_tokens, int64_t in_features,
+                     int64_t out_features, int group_size, const int32_t* qweight,
+                     const void* step16, const void* zero16, void* Y, int y_dtype, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* H[t, f] = act(G[t, f]) * U[t, f] with [G | U] = X W^T.  G and U stay in
+ * binary32; H rounds once.
+ *   H:   [n_tokens, half_features] dtype
+ *   pre: [n_tokens, 2 * half_features] dtype or NULL: [G | U] rounded to
+ *        dtype, what awq_w4a16_gated_backward reads */
+size_t awq_w4a16_gated_workspace_size(int64_t n_tokens, int64_t in_features, int64_t half_features,
+                                      int group_size, int dtype);
+int awq_w4a16_gated(const void* X, int dtype, int64_t n_tokens, int64_t in_features,
+                    int64_t half_features, int group_size, int act, const int32_t* qweight,
+                    const void* step16, const void* zero16, void* H, void* pre, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* dX[t, k] = sum_o dY[t, o] W[o, k], the packed codes frozen.  Each W[o, k]
+ * is rounded to fp16 (the step varies along the sum, so it cannot be applied
+ * to sums of exact products).
+ *   dY: [n_tokens, out_features] dtype; dX: [n_tokens, in_features] dtype */
+size_t awq_w4a16_input_grad_workspace_size(int64_t n_tokens, int64_t in_features,
+                                           int64_t out_features, int group_size, int dtype);
+int awq_w4a16_input_grad(const void* dY, int dtype, int64_t n_tokens, int64_t in_features,
+                         int64_t out_features, int group_size, const int32_t* qweight,
+                         const void* step16, const void* zero16, void* dX, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* The gated block's backward pass from the gradient of H and the kept pre:
+ *   dG = dH * U * act'(G), dU = dH * act(G), dpre = [dG | dU] in dtype;
+ *   dX = dpre W, from dpre as stored and W as awq_w4a16_input_grad takes it.
+ *   dH: [n_tokens, half_features]; pre, dpre: [n_tokens, 2 * half_features];
+ *   dX: [n_tokens, in_features]; all dtype.  dpre is also what
+ *   awq_w4a16_param_grad takes as dY for the block's steps and zeros. */
+size_t awq_w4a16_gated_backward_workspace_size(int64_t n_tokens, int64_t in_features,
+                                               int64_t half_features, int group_size, int dtype);
+int awq_w4a16_gated_backward(const void* dH, const void* pre, int dtype, int64_t n_tokens,
+                             int64_t in_features, int64_t half_features, int group_size, int act,
+                             const int32_t* qweight, const void* step16, const void* zero16,
+                             void* dpre, void* dX, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* Gradients of the group parameters, the codes frozen: with D = dY^T X,
+ *   dstep[o, g] = sum over k in g of D[o, k] (q[o, k] - zero[o, g])
+ *   dzero[o, g] = -step[o, g] * sum over k in g of D[o, k]
+ * D is formed tile by tile and never stored.
+ *   dY: [n_tokens, out_features], X: [n_tokens, in_features] dtype;
+ *   dstep, dzero: [out_features, in_features / group_size] fp32, overwritten */
+size_t awq_w4a16_param_grad_workspace_size(int64_t n_tokens, int64_t in_features,
+                                           int64_t out_features, int group_size, int dtype);
+int awq_w4a16_param_grad(const void* dY, const void* X, int dtype, int64_t n_tokens,
+                         int64_t in_features, int64_t out_features, int group_size,
+                         const int32_t* qweight, const void* step16, const void* zero16,
+                         float* dstep, float* dzero, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* ------------------------------------------------------------------------
  * Folding 1/s into whatever produces the layer's input channels:
  *   dst[j, c] = fp16( fp32(src[j, c]) / s[j] )   (IEEE binary32 division)
  * for a [rows, cols] fp16 array whose row j feeds input channel j: a norm's

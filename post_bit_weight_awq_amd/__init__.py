@@ -26,7 +26,8 @@ from ._lib import STAGE_ALL, STAGE_GRID, STAGE_PREPARE, STAGE_SELECT  # noqa: F4
 __all__ = ["AwqConfig", "AwqError", "default_config", "awq_act_stats", "awq_act_stats_noalloc",
            "awq_act_stats_workspace_size", "awq_search_plan", "awq_search_workspace_size",
            "awq_search_layer", "awq_pack", "awq_w4a16_matmul", "awq_fold_inverse_scale", "awq_select_top_channels", "awq_weight_saliency",
-           "SearchResult", "load"]
+           "awq_w4a16_linear", "awq_w4a16_gated", "awq_w4a16_input_grad", "awq_w4a16_gated_backward",
+           "awq_w4a16_param_grad", "SearchResult", "load"]
 
 
 def default_config(n_grid: int = 20, sal_floor: float = 1e-4, *, group_size: int = 128,
@@ -237,6 +238,171 @@ def awq_w4a16_matmul(X: torch.Tensor, qweight: torch.Tensor, step: torch.Tensor,
         ctypes.c_void_p(_dev(out, "out", torch.float32, (n, o))),
         _stream(stream)))
     return out
+
+
+# -------------------------------------------------- packed-weight operators
+_DTYPES = {torch.float16: _lib.DTYPE_F16, torch.bfloat16: _lib.DTYPE_BF16}
+_ACTS = {"silu": _lib.ACT_SILU, "gelu": _lib.ACT_GELU_TANH}
+
+
+def _w4_layer(lead: torch.Tensor, name: str, qweight, step, zero):
+    """Checks a packed layer against the activations or gradients ``lead`` and
+    returns (dtype code, tokens, in_features, rows, group size, pointers)."""
+    if not isinstance(lead, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if lead.dim() != 2 or qweight.dim() != 2 or step.dim() != 2:
+        raise ValueError(f"{name}, qweight and step must be 2-D")
+    dt = _DTYPES.get(lead.dtype)
+    if dt is None:
+        raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {lead.dtype}")
+    o, words = qweight.shape
+    k, ng = 8 * words, step.shape[1]
+    if ng == 0 or k % ng:
+        raise ValueError(f"step has {ng} groups for in_features={k}")
+    ptrs = (_dev(qweight, "qweight", torch.int32, (o, words)),
+            _dev(step, "step", torch.float16, (o, ng)),
+            _dev(zero, "zero", torch.float16, (o, ng)))
+    dev = lead.device
+    if not (qweight.device == step.device == zero.device == dev):
+        raise ValueError(f"{name}, qweight, step and zero must be on one device")
+    if lead.is_cuda and dev.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {dev}, the current device is {torch.cuda.current_device()}")
+    return dt, lead.shape[0], k, o, k // ng, ptrs
+
+
+def _w4_workspace(op: str, n, k, rows, group, dt, dev, workspace):
+    """(pointer, bytes) of the workspace, allocated where the call needs one."""
+    need = getattr(load(), f"awq_w4a16_{op}_workspace_size")(n, k, rows, group, dt)
+    if need == ctypes.c_size_t(-1).value:
+        raise AwqError(_lib.AWQ_ERR_INVALID_ARG, load().awq_last_error().decode())
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if not workspace.is_cuda or workspace.device != dev:
+        raise ValueError(f"workspace must be on {dev}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _w4_out(t, name, dtype, shape, dev):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _dev(t, name, dtype, shape)
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    return t
+
+
+def awq_w4a16_linear(X: torch.Tensor, qweight: torch.Tensor, step: torch.Tensor,
+                     zero: torch.Tensor, *, out: Optional[torch.Tensor] = None,
+                     out_dtype: Optional[torch.dtype] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Y = X W^T with the packed layer (qweight, step, zero) of awq_pack, any of
+    its group sizes; X [n_tokens, in_features] fp16 or bf16, Y in out_dtype
+    (X's type by default, or torch.float32)."""
+    dt, n, k, o, group, ptrs = _w4_layer(X, "X", qweight, step, zero)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else X.dtype
+    if out_dtype != X.dtype and out_dtype != torch.float32:
+        raise TypeError(f"out_dtype must be {X.dtype} or torch.float32, got {out_dtype}")
+    x = _dev(X, "X", X.dtype, (n, k))
+    with _on(stream):
+        out = _w4_out(out, "out", out_dtype, (n, o), X.device)
+        ws, size, _keep = _w4_workspace("linear", n, k, o, group, dt, X.device, workspace)
+    check(load().awq_w4a16_linear(x, dt, n, k, o, group, *ptrs, out.data_ptr(),
+                                  _lib.DTYPE_F32 if out_dtype == torch.float32 else dt, ws, size,
+                                  _stream(stream)))
+    return out
+
+
+def _w4_half(o: int) -> int:
+    if o % 2:
+        raise ValueError(f"a gated layer has the gate's rows and as many up rows, got {o}")
+    return o // 2
+
+
+def _w4_act(act: str) -> int:
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+    return _ACTS[act]
+
+
+def awq_w4a16_gated(X: torch.Tensor, qweight: torch.Tensor, step: torch.Tensor,
+                    zero: torch.Tensor, *, act: str = "silu", keep_pre: bool = False,
+                    out: Optional[torch.Tensor] = None, pre: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, stream=None):
+    """H = act(X Wg^T) * (X Wu^T) in one kernel; the packed layer holds the
+    gate's rows and then the up rows.  With keep_pre (or a pre buffer) returns
+    (H, pre), pre = [G | U] in X's type, which the backward pass reads."""
+    dt, n, k, o, group, ptrs = _w4_layer(X, "X", qweight, step, zero)
+    f, code = _w4_half(o), _w4_act(act)
+    x = _dev(X, "X", X.dtype, (n, k))
+    with _on(stream):
+        out = _w4_out(out, "out", X.dtype, (n, f), X.device)
+        if keep_pre or pre is not None:
+            pre = _w4_out(pre, "pre", X.dtype, (n, o), X.device)
+        ws, size, _keep = _w4_workspace("gated", n, k, f, group, dt, X.device, workspace)
+    check(load().awq_w4a16_gated(x, dt, n, k, f, group, code, *ptrs, out.data_ptr(),
+                                 None if pre is None else pre.data_ptr(), ws, size,
+                                 _stream(stream)))
+    return out if pre is None else (out, pre)
+
+
+def awq_w4a16_input_grad(dY: torch.Tensor, qweight: torch.Tensor, step: torch.Tensor,
+                         zero: torch.Tensor, *, out: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """dX = dY W [n_tokens, in_features] in dY's type, the packed codes frozen."""
+    dt, n, k, o, group, ptrs = _w4_layer(dY, "dY", qweight, step, zero)
+    d = _dev(dY, "dY", dY.dtype, (n, o))
+    with _on(stream):
+        out = _w4_out(out, "out", dY.dtype, (n, k), dY.device)
+        ws, size, _keep = _w4_workspace("input_grad", n, k, o, group, dt, dY.device, workspace)
+    check(load().awq_w4a16_input_grad(d, dt, n, k, o, group, *ptrs, out.data_ptr(), ws, size,
+                                      _stream(stream)))
+    return out
+
+
+def awq_w4a16_gated_backward(dH: torch.Tensor, pre: torch.Tensor, qweight: torch.Tensor,
+                             step: torch.Tensor, zero: torch.Tensor, *, act: str = "silu",
+                             out: Optional[torch.Tensor] = None,
+                             dpre: Optional[torch.Tensor] = None,
+                             workspace: Optional[torch.Tensor] = None, stream=None):
+    """(dX, dpre) of awq_w4a16_gated from the gradient of H and the kept pre;
+    dpre = [dG | dU] is what awq_w4a16_param_grad takes as dY."""
+    dt, n, k, o, group, ptrs = _w4_layer(dH, "dH", qweight, step, zero)
+    f, code = _w4_half(o), _w4_act(act)
+    d = _dev(dH, "dH", dH.dtype, (n, f))
+    p = _dev(pre, "pre", dH.dtype, (n, o))
+    if pre.device != dH.device:
+        raise ValueError(f"pre must be on {dH.device}")
+    with _on(stream):
+        out = _w4_out(out, "out", dH.dtype, (n, k), dH.device)
+        dpre = _w4_out(dpre, "dpre", dH.dtype, (n, o), dH.device)
+        ws, size, _keep = _w4_workspace("gated_backward", n, k, f, group, dt, dH.device, workspace)
+    check(load().awq_w4a16_gated_backward(d, p, dt, n, k, f, group, code, *ptrs, dpre.data_ptr(),
+                                          out.data_ptr(), ws, size, _stream(stream)))
+    return out, dpre
+
+
+def awq_w4a16_param_grad(dY: torch.Tensor, X: torch.Tensor, qweight: torch.Tensor,
+                         step: torch.Tensor, zero: torch.Tensor, *,
+                         dstep: Optional[torch.Tensor] = None,
+                         dzero: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None):
+    """(dstep, dzero), fp32 in step's shape: gradients of the group parameters
+    of Y = X W^T for the output gradient dY, the packed codes frozen."""
+    dt, n, k, o, group, ptrs = _w4_layer(dY, "dY", qweight, step, zero)
+    d = _dev(dY, "dY", dY.dtype, (n, o))
+    x = _dev(X, "X", dY.dtype, (n, k))
+    if X.device != dY.device:
+        raise ValueError(f"X must be on {dY.device}")
+    with _on(stream):
+        dstep = _w4_out(dstep, "dstep", torch.float32, tuple(step.shape), dY.device)
+        dzero = _w4_out(dzero, "dzero", torch.float32, tuple(step.shape), dY.device)
+        ws, size, _keep = _w4_workspace("param_grad", n, k, o, group, dt, dY.device, workspace)
+    check(load().awq_w4a16_param_grad(d, x, dt, n, k, o, group, *ptrs, dstep.data_ptr(),
+                                      dzero.data_ptr(), ws, size, _stream(stream)))
+    return dstep, dzero
 
 
 def awq_fold_inverse_scale(src: torch.Tensor, s: torch.Tensor, *,

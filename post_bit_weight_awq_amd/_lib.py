@@ -25,7 +25,14 @@ EXPORTS = (
     "awq_search_plan_query", "awq_search_workspace_size", "awq_search_layer",
     "awq_search_layer_stages", "awq_pack", "awq_w4a16_matmul", "awq_fold_inverse_scale",
     "awq_select_top_channels",
+    "awq_w4a16_linear_workspace_size", "awq_w4a16_linear",
+    "awq_w4a16_gated_workspace_size", "awq_w4a16_gated",
+    "awq_w4a16_input_grad_workspace_size", "awq_w4a16_input_grad",
+    "awq_w4a16_gated_backward_workspace_size", "awq_w4a16_gated_backward",
+    "awq_w4a16_param_grad_workspace_size", "awq_w4a16_param_grad",
 )
+DTYPE_F16, DTYPE_BF16, DTYPE_F32 = 0, 1, 2
+ACT_SILU, ACT_GELU_TANH = 0, 1
 
 
 class AwqConfig(ctypes.Structure):
@@ -91,6 +98,17 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.awq_fold_inverse_scale.restype = I32
     lib.awq_select_top_channels.argtypes = [P, I64, I64, P, P]
     lib.awq_select_top_channels.restype = I32
+    for op in ("linear", "gated", "input_grad", "gated_backward", "param_grad"):
+        f = getattr(lib, f"awq_w4a16_{op}_workspace_size")
+        f.argtypes = [I64, I64, I64, I32, I32]
+        f.restype = SZ
+        getattr(lib, f"awq_w4a16_{op}").restype = I32
+    lib.awq_w4a16_linear.argtypes = [P, I32, I64, I64, I64, I32, P, P, P, P, I32, P, SZ, P]
+    lib.awq_w4a16_gated.argtypes = [P, I32, I64, I64, I64, I32, I32, P, P, P, P, P, P, SZ, P]
+    lib.awq_w4a16_input_grad.argtypes = [P, I32, I64, I64, I64, I32, P, P, P, P, P, SZ, P]
+    lib.awq_w4a16_gated_backward.argtypes = [P, P, I32, I64, I64, I64, I32, I32, P, P, P, P, P,
+                                             P, SZ, P]
+    lib.awq_w4a16_param_grad.argtypes = [P, P, I32, I64, I64, I64, I32, P, P, P, P, P, P, SZ, P]
     _lib = lib
     return lib
 

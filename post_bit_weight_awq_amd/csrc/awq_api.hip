@@ -85,6 +85,86 @@ int hip_result(hipError_t e, const char* what) {
   return ok();
 }
 
+// Sizes and types of a packed-weight operator; `rows` counts the packed
+// matrix's rows.
+int check_w4(int64_t n_tokens, int64_t in_features, int64_t rows, int group_size, int dtype) {
+  int rc;
+  if ((rc = check_dims(1, in_features, rows, false, true, 128))) return rc;
+  if (n_tokens < 1 || n_tokens > awq::kMaxW4OpTokens)
+    return fail(AWQ_ERR_INVALID_ARG, "n_tokens=%lld outside 1..%lld", (long long)n_tokens,
+                (long long)awq::kMaxW4OpTokens);
+  if (group_size != 128 && group_size != 64 && group_size != 32)
+    return fail(AWQ_ERR_UNSUPPORTED, "group_size=%d: 32, 64 and 128 are implemented", group_size);
+  if (dtype != AWQ_F16 && dtype != AWQ_BF16)
+    return fail(AWQ_ERR_UNSUPPORTED, "dtype=%d: AWQ_F16 and AWQ_BF16 are implemented", dtype);
+  return AWQ_OK;
+}
+
+// The gated forms take half the packed matrix's rows.
+int check_w4_gated(int64_t n_tokens, int64_t in_features, int64_t half, int group_size, int dtype,
+                   int act) {
+  if (half < 1 || half > kMaxFeatures / 2)
+    return fail(AWQ_ERR_INVALID_ARG, "half_features=%lld outside 1..%lld", (long long)half,
+                (long long)(kMaxFeatures / 2));
+  if (act != AWQ_ACT_SILU && act != AWQ_ACT_GELU_TANH)
+    return fail(AWQ_ERR_UNSUPPORTED, "act=%d: AWQ_ACT_SILU and AWQ_ACT_GELU_TANH are implemented",
+                act);
+  return check_w4(n_tokens, in_features, 2 * half, group_size, dtype);
+}
+
+awq::W4Args w4_args(int64_t n_tokens, int64_t in_features, int64_t rows, int group_size, int dtype,
+                    int act, const int32_t* qweight, const void* step16, const void* zero16) {
+  awq::W4Args a{};
+  a.N = n_tokens;
+  a.K = in_features;
+  a.O = rows;
+  a.group = group_size;
+  a.type = a.y_type = dtype;
+  a.act = act;
+  a.qweight = qweight;
+  a.step16 = step16;
+  a.zero16 = zero16;
+  return a;
+}
+
+int check_layer(const int32_t* qweight, const void* step16, const void* zero16) {
+  int rc;
+  if ((rc = check_ptr(qweight, "qweight")) || (rc = check_ptr(step16, "step16"))) return rc;
+  return check_ptr(zero16, "zero16");
+}
+
+// Bytes of the activation arguments, in the order of W4Args.
+struct W4Bytes {
+  int64_t in0, in1, out0, out1;
+};
+
+int run_w4(awq::W4Op op, awq::W4Args& a, const W4Bytes& b, void* workspace, size_t workspace_bytes,
+           void* stream, const char* what) {
+  const size_t need = awq::w4_workspace(op, a);
+  if (need) {
+    int rc;
+    if ((rc = check_ptr(workspace, "workspace"))) return rc;
+    if (workspace_bytes < need)
+      return fail(AWQ_ERR_WORKSPACE, "workspace %zu bytes < %zu required", workspace_bytes, need);
+  }
+  a.ws = workspace;
+  // what is written (the first three) shares no byte with anything else
+  const int64_t groups = 2 * a.O * (a.K / a.group);
+  const struct {
+    const void* p;
+    int64_t n;
+  } r[8] = {{a.out0, b.out0},    {a.out1, b.out1},        {a.ws, (int64_t)need},
+            {a.in0, b.in0},      {a.in1, b.in1},          {a.qweight, a.O * a.K / 2},
+            {a.step16, groups},  {a.zero16, groups}};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 8; ++j) {
+      const uintptr_t x = (uintptr_t)r[i].p, y = (uintptr_t)r[j].p;
+      if (x && y && r[i].n && r[j].n && x < y + r[j].n && y < x + r[i].n)
+        return fail(AWQ_ERR_INVALID_ARG, "an output or the workspace overlaps another argument");
+    }
+  return hip_result(awq::launch_w4(op, a, (hipStream_t)stream), what);
+}
+
 }  // namespace
 
 extern "C" {
@@ -239,6 +319,150 @@ int awq_w4a16_matmul(const void* X, int64_t n_tokens, int64_t in_features, int64
   return hip_result(awq::launch_w4a16(X, n_tokens, in_features, out_features, qweight, step16,
                                       zero16, Y, (hipStream_t)stream),
                     "awq_w4a16_matmul launch");
+}
+
+size_t awq_w4a16_linear_workspace_size(int64_t n_tokens, int64_t in_features, int64_t out_features,
+                                       int group_size, int dtype) {
+  if (check_w4(n_tokens, in_features, out_features, group_size, dtype)) return (size_t)-1;
+  ok();
+  return awq::w4_workspace(awq::kOpLinear, w4_args(n_tokens, in_features, out_features, group_size,
+                                                   dtype, 0, nullptr, nullptr, nullptr));
+}
+
+int awq_w4a16_linear(const void* X, int dtype, int64_t n_tokens, int64_t in_features,
+                     int64_t out_features, int group_size, const int32_t* qweight,
+                     const void* step16, const void* zero16, void* Y, int y_dtype, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  int rc;
+  if ((rc = check_w4(n_tokens, in_features, out_features, group_size, dtype))) return rc;
+  if (y_dtype != dtype && y_dtype != AWQ_F32)
+    return fail(AWQ_ERR_UNSUPPORTED, "y_dtype=%d: dtype (%d) or AWQ_F32", y_dtype, dtype);
+  if ((rc = check_ptr(X, "X")) || (rc = check_layer(qweight, step16, zero16)) ||
+      (rc = check_ptr(Y, "Y")))
+    return rc;
+  awq::W4Args a = w4_args(n_tokens, in_features, out_features, group_size, dtype, 0, qweight,
+                          step16, zero16);
+  a.y_type = y_dtype;
+  a.in0 = X;
+  a.out0 = Y;
+  const W4Bytes b{2 * a.N * a.K, 0, (y_dtype == AWQ_F32 ? 4 : 2) * a.N * a.O, 0};
+  return run_w4(awq::kOpLinear, a, b, workspace, workspace_bytes, stream, "awq_w4a16_linear launch");
+}
+
+size_t awq_w4a16_gated_workspace_size(int64_t n_tokens, int64_t in_features, int64_t half_features,
+                                      int group_size, int dtype) {
+  if (check_w4_gated(n_tokens, in_features, half_features, group_size, dtype, 0)) return (size_t)-1;
+  ok();
+  return awq::w4_workspace(awq::kOpGated, w4_args(n_tokens, in_features, 2 * half_features,
+                                                  group_size, dtype, 0, nullptr, nullptr, nullptr));
+}
+
+int awq_w4a16_gated(const void* X, int dtype, int64_t n_tokens, int64_t in_features,
+                    int64_t half_features, int group_size, int act, const int32_t* qweight,
+                    const void* step16, const void* zero16, void* H, void* pre, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  int rc;
+  if ((rc = check_w4_gated(n_tokens, in_features, half_features, group_size, dtype, act))) return rc;
+  if ((rc = check_ptr(X, "X")) || (rc = check_layer(qweight, step16, zero16)) ||
+      (rc = check_ptr(H, "H")) || (pre && (rc = check_ptr(pre, "pre"))))
+    return rc;
+  awq::W4Args a = w4_args(n_tokens, in_features, 2 * half_features, group_size, dtype, act, qweight,
+                          step16, zero16);
+  a.in0 = X;
+  a.out0 = H;
+  a.out1 = pre;
+  const W4Bytes b{2 * a.N * a.K, 0, a.N * a.O, 2 * a.N * a.O};
+  return run_w4(awq::kOpGated, a, b, workspace, workspace_bytes, stream, "awq_w4a16_gated launch");
+}
+
+size_t awq_w4a16_input_grad_workspace_size(int64_t n_tokens, int64_t in_features,
+                                           int64_t out_features, int group_size, int dtype) {
+  if (check_w4(n_tokens, in_features, out_features, group_size, dtype)) return (size_t)-1;
+  ok();
+  return awq::w4_workspace(awq::kOpInputGrad, w4_args(n_tokens, in_features, out_features,
+                                                      group_size, dtype, 0, nullptr, nullptr,
+                                                      nullptr));
+}
+
+int awq_w4a16_input_grad(const void* dY, int dtype, int64_t n_tokens, int64_t in_features,
+                         int64_t out_features, int group_size, const int32_t* qweight,
+                         const void* step16, const void* zero16, void* dX, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  int rc;
+  if ((rc = check_w4(n_tokens, in_features, out_features, group_size, dtype))) return rc;
+  if ((rc = check_ptr(dY, "dY")) || (rc = check_layer(qweight, step16, zero16)) ||
+      (rc = check_ptr(dX, "dX")))
+    return rc;
+  awq::W4Args a = w4_args(n_tokens, in_features, out_features, group_size, dtype, 0, qweight,
+                          step16, zero16);
+  a.in0 = dY;
+  a.out0 = dX;
+  const W4Bytes b{2 * a.N * a.O, 0, 2 * a.N * a.K, 0};
+  return run_w4(awq::kOpInputGrad, a, b, workspace, workspace_bytes, stream,
+                "awq_w4a16_input_grad launch");
+}
+
+size_t awq_w4a16_gated_backward_workspace_size(int64_t n_tokens, int64_t in_features,
+                                               int64_t half_features, int group_size, int dtype) {
+  if (check_w4_gated(n_tokens, in_features, half_features, group_size, dtype, 0)) return (size_t)-1;
+  ok();
+  return awq::w4_workspace(awq::kOpGatedBackward,
+                           w4_args(n_tokens, in_features, 2 * half_features, group_size, dtype, 0,
+                                   nullptr, nullptr, nullptr));
+}
+
+int awq_w4a16_gated_backward(const void* dH, const void* pre, int dtype, int64_t n_tokens,
+                             int64_t in_features, int64_t half_features, int group_size, int act,
+                             const int32_t* qweight, const void* step16, const void* zero16,
+                             void* dpre, void* dX, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  int rc;
+  if ((rc = check_w4_gated(n_tokens, in_features, half_features, group_size, dtype, act))) return rc;
+  if ((rc = check_ptr(dH, "dH")) || (rc = check_ptr(pre, "pre")) ||
+      (rc = check_layer(qweight, step16, zero16)) || (rc = check_ptr(dpre, "dpre")) ||
+      (rc = check_ptr(dX, "dX")))
+    return rc;
+  awq::W4Args a = w4_args(n_tokens, in_features, 2 * half_features, group_size, dtype, act, qweight,
+                          step16, zero16);
+  a.in0 = dH;
+  a.in1 = pre;
+  a.out0 = dX;
+  a.out1 = dpre;
+  const W4Bytes b{a.N * a.O, 2 * a.N * a.O, 2 * a.N * a.K, 2 * a.N * a.O};
+  return run_w4(awq::kOpGatedBackward, a, b, workspace, workspace_bytes, stream,
+                "awq_w4a16_gated_backward launch");
+}
+
+size_t awq_w4a16_param_grad_workspace_size(int64_t n_tokens, int64_t in_features,
+                                           int64_t out_features, int group_size, int dtype) {
+  if (check_w4(n_tokens, in_features, out_features, group_size, dtype)) return (size_t)-1;
+  ok();
+  return awq::w4_workspace(awq::kOpParamGrad, w4_args(n_tokens, in_features, out_features,
+                                                      group_size, dtype, 0, nullptr, nullptr,
+                                                      nullptr));
+}
+
+int awq_w4a16_param_grad(const void* dY, const void* X, int dtype, int64_t n_tokens,
+                         int64_t in_features, int64_t out_features, int group_size,
+                         const int32_t* qweight, const void* step16, const void* zero16,
+                         float* dstep, float* dzero, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  int rc;
+  if ((rc = check_w4(n_tokens, in_features, out_features, group_size, dtype))) return rc;
+  if ((rc = check_ptr(dY, "dY")) || (rc = check_ptr(X, "X")) ||
+      (rc = check_layer(qweight, step16, zero16)) || (rc = check_ptr(dstep, "dstep")) ||
+      (rc = check_ptr(dzero, "dzero")))
+    return rc;
+  awq::W4Args a = w4_args(n_tokens, in_features, out_features, group_size, dtype, 0, qweight,
+                          step16, zero16);
+  a.in0 = dY;
+  a.in1 = X;
+  a.out0 = dstep;
+  a.out1 = dzero;
+  const int64_t params = 4 * a.O * (a.K / a.group);
+  const W4Bytes b{2 * a.N * a.O, 2 * a.N * a.K, params, params};
+  return run_w4(awq::kOpParamGrad, a, b, workspace, workspace_bytes, stream,
+                "awq_w4a16_param_grad launch");
 }
 
 int awq_fold_inverse_scale(const void* src, const float* s, int64_t rows, int64_t cols, void* dst,

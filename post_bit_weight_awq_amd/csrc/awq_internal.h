@@ -78,6 +78,25 @@ hipError_t launch_w4a16(const void* X, int64_t M, int64_t K, int64_t OUT, const 
 // largest token count of one W4A16 launch (16 tokens per block row of the grid)
 constexpr int64_t kMaxW4Tokens = (int64_t)65535 * 16;
 
+// Packed-weight operators (w4_linear.hip).  The layer is [O, K] with groups
+// of `group` columns; a gated block's O counts the gate's and the up rows.
+enum W4Op { kOpLinear, kOpGated, kOpInputGrad, kOpGatedBackward, kOpParamGrad };
+enum ElemType { kF16 = 0, kBF16 = 1, kF32 = 2 };
+struct W4Args {
+  int64_t N, K, O;
+  int group, type, y_type, act;
+  const void *qweight, *step16, *zero16;
+  const void *in0, *in1;  // linear, gated: X; input_grad: dY; gated_backward: dH, pre;
+                          // param_grad: dY, X
+  void *out0, *out1;      // linear: Y; gated: H, pre or NULL; input_grad: dX;
+                          // gated_backward: dX, dpre; param_grad: dstep, dzero
+  void* ws;
+};
+// largest token count of one call
+constexpr int64_t kMaxW4OpTokens = (int64_t)1 << 20;
+size_t w4_workspace(W4Op op, const W4Args& a);
+hipError_t launch_w4(W4Op op, const W4Args& a, hipStream_t stream);
+
 hipError_t launch_fold(const void* src, const float* s, int64_t rows, int64_t cols, void* dst,
                        hipStream_t stream);
 
