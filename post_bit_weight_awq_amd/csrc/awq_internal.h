@@ -95,6 +95,9 @@ struct W4Args {
 // largest token count of one call
 constexpr int64_t kMaxW4OpTokens = (int64_t)1 << 20;
 size_t w4_workspace(W4Op op, const W4Args& a);
+// linear and gated calls of few tokens (w4_skinny.hip)
+bool w4_skinny_fits(const W4Args& a);
+hipError_t launch_w4_skinny(W4Op op, const W4Args& a, hipStream_t stream);
 hipError_t launch_w4(W4Op op, const W4Args& a, hipStream_t stream);
 
 hipError_t launch_fold(const void* src, const float* s, int64_t rows, int64_t cols, void* dst,

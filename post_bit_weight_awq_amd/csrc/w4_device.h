@@ -1,5 +1,5 @@
 // Device-side helpers of the packed-weight operators (w4_linear.hip,
-// w4_grad.hip): element types, activation functions.
+// w4_grad.hip): element types, activation functions, codes as fp16.
 #pragma once
 
 #include "awq_device.h"
@@ -37,6 +37,72 @@ __device__ __forceinline__ float act_value(float g, float* slope) {
     *slope = t == 0.0f && fabsf(g) < INFINITY ? p : fmaf(g * dy, t, p);
   }
   return g * p;
+}
+
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// Differences are held in units of 2^-9 between the codes and the step, which
+// takes the factor back: a nibble in bits 0-3 of a half is the fp16 subnormal
+// q 2^-24 and in bits 4-7 q 2^-20, so one packed fma by (2^15, 2^11) gives
+// (q - z) 2^-9 with one rounding, for any fp16 zero.
+constexpr float kCodeScale = 512.0f;
+__device__ __forceinline__ uint32_t neg_zero_pair(_Float16 z) {
+  const _Float16 n = (_Float16)(-0.001953125f) * z;
+  const uint32_t b = __builtin_bit_cast(uint16_t, n);
+  return b | (b << 16);
+}
+
+// The eight codes of a word, in column order, as (q - z) 2^-9: ten operations.
+__device__ __forceinline__ uint4 dequant_word(uint32_t w, uint32_t nz) {
+  const uint32_t lo = w & 0x0F0F0F0Fu, hi = w & 0xF0F0F0F0u;
+  const half2v m = {(_Float16)32768.0f, (_Float16)2048.0f};
+  const half2v z = __builtin_bit_cast(half2v, nz);
+  auto pair = [&](uint32_t sel) {
+    const half2v c = __builtin_bit_cast(half2v, __builtin_amdgcn_perm(hi, lo, sel));
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(c, m, z));
+  };
+  return make_uint4(pair(0x0c040c00u), pair(0x0c050c01u), pair(0x0c060c02u), pair(0x0c070c03u));
+}
+
+// Words of four lane groups of 16: word j of group q becomes word q of group
+// j.  A group that loaded words 4q .. 4q+3 of a row's 16 (one 16-byte load)
+// then holds words q, 4 + q, 8 + q, 12 + q: word j of every group lies in the
+// j-th 32 of the 128 columns.
+__device__ __forceinline__ void transpose_words(uint4& w) {
+  const auto a = __builtin_amdgcn_permlane32_swap(w.x, w.z, false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(w.y, w.w, false, false);
+  const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+  const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+  w = make_uint4(c[0], c[1], d[0], d[1]);
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int j) {
+  return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
+}
+
+// Packed fp16 to packed bf16, rounded to nearest even, and what that
+// rounding leaves.
+__device__ __forceinline__ uint32_t half2_to_bf16x2(uint32_t v) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 r = {(__bf16)f16_lo(v), (__bf16)f16_hi(v)};
+  return __builtin_bit_cast(uint32_t, r);
+}
+__device__ __forceinline__ uint32_t half2_minus_bf16x2(uint32_t v, uint32_t b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 r = {(__bf16)(f16_lo(v) - __uint_as_float(b << 16)),
+                    (__bf16)(f16_hi(v) - __uint_as_float(b & 0xffff0000u))};
+  return __builtin_bit_cast(uint32_t, r);
+}
+
+template <typename T>
+__device__ __forceinline__ floatx4 mfma16(uint4 a, uint4 b, floatx4 c) {
+  if constexpr (sizeof(T) == 2 && __is_same(T, _Float16))
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a),
+                                                  __builtin_bit_cast(half8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
 }  // namespace awq

@@ -198,6 +198,8 @@ static hipError_t w4_launch(W4Op op, const W4Args& a, hipStream_t stream) {
 }
 
 hipError_t launch_w4(W4Op op, const W4Args& a, hipStream_t stream) {
+  if ((op == kOpLinear || op == kOpGated) && w4_skinny_fits(a))
+    return launch_w4_skinny(op, a, stream);
   return a.type == kF16 ? w4_launch<_Float16>(op, a, stream) : w4_launch<__bf16>(op, a, stream);
 }
 
