@@ -9,6 +9,7 @@
 // lays the sums out in LDS and applies the operator's epilogue.
 #include "awq_internal.h"
 #include "w4_device.h"
+#include "w4_internal.h"
 
 namespace awq {
 
@@ -148,7 +149,10 @@ static W4Layer layer_of(const W4Args& a) {
                  (int)a.K, (int)a.O, a.group};
 }
 
-size_t w4_workspace(W4Op, const W4Args&) { return 0; }
+size_t w4_workspace(W4Op op, const W4Args& a) {
+  if (op == kOpLinear || op == kOpGated) return w4_skinny_fits(a) ? 0 : w4_gemm_workspace(a);
+  return 0;
+}
 
 template <typename T>
 static hipError_t w4_launch(W4Op op, const W4Args& a, hipStream_t stream) {
@@ -200,6 +204,7 @@ static hipError_t w4_launch(W4Op op, const W4Args& a, hipStream_t stream) {
 hipError_t launch_w4(W4Op op, const W4Args& a, hipStream_t stream) {
   if ((op == kOpLinear || op == kOpGated) && w4_skinny_fits(a))
     return launch_w4_skinny(op, a, stream);
+  if (op == kOpLinear || op == kOpGated) return launch_w4_gemm(op, a, stream);
   return a.type == kF16 ? w4_launch<_Float16>(op, a, stream) : w4_launch<__bf16>(op, a, stream);
 }
 
