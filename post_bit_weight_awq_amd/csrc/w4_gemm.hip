@@ -49,11 +49,12 @@ k_w4_params(const uint16_t* __restrict__ step16, const uint16_t* __restrict__ ze
   }
 }
 
-// Rows of bf16 as fp16 times 2^e, e chosen by the row's largest finite
+// Rows padded to ld_out with zeros; fp16 rows as they are, back = 0.  Rows of
+// bf16 become fp16 times 2^e, e chosen by the row's largest finite
 // magnitude (which lands in [2^14, 2^15)); back[row] = 2^-e as an exponent.
 // Values down to 2^-32 of the largest stay exact, smaller ones are rounded at
-// 2^-40 of it.  COLS elements of a row are kept ld_out apart, zeros behind
-// them.
+// 2^-40 of it.
+template <bool BF16>
 __global__ void __launch_bounds__(256)
 k_rows_to_half(const uint16_t* __restrict__ in, int cols, int ld_out, _Float16* __restrict__ out,
                int* __restrict__ back) {
@@ -61,6 +62,16 @@ k_rows_to_half(const uint16_t* __restrict__ in, int cols, int ld_out, _Float16* 
   const size_t row = blockIdx.x;
   const uint16_t* src = in + row * cols;
   const bool vec = (cols & 7) == 0;
+  _Float16* dst = out + row * ld_out;
+  for (int c = cols + threadIdx.x; c < ld_out; c += 256) dst[c] = (_Float16)0.0f;
+  if constexpr (!BF16) {
+    if (vec)
+      for (int c = threadIdx.x * 8; c < cols; c += 2048) *(uint4*)(dst + c) = *(const uint4*)(src + c);
+    else
+      for (int c = threadIdx.x; c < cols; c += 256) dst[c] = __builtin_bit_cast(_Float16, src[c]);
+    if (threadIdx.x == 0) back[row] = 0;
+    return;
+  }
   uint32_t top = 0;  // largest finite magnitude, as bits
   auto look = [&](uint32_t b) {
     b &= 0x7fffu;
@@ -92,7 +103,6 @@ k_rows_to_half(const uint16_t* __restrict__ in, int cols, int ld_out, _Float16* 
   if (top) (void)frexpf(__uint_as_float(top << 16), &x);
   const int e = top ? 15 - x : 0;
   if (threadIdx.x == 0) back[row] = -e;
-  _Float16* dst = out + row * ld_out;
   auto half = [&](uint32_t b) -> uint32_t {
     return __builtin_bit_cast(uint16_t, (_Float16)ldexpf(__uint_as_float(b << 16), e));
   };
@@ -109,13 +119,16 @@ k_rows_to_half(const uint16_t* __restrict__ in, int cols, int ld_out, _Float16* 
     for (int c = threadIdx.x; c < cols; c += 256)
       dst[c] = __builtin_bit_cast(_Float16, (uint16_t)half(src[c]));
   }
-  for (int c = cols + threadIdx.x; c < ld_out; c += 256) dst[c] = (_Float16)0.0f;
 }
 
-hipError_t launch_rows_to_half(const void* in, int64_t rows, int64_t cols, int64_t ld_out, void* out,
+hipError_t launch_rows_to_half(const void* in, int type, int64_t rows, int64_t cols, int64_t ld_out, void* out,
                                int* back, hipStream_t stream) {
-  hipLaunchKernelGGL(k_rows_to_half, dim3((unsigned)rows), dim3(256), 0, stream,
-                     (const uint16_t*)in, (int)cols, (int)ld_out, (_Float16*)out, back);
+  if (type == kBF16)
+    hipLaunchKernelGGL(k_rows_to_half<true>, dim3((unsigned)rows), dim3(256), 0, stream,
+                       (const uint16_t*)in, (int)cols, (int)ld_out, (_Float16*)out, back);
+  else
+    hipLaunchKernelGGL(k_rows_to_half<false>, dim3((unsigned)rows), dim3(256), 0, stream,
+                       (const uint16_t*)in, (int)cols, (int)ld_out, (_Float16*)out, back);
   return hipGetLastError();
 }
 
@@ -136,7 +149,7 @@ k_w4_gemm(const _Float16* __restrict__ A, const int* __restrict__ back, int N, i
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 2, wn = wave & 3;
   const int r16 = lane & 15, q4 = lane >> 4;
-  const TileUnit un = tile_unit(blockIdx.x, nt, no);
+  const TileUnit un = tile_unit(blockIdx.x, nt, no, nt * no);
   const int F = O >> 1;
   const int t0 = un.t * BM, rb = un.o * (GATED ? kBN / 2 : kBN);
   const int outs = GATED ? F : O;
@@ -154,13 +167,7 @@ k_w4_gemm(const _Float16* __restrict__ A, const int* __restrict__ back, int N, i
     const _Float16* base = a0 + s * 128;
     const _Float16* d = smem + (s & 1) * STAGE + wave * MT * 512;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const uint32_t la = (uint32_t)(uintptr_t)(d + i * 512);
-      asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
-                   :
-                   : "v"(oa[i]), "s"(base), "s"(la)
-                   : "memory");
-    }
+    for (int i = 0; i < MT; ++i) dma16(base, oa[i], (uint32_t)(uintptr_t)(d + i * 512));
   };
   // row of tile n (16 rows each) for this lane, past the end the last one
   int prow[4];
@@ -330,8 +337,6 @@ k_w4_gemm(const _Float16* __restrict__ A, const int* __restrict__ back, int N, i
   }
 }
 
-static size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
-
 struct GemmPlan {
   size_t off_prm, off_a, off_back, bytes;
 };
@@ -402,7 +407,7 @@ hipError_t launch_w4_gemm(W4Op op, const W4Args& a, hipStream_t stream) {
                      dim3(256), 0, stream, (const uint16_t*)a.step16, (const uint16_t*)a.zero16,
                      (int)a.O, ng, (uint32_t*)(ws + p.off_prm));
   if (a.type == kBF16) {
-    const hipError_t e = launch_rows_to_half(a.in0, a.N, a.K, a.K, ws + p.off_a,
+    const hipError_t e = launch_rows_to_half(a.in0, a.type, a.N, a.K, a.K, ws + p.off_a,
                                              (int*)(ws + p.off_back), stream);
     if (e != hipSuccess) return e;
     return by_group<__bf16>(op, a, p, stream);

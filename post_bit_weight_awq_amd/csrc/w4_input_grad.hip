@@ -1,0 +1,329 @@
+// dX = dY W on packed weights: W[o, k] = (q[o, k] - z[o, g]) step[o, g], the
+// sum running over the packed rows o.
+//
+// Block tile 32 MT tokens x 256 columns, eight wavefronts as 2 (tokens) x 4
+// (columns), each 16 MT x 64 as MT x 4 tiles of v_mfma_f32_16x16x32_f16, 64
+// packed rows a step.  dY, the codes and the group parameters move to LDS by
+// direct loads, three stages, two steps ahead.
+//   * An MFMA needs eight consecutive rows of one column per lane, while a
+//     word holds eight columns of one row.  So lane l reads the word l % 16 of
+//     each of its eight rows (8 (l / 16) ..), pairs the rows' halves with one
+//     byte permute, and each nibble position of the pair is the fragment of
+//     another column tile: tile c of a wavefront is the columns 8 j + 4 h + c,
+//     j = 0..15, h the wavefront's half of the words.  No transpose, and a
+//     lane's four tiles are four neighbouring columns of dX.
+//   * The step changes along the sum, so it has to enter the operand: weights
+//     are formed as fp16((q - z) step), one rounding, 14 operations per eight.
+//   * The LDS rows of the codes are ordered (row % 8, row / 8) and every
+//     second pair swaps its 64-byte halves: the 64 words of a read then lie
+//     in 64 banks.
+//   * dY in bf16, or of a width that is no multiple of 64, is copied to fp16
+//     rows of a padded width first (k_rows_to_half; zeros behind the row's
+//     end meet weights of 0).
+#include "w4_internal.h"
+
+namespace awq {
+
+// Group parameters by steps of 64 packed rows: prm[(s * ng + g) * 64 + ..] as
+// 64 halfs -zero 2^-9 and 64 halfs of the step; 0 for rows past the end.
+__global__ void __launch_bounds__(256)
+k_dx_params(const _Float16* __restrict__ step16, const _Float16* __restrict__ zero16, int O, int ng,
+            _Float16* __restrict__ prm) {
+  __shared__ uint32_t tile[64][33];
+  const int o0 = blockIdx.x * 64, g0 = blockIdx.y * 32;
+  for (int e = threadIdx.x; e < 64 * 32; e += 256) {
+    const int r = e >> 5, c = e & 31;
+    uint32_t v = 0;
+    if (o0 + r < O && g0 + c < ng) {
+      const size_t at = (size_t)(o0 + r) * ng + g0 + c;
+      v = (neg_zero_pair(zero16[at]) & 0xffffu) |
+          ((uint32_t)__builtin_bit_cast(uint16_t, step16[at]) << 16);
+    }
+    tile[r][c] = v;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < 64 * 32; e += 256) {
+    const int c = e >> 6, r = e & 63;
+    if (g0 + c >= ng) continue;
+    _Float16* p = prm + ((size_t)blockIdx.x * ng + g0 + c) * 128;
+    p[r] = __builtin_bit_cast(_Float16, (uint16_t)(tile[r][c] & 0xffffu));
+    p[64 + r] = __builtin_bit_cast(_Float16, (uint16_t)(tile[r][c] >> 16));
+  }
+}
+
+constexpr int kStages = 3;
+template <int MT>
+struct DxLds {
+  static constexpr int kA = 32 * MT * 128;  // bytes of dY per stage
+  static constexpr int kC = 64 * 128;       // codes
+  static constexpr int kP = 2048;           // group parameters
+  static constexpr int kStage = kA + kC + kP;
+};
+
+// Values of one token's four neighbouring columns per lane, tile by tile.
+template <typename T, int MT>
+__device__ __forceinline__ void store_dx(const floatx4 (&acc)[MT][4], const int* back, int N, int K,
+                                         int t0, int col, int lane, T* dX) {
+  if (col >= K) return;
+  typedef T Tx4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = t0 + 16 * m + 4 * (lane >> 4) + r;
+      if (t >= N) continue;
+      const int x = back ? back[t] : 0;
+      Tx4 v;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] = from_f32<T>(back ? ldexpf(acc[m][c][r], x) : acc[m][c][r]);
+      *(Tx4*)(dX + (size_t)t * K + col) = v;
+    }
+}
+
+template <typename T, int GROUP, int MT>
+__global__ void __launch_bounds__(512, 2)
+k_w4_dx(const _Float16* __restrict__ A, int lda, const int* __restrict__ back, int N, int K, int O,
+        const char* __restrict__ qw, const char* __restrict__ prm, T* __restrict__ dX,
+        float* __restrict__ parts, TileSplit sp) {
+  using L = DxLds<MT>;
+  constexpr int BM = 32 * MT;
+  constexpr int AL = MT / 2;           // direct loads of dY per wavefront and step
+  constexpr int PB = 8192 / GROUP;     // parameter bytes per wavefront and step
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 2, wn = wave & 3, wb = wn >> 1, half = wn & 1;
+  const int r16 = lane & 15, q4 = lane >> 4;
+  const SplitUnit un = split_unit(blockIdx.x, sp);
+  const int t0 = un.t * BM, k0 = un.o * 256;
+  const int ng = K / GROUP;
+
+  // dY: load i brings 8 rows of 128 bytes; 16-byte piece p of row r at p ^ (r % 8)
+  uint32_t oa[AL];
+#pragma unroll
+  for (int i = 0; i < AL; ++i) {
+    const int r = 8 * (wave * AL + i) + (lane >> 3);
+    oa[i] = 2u * ((uint32_t)(min(t0 + r, N - 1) - t0) * (uint32_t)lda + 8 * ((lane & 7) ^ (r & 7)));
+  }
+  const char* a0 = (const char*)(A + (size_t)t0 * lda);
+  // codes: one load of 8 LDS rows of 128 bytes; LDS row 32 c + 4 i + q is
+  // packed row 32 c + 8 q + i of the step
+  const int lr = 8 * wave + (lane >> 3);
+  const int crow = 32 * (lr >> 5) + 8 * (lr & 3) + ((lr & 31) >> 2);
+  int piece = (lane & 7) ^ (((lr >> 1) & 1) << 2);
+  if (k0 + 32 * piece >= K) piece -= 4;  // a last tile of 128 columns
+  const uint32_t oc = (uint32_t)(k0 / 2 + 16 * piece);
+  // parameters: PB bytes of the block's groups per wavefront
+  const int pbyte = wave * PB + 4 * lane;
+  const int pg = min(k0 / GROUP + pbyte / 256, ng - 1);
+  const uint32_t op = (uint32_t)pg * 256u + (pbyte & 255);
+
+  auto load = [&](int s) {
+    const uint32_t l = (uint32_t)(uintptr_t)smem + (uint32_t)(s % kStages) * L::kStage;
+#pragma unroll
+    for (int i = 0; i < AL; ++i)
+      dma16(a0 + s * 128, oa[i], l + (wave * AL + i) * 1024);
+    // each lane's row, the last one where the step passes the end
+    const int row = min(64 * s + crow, O - 1);
+    dma16(qw + (size_t)(64 * s) * (K / 2), (uint32_t)(row - 64 * s) * (uint32_t)(K / 2) + oc,
+          l + L::kA + wave * 1024);
+    if (lane < PB / 4) dma4(prm + (size_t)s * ng * 256, op, l + L::kA + L::kC + wave * PB);
+  };
+
+  floatx4 acc[MT][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[m][c] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+  const int cbase = q4 * 128 + ((wb ^ (q4 >> 1)) * 64) + 4 * r16;
+  const int gl = (128 * wb + 8 * r16) / GROUP;  // the lane's group among the block's
+  const uint32_t sel = half ? 0x07060302u : 0x05040100u;
+
+  load(un.s0);
+  if (un.s0 + 1 < un.s1) load(un.s0 + 1);
+  for (int s = un.s0; s < un.s1; ++s) {
+    // the step's loads have landed (the next step's may be in flight), and no
+    // wavefront still reads the stage that is loaded next
+    if (s + 1 < un.s1)
+      wait_vm<AL + 2>();
+    else
+      wait_vm<0>();
+    __syncthreads();
+    if (s + 2 < un.s1) load(s + 2);
+    const char* st = smem + (s % kStages) * L::kStage;
+    const char* pc = st + L::kA + cbase;
+    const char* pp = st + L::kA + L::kC + gl * 256 + 16 * q4;
+#pragma unroll
+    for (int ch = 0; ch < 2; ++ch) {
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = *(const uint32_t*)(pc + ch * 4096 + i * 512);
+      const uint4 zv = *(const uint4*)(pp + ch * 64);
+      const uint4 sv = *(const uint4*)(pp + ch * 64 + 128);
+      uint4 b[4];
+      uint32_t bw[4][4];
+      uint32_t over = 0;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const uint32_t t = __builtin_amdgcn_perm(w[2 * p + 1], w[2 * p], sel);
+        const uint32_t t8 = t >> 8;
+        const half2v z = __builtin_bit_cast(half2v, word_of(zv, p));
+        const half2v s1 = __builtin_bit_cast(half2v, word_of(sv, p));
+        const half2v m0 = {(_Float16)32768.0f, (_Float16)32768.0f};
+        const half2v m1 = {(_Float16)2048.0f, (_Float16)2048.0f};
+        const half2v k512 = {(_Float16)512.0f, (_Float16)512.0f};
+        const half2v zeros = {(_Float16)0.0f, (_Float16)0.0f};
+        const half2v s5 = s1 * k512;
+        // 0 where 512 step stays finite
+        over |= __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(s5, zeros, zeros));
+        const uint32_t n[4] = {t & 0x000F000Fu, t & 0x00F000F0u, t8 & 0x000F000Fu,
+                               t8 & 0x00F000F0u};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const half2v d = __builtin_elementwise_fma(__builtin_bit_cast(half2v, n[c]),
+                                                     c & 1 ? m1 : m0, z);
+          bw[c][p] = __builtin_bit_cast(uint32_t, d * s5);
+        }
+      }
+      if (__any(over != 0)) {
+        // steps of 128 and more: the factor 512 goes to the differences
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const uint32_t t = __builtin_amdgcn_perm(w[2 * p + 1], w[2 * p], sel);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t n = (t >> (4 * c)) & 0x000F000Fu;
+            const half2v m0 = {(_Float16)32768.0f, (_Float16)32768.0f};
+            const half2v k512 = {(_Float16)512.0f, (_Float16)512.0f};
+            const half2v d = __builtin_elementwise_fma(__builtin_bit_cast(half2v, n), m0,
+                                                       __builtin_bit_cast(half2v, word_of(zv, p)));
+            bw[c][p] = __builtin_bit_cast(
+                uint32_t, (d * k512) * __builtin_bit_cast(half2v, word_of(sv, p)));
+          }
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) b[c] = make_uint4(bw[c][0], bw[c][1], bw[c][2], bw[c][3]);
+      const char* ta = st + (wm * MT * 16 + r16) * 128 + 16 * ((4 * ch + q4) ^ (r16 & 7));
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const uint4 a = *(const uint4*)(ta + m * 2048);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[m][c] = mfma16<_Float16>(a, b[c], acc[m][c]);
+      }
+    }
+  }
+  if (un.parts > 1) {
+    floatx4* p = (floatx4*)parts + ((size_t)un.slot * 8 + wave) * (MT * 4 * 64) + lane;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) p[(m * 4 + c) * 64] = acc[m][c];
+    return;
+  }
+  store_dx<T, MT>(acc, back, N, K, t0 + wm * MT * 16, k0 + 128 * wb + 8 * r16 + 4 * half, lane, dX);
+}
+
+// Sums of a split tile's parts, in order, one wavefront's share per block.
+template <typename T, int MT>
+__global__ void __launch_bounds__(64)
+k_dx_join(const float* __restrict__ parts, const int* __restrict__ back, int N, int K,
+          T* __restrict__ dX, TileSplit sp) {
+  const int lane = threadIdx.x, wave = blockIdx.x & 7, left = blockIdx.x >> 3;
+  const TileUnit un = tile_unit(sp.full + left, sp.nt, sp.no, sp.full + sp.left);
+  const floatx4* p = (const floatx4*)parts + ((size_t)left * sp.parts * 8 + wave) * (MT * 4 * 64) + lane;
+  floatx4 acc[MT][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[m][c] = p[(m * 4 + c) * 64];
+  for (int i = 1; i < sp.parts; ++i) {
+    const floatx4* q = p + (size_t)i * 8 * (MT * 4 * 64);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[m][c] += q[(m * 4 + c) * 64];
+  }
+  const int wm = wave >> 2, wn = wave & 3;
+  store_dx<T, MT>(acc, back, N, K, un.t * 32 * MT + wm * MT * 16,
+                  un.o * 256 + 128 * (wn >> 1) + 8 * (lane & 15) + 4 * (wn & 1), lane, dX);
+}
+
+struct DxPlan {
+  int mt, steps, lda;
+  bool copy;
+  TileSplit sp;
+  size_t off_prm, off_a, off_back, off_parts, bytes;
+};
+static DxPlan dx_plan(const W4Args& a) {
+  DxPlan p;
+  p.steps = (int)((a.O + 63) / 64);
+  p.copy = a.type == kBF16 || a.O % 64;
+  p.lda = p.copy ? p.steps * 64 : (int)a.O;
+  p.mt = a.N <= 64 ? 2 : a.N <= 128 ? 4 : 8;
+  const int bm = 32 * p.mt;
+  p.sp = tile_split((int)((a.N + bm - 1) / bm), (int)((a.K + 255) / 256), p.steps, 4);
+  size_t at = 0;
+  p.off_prm = at;
+  at += align256((size_t)p.steps * 64 * (a.K / a.group) * 4);
+  p.off_a = at;
+  if (p.copy) at += align256((size_t)a.N * p.lda * 2);
+  p.off_back = at;
+  if (p.copy) at += align256((size_t)a.N * 4);
+  p.off_parts = at;
+  if (p.sp.parts > 1) at += (size_t)p.sp.left * p.sp.parts * bm * 256 * 4;
+  p.bytes = at;
+  return p;
+}
+size_t w4_input_grad_workspace(const W4Args& a) { return dx_plan(a).bytes; }
+
+template <typename T, int GROUP, int MT>
+static hipError_t launch(const W4Args& a, const void* dY, const DxPlan& p, hipStream_t stream) {
+  auto* kernel = &k_w4_dx<T, GROUP, MT>;
+  const int lds = kStages * DxLds<MT>::kStage;
+  hipError_t e =
+      hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (e != hipSuccess) return e;
+  char* ws = (char*)a.ws;
+  const int* back = a.type == kBF16 ? (const int*)(ws + p.off_back) : nullptr;
+  float* parts = (float*)(ws + p.off_parts);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(p.sp.full + p.sp.left * p.sp.parts)), dim3(512), lds,
+                     stream, p.copy ? (const _Float16*)(ws + p.off_a) : (const _Float16*)dY, p.lda,
+                     back, (int)a.N, (int)a.K, (int)a.O, (const char*)a.qweight, ws + p.off_prm,
+                     (T*)a.out0, parts, p.sp);
+  if (p.sp.parts > 1)
+    hipLaunchKernelGGL((k_dx_join<T, MT>), dim3((unsigned)(p.sp.left * 8)), dim3(64), 0, stream,
+                       parts, back, (int)a.N, (int)a.K, (T*)a.out0, p.sp);
+  return hipGetLastError();
+}
+
+template <typename T, int GROUP>
+static hipError_t by_tokens(const W4Args& a, const void* dY, const DxPlan& p, hipStream_t stream) {
+  if (p.mt == 2) return launch<T, GROUP, 2>(a, dY, p, stream);
+  if (p.mt == 4) return launch<T, GROUP, 4>(a, dY, p, stream);
+  return launch<T, GROUP, 8>(a, dY, p, stream);
+}
+
+template <typename T>
+static hipError_t by_group(const W4Args& a, const void* dY, const DxPlan& p, hipStream_t stream) {
+  if (a.group == 128) return by_tokens<T, 128>(a, dY, p, stream);
+  if (a.group == 64) return by_tokens<T, 64>(a, dY, p, stream);
+  return by_tokens<T, 32>(a, dY, p, stream);
+}
+
+hipError_t launch_w4_input_grad(const W4Args& a, const void* dY, hipStream_t stream) {
+  const DxPlan p = dx_plan(a);
+  char* ws = (char*)a.ws;
+  const int ng = (int)(a.K / a.group);
+  hipLaunchKernelGGL(k_dx_params, dim3((unsigned)p.steps, (unsigned)((ng + 31) / 32)), dim3(256), 0,
+                     stream, (const _Float16*)a.step16, (const _Float16*)a.zero16, (int)a.O, ng,
+                     (_Float16*)(ws + p.off_prm));
+  if (p.copy) {
+    const hipError_t e = launch_rows_to_half(dY, a.type, a.N, a.O, p.lda, ws + p.off_a,
+                                             (int*)(ws + p.off_back), stream);
+    if (e != hipSuccess) return e;
+  }
+  return a.type == kF16 ? by_group<_Float16>(a, dY, p, stream) : by_group<__bf16>(a, dY, p, stream);
+}
+
+}  // namespace awq

@@ -14,8 +14,8 @@ namespace awq {
 struct TileUnit {
   int t, o;
 };
-__device__ __forceinline__ TileUnit tile_unit(int b, int nt, int no) {
-  const int total = nt * no, x = b & 7, i = b >> 3;
+__device__ __forceinline__ TileUnit tile_unit(int b, int nt, int no, int total) {
+  const int x = b & 7, i = b >> 3;
   // XCD x has total / 8 tiles, one more for the first total % 8
   const int per = total >> 3, rest = total & 7;
   const int u = x * per + min(x, rest) + i;
@@ -26,6 +26,67 @@ __device__ __forceinline__ TileUnit tile_unit(int b, int nt, int no) {
   r.o = 4 * strip + in - r.t * wide;
   return r;
 }
+
+// A launch runs its tiles in rounds of one per compute unit.  The tiles of a
+// last, partial round are split along the sum into parts that fill the chip;
+// the parts' sums go to the workspace in fp32 and a second launch adds them in
+// order.  `full` tiles run whole, `left` in `parts` parts.
+struct TileSplit {
+  int nt, no, steps, full, left, parts;
+};
+constexpr int kCUs = 256;
+// A part takes `least` steps or more.
+inline TileSplit tile_split(int nt, int no, int steps, int least) {
+  TileSplit s{nt, no, steps, nt * no, 0, 1};
+  const int left = s.full % kCUs;
+  if (left == 0) return s;
+  int parts = kCUs / left;
+  if (parts > steps / least) parts = steps / least;
+  if (parts < 2) return s;
+  s.left = left;
+  s.full -= left;
+  s.parts = parts;
+  return s;
+}
+struct SplitUnit {
+  int t, o, s0, s1, parts, slot;
+};
+__device__ __forceinline__ SplitUnit split_unit(int b, const TileSplit& s) {
+  SplitUnit r;
+  const int i = b - s.full;
+  const bool whole = i < 0;
+  const int tile = whole ? b : s.full + i / s.parts, part = whole ? 0 : i % s.parts;
+  const TileUnit u = tile_unit(tile, s.nt, s.no, s.full + s.left);
+  r.t = u.t;
+  r.o = u.o;
+  r.parts = whole ? 1 : s.parts;
+  r.s0 = (int)((int64_t)s.steps * part / r.parts);
+  r.s1 = (int)((int64_t)s.steps * (part + 1) / r.parts);
+  r.slot = i;
+  return r;
+}
+
+// Direct loads to LDS: 16 (or 4) bytes per lane from base + off to l + 16 (4)
+// times the lane.
+__device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t l) {
+  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
+               :
+               : "v"(off), "s"(base), "s"(l)
+               : "memory");
+}
+__device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t l) {
+  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1"
+               :
+               : "v"(off), "s"(base), "s"(l)
+               : "memory");
+}
+// All but the wavefront's last N vector memory operations have ended.
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | ((N >> 4) << 14));
+}
+
+inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // Up to eight values of one row, rounded once: `n` are left in the row; whole
 // 16-byte stores where rows begin on such a boundary.
@@ -50,9 +111,12 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8], int n, bool al
   }
 }
 
-hipError_t launch_rows_to_half(const void* in, int64_t rows, int64_t cols, int64_t ld_out, void* out,
+hipError_t launch_rows_to_half(const void* in, int type, int64_t rows, int64_t cols, int64_t ld_out, void* out,
                                int* back, hipStream_t stream);
 size_t w4_gemm_workspace(const W4Args& a);
+size_t w4_input_grad_workspace(const W4Args& a);
+// dX of a.out0 from dY
+hipError_t launch_w4_input_grad(const W4Args& a, const void* dY, hipStream_t stream);
 hipError_t launch_w4_gemm(W4Op op, const W4Args& a, hipStream_t stream);
 
 }  // namespace awq

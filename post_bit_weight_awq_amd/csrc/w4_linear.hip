@@ -151,6 +151,7 @@ static W4Layer layer_of(const W4Args& a) {
 
 size_t w4_workspace(W4Op op, const W4Args& a) {
   if (op == kOpLinear || op == kOpGated) return w4_skinny_fits(a) ? 0 : w4_gemm_workspace(a);
+  if (op == kOpInputGrad || op == kOpGatedBackward) return w4_input_grad_workspace(a);
   return 0;
 }
 
@@ -176,9 +177,7 @@ static hipError_t w4_launch(W4Op op, const W4Args& a, hipStream_t stream) {
                                               nullptr, nullptr, stream);
       break;
     case kOpInputGrad:
-      launch_tile<T, kW4InputGrad, 0, T>(a.in0, nullptr, w, a.N, a.N, a.K, a.out0, nullptr, nullptr,
-                                         nullptr, stream);
-      break;
+      return launch_w4_input_grad(a, a.in0, stream);
     case kOpGatedBackward: {
       const int64_t n = a.N * F;
       const int64_t want = (n + 255) / 256;
@@ -189,9 +188,7 @@ static hipError_t w4_launch(W4Op op, const W4Args& a, hipStream_t stream) {
       else
         hipLaunchKernelGGL((k_gated_grad<T, kActGelu>), grid, dim3(256), 0, stream,
                            (const T*)a.in0, (const T*)a.in1, n, (int)F, (T*)a.out1);
-      launch_tile<T, kW4InputGrad, 0, T>(a.out1, nullptr, w, a.N, a.N, a.K, a.out0, nullptr,
-                                         nullptr, nullptr, stream);
-      break;
+      return launch_w4_input_grad(a, a.out1, stream);
     }
     case kOpParamGrad:
       launch_tile<T, kW4ParamGrad, 0, T>(a.in0, a.in1, w, a.N, a.O, a.K, nullptr, nullptr,

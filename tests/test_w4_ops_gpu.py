@@ -385,3 +385,37 @@ def test_binding_refusals_on_device(awq):
     with pytest.raises(awq.AwqError, match="aligned"):
         off = torch.zeros(2 * 256 + 1, dtype=F16, device="cuda")[1:].view(2, 256)
         awq.awq_w4a16_linear(off, q, s, z)
+
+
+@pytest.mark.parametrize("n", [1, 40, 130, 520])
+@by_type
+def test_steps_of_any_size(awq, n, t, group):
+    """Steps of 0, subnormal, negative and 128 to 300 beside ordinary ones; a
+    row whose first, last or only groups have none."""
+    _say(f"steps {n} {t} g{group}")
+    k, o = 512, 72
+    q, s, z = P.make_layer(o, k, group, 21, "cuda")
+    s[0] = 0
+    s[1, 0] = 0
+    s[2, -1] = 0
+    s[3, ::2] = 0
+    s[4] = 2.0 ** -24
+    s[5, 0] = 2.0 ** -24
+    s[6] = -s[6]
+    s[7, -1] = 300.0
+    s[8] = 128.0
+    s[9, 0], s[9, 1] = 2.0 ** -24, 200.0
+    layer = (q, s, z)
+    x = rnd(n, k, t, 22, 0.25)
+    check_linear(awq, x, layer, F32, "Y")
+    w = P.weights(*layer)
+    y, e = P.linear(x, w)
+    assert bool((awq.awq_w4a16_linear(x, *layer, out_dtype=F32)[:, 0] == 0).all())
+    dy = rnd(n, o, t, 23, 0.01)
+    got = awq.awq_w4a16_input_grad(dy, *layer)
+    want, e = P.input_grad(dy, w, t)
+    close(got, want, P.rounded(want, e, t), "dX")
+    ds, dz = awq.awq_w4a16_param_grad(dy, x, *layer)
+    ws_, es, wz, ez = P.param_grad(dy, x, *layer)
+    close(ds, ws_, P.rounded(ws_, es, F32), "dstep")
+    close(dz, wz, P.rounded(wz, ez.abs(), F32), "dzero")
