@@ -268,10 +268,11 @@ int awq_w4a16_matmul(const void* X, int64_t n_tokens, int64_t in_features, int64
  *               projection's (a fused layer, as awq_search_layer takes it)
  *   group_size: 32, 64 or 128
  *   qweight:    [rows, in_features / 8] int32, nibble j of word w = column 8w + j
- *   step16, zero16: [rows, in_features / group_size] fp16; zero may be any
- *               finite fp16 value (awq_pack writes integers).  q - zero is
- *               rounded once to fp16, which is exact for integer zeros of
- *               magnitude up to 2032
+ *   step16, zero16: [rows, in_features / group_size] fp16, finite; zero may
+ *               have any value (awq_pack writes integers).  q - zero is held in
+ *               fp16 in units of 2^-9: exact for integer zeros of magnitude up
+ *               to 2032, else rounded once to 11 bits or, below 2^-5, to a
+ *               multiple of 2^-15 (a zero below 2^-5 is rounded so first)
  *   workspace:  scratch of at least the matching *_workspace_size bytes; its
  *               contents on entry do not matter.  A size of 0 means that none
  *               is used and workspace may be NULL; (size_t)-1 means that the

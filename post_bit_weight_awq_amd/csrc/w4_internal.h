@@ -117,6 +117,8 @@ size_t w4_gemm_workspace(const W4Args& a);
 size_t w4_input_grad_workspace(const W4Args& a);
 // dX of a.out0 from dY
 hipError_t launch_w4_input_grad(const W4Args& a, const void* dY, hipStream_t stream);
+size_t w4_param_grad_workspace(const W4Args& a);
+hipError_t launch_w4_param_grad(const W4Args& a, hipStream_t stream);
 hipError_t launch_w4_gemm(W4Op op, const W4Args& a, hipStream_t stream);
 
 }  // namespace awq

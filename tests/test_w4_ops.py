@@ -117,8 +117,10 @@ def test_plain_weights_brute_force():
     for o in range(3):
         for k in range(128):
             c = (int(q[o, k // 8]) >> (4 * (k % 8))) & 15
-            d = float(torch.tensor(c - float(z[o, k // 32])).half())
-            assert float(w[o, k]) == d * float(s[o, k // 32])
+            d = float(w[o, k]) / float(s[o, k // 32])
+            exact = c - float(z[o, k // 32])
+            # 11 bits, or within 2^-15 (two roundings to its multiples)
+            assert abs(d - exact) <= max(2.0 ** -11 * abs(exact), 2.0 ** -15)
 
 
 @pytest.mark.parametrize("name", ["silu", "gelu"])

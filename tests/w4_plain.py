@@ -48,9 +48,12 @@ def spread(p, k):
 
 
 def differences(qweight, zero):
-    """q - zero, rounded once to fp16 as the operators take it."""
+    """q - zero as the operators take it: in fp16 and units of 2^-9, so with 11
+    bits or to a multiple of 2^-15, the zero first (where it is below 2^-5)
+    and then the difference."""
     q = codes(qweight)
-    return (q - spread(zero, q.shape[1])).to(torch.float16).to(F64)
+    z = (zero.to(F64) / 512).to(torch.float16).to(F64)
+    return (q / 512 - spread(z, q.shape[1])).to(torch.float16).to(F64) * 512
 
 
 def weights(qweight, step, zero):
