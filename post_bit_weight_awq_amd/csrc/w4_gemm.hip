@@ -4,16 +4,14 @@
 // Block tile 32 MT tokens x 256 packed rows (gated: 128 rows of the gate and
 // the same features' 128 up rows), eight wavefronts as 2 (tokens) x 4 (rows),
 // each 16 MT x 64 as MT x 4 tiles of v_mfma_f32_16x16x32_f16.
-//   * Activations move to LDS 128 columns at a time by direct loads, two
-//     stages; the 16-byte piece p of row r sits at p ^ (r % 16), so fragment
-//     reads hit every bank once.
-//   * Codes go from memory to registers (16 bytes per lane, row and step, one
-//     step ahead) and become (q - z) 2^-9 in fp16 there, exactly, ten
-//     operations per eight: no LDS traffic and a quarter of the load bytes of
-//     16-bit weights.
+//   * Activations move to LDS 64 columns at a time, codes and group parameters
+//     128 columns at a time, by direct loads up to two steps ahead; 16-byte
+//     pieces are permuted by row so that reads hit every bank once.
+//   * Codes become (q - z) 2^-9 in fp16 in registers, exactly, ten operations
+//     per eight: four bits per weight through LDS instead of sixteen.
 //   * The step enters in fp32.  The accumulators of a row are kept in units
 //     of the present group's step: where a group begins they are multiplied
-//     by (last step / this step), and the last group's step by the epilogue.
+//     by (last step / this step), and by the last group's step at the end.
 //     So the MFMAs accumulate in place and no product is rounded to 16 bits.
 //   * A group whose step is 0 leaves the unit as it is and takes codes and
 //     zero as 0.
@@ -132,68 +130,168 @@ hipError_t launch_rows_to_half(const void* in, int type, int64_t rows, int64_t c
   return hipGetLastError();
 }
 
-constexpr int kBN = 256;   // packed rows per block
+constexpr int kBN = 256;    // packed rows per block
 constexpr int kEpRow = 68;  // floats per token of a wavefront's 64 columns in the epilogue's LDS
-constexpr int kEpBytes = 8 * 32 * kEpRow * 4;
+constexpr int kEpWave = 32 * kEpRow;
 
-template <typename T, int GROUP, bool GATED, int ACT, int MT, typename TY>
+// What the last step of a product does with its sums.
+struct Epilogue {
+  const int* back;  // a token's exponent, or NULL
+  void *y, *pre;
+  int N, O, y_type, type, act;
+};
+
+template <bool GATED, typename T>
+__device__ __forceinline__ void store_outputs(const Epilogue& e, int token, int o, int outs,
+                                              float (&v)[8], const float (&u)[8], T* y) {
+  if constexpr (GATED) {
+    const int F = outs;
+    if (e.pre) {
+      T* pre = (T*)e.pre + (size_t)token * 2 * F + o;
+      store8(pre, v, F - o, (F & 7) == 0);
+      store8(pre + F, u, F - o, (F & 7) == 0);
+    }
+    if (e.act == kActSilu) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = act_value<kActSilu>(v[i], nullptr) * u[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = act_value<kActGelu>(v[i], nullptr) * u[i];
+    }
+  }
+  store8(y + (size_t)token * outs + o, v, outs - o, (outs & 7) == 0);
+}
+
+// 32 tokens from t0 of a wavefront's 64 columns (gated: 32 of the gate, then
+// their 32 up columns), through the wavefront's own LDS: eight columns of a
+// token per lane then, stored as whole 16-byte pieces.  Register r of lane l
+// is token 4 (l / 16) + r, column l % 16 of its tile.
+template <bool GATED>
+__device__ __forceinline__ void finish32(const floatx4 (&v0)[4], const floatx4 (&v1)[4], float* ep,
+                                         const Epilogue& e, int t0, int ob, int lane) {
+  constexpr int CW = GATED ? 32 : 64, LPT = CW / 8;
+  const int r16 = lane & 15, q4 = lane >> 4;
+  const int outs = GATED ? e.O / 2 : e.O;
+#pragma unroll
+  for (int n = 0; n < 4; ++n)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      ep[(4 * q4 + r) * kEpRow + 16 * n + r16] = v0[n][r];
+      ep[(16 + 4 * q4 + r) * kEpRow + 16 * n + r16] = v1[n][r];
+    }
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the wavefront's own writes
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int it = 0; it < 32 * LPT / 64; ++it) {
+    const int tl = it * (64 / LPT) + lane / LPT, c8 = 8 * (lane % LPT);
+    const int token = t0 + tl, o = ob + c8;
+    float v[8], u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = ep[tl * kEpRow + c8 + i];
+      u[i] = GATED ? ep[tl * kEpRow + 32 + c8 + i] : 0.0f;
+    }
+    if (token >= e.N || o >= outs) continue;
+    if (e.back) {
+      const int x = e.back[token];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] = ldexpf(v[i], x);
+        if (GATED) u[i] = ldexpf(u[i], x);
+      }
+    }
+    if (!GATED && e.y_type == kF32)
+      store_outputs<GATED>(e, token, o, outs, v, u, (float*)e.y);
+    else if (e.type == kF16)
+      store_outputs<GATED>(e, token, o, outs, v, u, (_Float16*)e.y);
+    else
+      store_outputs<GATED>(e, token, o, outs, v, u, (__bf16*)e.y);
+  }
+  asm volatile("" ::: "memory");
+}
+
+template <int GROUP, int MT>
+struct GemmLds {
+  static constexpr int kA = 32 * MT * 128;            // 64 columns of the activations
+  static constexpr int kC = kBN * 64;                 // 128 columns of codes
+  static constexpr int kP = kBN * 4 * (128 / GROUP);  // their group parameters
+  static constexpr int kOffC = 3 * kA, kOffP = kOffC + 2 * kC;
+  static constexpr int kMain = kOffP + 2 * kP;
+  static constexpr int kBytes = kMain > 8 * kEpWave * 4 ? kMain : 8 * kEpWave * 4;
+};
+
+template <int GROUP, bool GATED, int MT>
 __global__ void __launch_bounds__(512, 2)
-k_w4_gemm(const _Float16* __restrict__ A, const int* __restrict__ back, int N, int K, int O,
-          const uint32_t* __restrict__ qw, const uint32_t* __restrict__ prm, TY* __restrict__ Y,
-          T* __restrict__ pre, int nt, int no) {
+k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
+          const char* __restrict__ prm, float* __restrict__ parts, TileSplit sp, Epilogue ep) {
+  using L = GemmLds<GROUP, MT>;
   constexpr int BM = 32 * MT;
   constexpr int GPB = 128 / GROUP, JG = 4 / GPB;
-  constexpr int STAGE = BM * 128;  // halfs
-  extern __shared__ __attribute__((aligned(16))) _Float16 smem[];
+  constexpr int AL = MT / 2;                  // direct loads of activations per wavefront and step
+  constexpr int PL = GPB == 4 ? 2 : 1;        // of group parameters per 128 columns
+  extern __shared__ __attribute__((aligned(16))) char smem[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 2, wn = wave & 3;
   const int r16 = lane & 15, q4 = lane >> 4;
-  const TileUnit un = tile_unit(blockIdx.x, nt, no, nt * no);
-  const int F = O >> 1;
+  const SplitUnit un = split_unit(blockIdx.x, sp);
+  const int N = ep.N, O = ep.O, F = O >> 1;
   const int t0 = un.t * BM, rb = un.o * (GATED ? kBN / 2 : kBN);
-  const int outs = GATED ? F : O;
-  const int nkb = K >> 7;
+  const uint32_t lds = (uint32_t)(uintptr_t)smem;
 
-  // direct loads of the activations: load i brings 4 rows of 256 bytes
-  uint32_t oa[MT];
+  // activations: load i brings 8 rows of 128 bytes; 16-byte piece p of row r
+  // at p ^ (r % 8)
+  uint32_t oa[AL];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int r = 4 * (wave * MT + i) + q4;
-    oa[i] = 2u * ((uint32_t)(min(t0 + r, N - 1) - t0) * (uint32_t)K + 8 * (r16 ^ (r & 15)));
+  for (int i = 0; i < AL; ++i) {
+    const int r = 8 * (wave * AL + i) + (lane >> 3);
+    oa[i] = 2u * ((uint32_t)(min(t0 + r, N - 1) - t0) * (uint32_t)K + 8 * ((lane & 7) ^ (r & 7)));
   }
-  const _Float16* a0 = A + (size_t)t0 * K;
+  const char* a0 = (const char*)(A + (size_t)t0 * K);
   auto load_a = [&](int s) {
-    const _Float16* base = a0 + s * 128;
-    const _Float16* d = smem + (s & 1) * STAGE + wave * MT * 512;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) dma16(base, oa[i], (uint32_t)(uintptr_t)(d + i * 512));
+    for (int i = 0; i < AL; ++i)
+      dma16(a0 + s * 128, oa[i], lds + (s % 3) * L::kA + (wave * AL + i) * 1024);
   };
-  // row of tile n (16 rows each) for this lane, past the end the last one
-  int prow[4];
-  uint32_t oq[4];
+  // Block row i: wavefront column i / 64; gated, its first 32 rows are the
+  // gate's and the next 32 the same features' up rows.  Past the end the last
+  // row is repeated.
+  auto packed_row = [&](int i) {
+    if (GATED) return min(rb + 32 * (i >> 6) + (i & 31), F - 1) + (i & 32 ? F : 0);
+    return min(rb + i, O - 1);
+  };
+  // codes: a load brings 16 rows of 64 bytes; 16-byte piece p of row r at
+  // p ^ (r / 4 % 4)
+  uint32_t oc[2];
+  const char* c0[2];
 #pragma unroll
-  for (int n = 0; n < 4; ++n) {
-    if (GATED)
-      prow[n] = min(rb + 32 * wn + 16 * (n & 1) + r16, F - 1) + (n < 2 ? 0 : F);
-    else
-      prow[n] = min(rb + 64 * wn + 16 * n + r16, O - 1);
+  for (int i = 0; i < 2; ++i) {
+    // a load's 16 rows lie in one half of the packed rows
+    const int r = 16 * (2 * wave + i), row = packed_row(r);
+    c0[i] = qw + (size_t)row * (K >> 1);
+    oc[i] = (uint32_t)(packed_row(r + (lane >> 2)) - row) * (uint32_t)(K >> 1) +
+            16 * ((lane & 3) ^ ((lane >> 4) & 3));
   }
-  // codes relative to the block's first row (of the gate's or the up rows)
-  const uint32_t* q0 = qw + (size_t)rb * (K >> 3);
-  const uint32_t* q1 = GATED ? q0 + (size_t)F * (K >> 3) : q0;
+  // parameters: 64 rows of one group (32 with one group per 128 columns)
+  uint32_t op[PL];
 #pragma unroll
-  for (int n = 0; n < 4; ++n)
-    oq[n] = (uint32_t)(prow[n] - rb - (GATED && n >= 2 ? F : 0)) * (uint32_t)(K >> 3) + 4 * q4;
-  uint4 cn[4];
-  uint32_t pn[4][GPB];
-  auto load_w = [&](int s) {
+  for (int i = 0; i < PL; ++i) {
+    const int at = GPB == 1 ? 32 * wave + (lane & 31) : 64 * (wave * PL + i) + lane;
+    op[i] = 4u * ((uint32_t)(at / kBN) * (uint32_t)O + (uint32_t)packed_row(at % kBN));
+  }
+  auto load_w = [&](int kb) {
 #pragma unroll
-    for (int n = 0; n < 4; ++n) cn[n] = *(const uint4*)((n < 2 ? q0 : q1) + oq[n] + 16 * s);
+    for (int i = 0; i < 2; ++i)
+      dma16(c0[i] + 64 * kb, oc[i], lds + L::kOffC + (kb & 1) * L::kC + (2 * wave + i) * 1024);
+    const char* p = prm + (size_t)kb * GPB * O * 4;
+    const uint32_t l = lds + L::kOffP + (kb & 1) * L::kP;
+    if (GPB == 1) {
+      if (lane < 32) dma4(p, op[0], l + wave * 128);
+    } else {
 #pragma unroll
-    for (int g = 0; g < GPB; ++g)
-#pragma unroll
-      for (int n = 0; n < 4; ++n) pn[n][g] = prm[(size_t)(s * GPB + g) * O + prow[n]];
+      for (int i = 0; i < PL; ++i) dma4(p, op[i], l + (wave * PL + i) * 256);
+    }
   };
 
   floatx4 acc[MT][4];
@@ -204,77 +302,72 @@ k_w4_gemm(const _Float16* __restrict__ A, const int* __restrict__ back, int N, i
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[m][n] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  load_w(0);
-  load_a(0);
-  for (int s = 0; s < nkb; ++s) {
-    // this step's operands have landed, and no wavefront still reads the
-    // other stage
-    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
-    __syncthreads();
-    uint4 c[4];
-    uint32_t p[4][GPB];
+  const int kend = un.s1;
+  load_a(2 * un.s0);
+  load_w(un.s0);
+  load_a(2 * un.s0 + 1);
+  for (int kb = un.s0; kb < kend; ++kb) {
+    const char* pc = smem + L::kOffC + (kb & 1) * L::kC + (64 * wn + r16) * 64 + 4 * q4;
+    const char* pp = smem + L::kOffP + (kb & 1) * L::kP + (64 * wn + r16) * 4;
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      c[n] = cn[n];
-#pragma unroll
-      for (int g = 0; g < GPB; ++g) p[n][g] = pn[n][g];
-    }
-    if (s + 1 < nkb) {
-      load_w(s + 1);
-      load_a(s + 1);
-    }
-    if (GPB > 1)
-#pragma unroll
-      for (int n = 0; n < 4; ++n) transpose_words(c[n]);
-    const _Float16* ta = smem + (s & 1) * STAGE + (wm * MT * 16 + r16) * 128;
-#pragma unroll
-    for (int g = 0; g < GPB; ++g) {
-      float ratio[4];
-      uint32_t nz[4];
-      bool none = false;
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const uint32_t w = p[n][g];
-        nz[n] = (w >> 16) | (w & 0xffff0000u);
-        none |= (w & 0x7fffu) == 0;
+    for (int h = 0; h < 2; ++h) {
+      const int s = 2 * kb + h;
+      // first half: its activations and the block's codes have landed (the
+      // second half's activations may be in flight); second half: its
+      // activations have (what the first half requested may be in flight).
+      // No wavefront still reads the stages requested next.
+      if (h == 0)
+        wait_vm<AL>();
+      else if (kb + 1 < kend)
+        wait_vm<AL + 2 + PL>();
+      else
+        wait_vm<0>();
+      __syncthreads();
+      if (kb + 1 < kend) {
+        load_a(s + 2);
+        if (h == 0) load_w(kb + 1);
       }
-      if (__any(none)) {
+      const char* ta = smem + (s % 3) * L::kA + (wm * MT * 16 + r16) * 128;
+#pragma unroll
+      for (int j2 = 0; j2 < 2; ++j2) {
+        const int j = 2 * h + j2, g = j / JG;
+        uint32_t w[4], nz[4];
+        float ratio[4];
 #pragma unroll
         for (int n = 0; n < 4; ++n)
-          if ((p[n][g] & 0x7fffu) == 0) {
-            // nothing of this group counts: its codes and zero are 0
-            nz[n] = 0;
+          w[n] = *(const uint32_t*)(pc + n * 1024 + 16 * (j ^ (r16 >> 2)));
+        bool none = false;
 #pragma unroll
-            for (int j = 0; j < JG; ++j) {
-              const int at = g * JG + j;
-              if (at == 0) c[n].x = 0;
-              if (at == 1) c[n].y = 0;
-              if (at == 2) c[n].z = 0;
-              if (at == 3) c[n].w = 0;
-            }
+        for (int n = 0; n < 4; ++n) {
+          const uint32_t p = *(const uint32_t*)(pp + g * (kBN * 4) + n * 64);
+          nz[n] = (p >> 16) | (p & 0xffff0000u);
+          const bool zero = (p & 0x7fffu) == 0;
+          none |= zero;
+          if (j % JG == 0) {
+            const float st = zero ? unit[n] : f16_lo(p);
+            // 1 / st to the last bit by one Newton step
+            const float r = __builtin_amdgcn_rcpf(st);
+            ratio[n] = unit[n] * fmaf(fmaf(-st, r, 1.0f), r, r);
+            unit[n] = st;
           }
-      }
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const float st = (p[n][g] & 0x7fffu) == 0 ? unit[n] : f16_lo(p[n][g]);
-        // 1 / st to the last bit by one Newton step
-        const float r = __builtin_amdgcn_rcpf(st);
-        ratio[n] = unit[n] * fmaf(fmaf(-st, r, 1.0f), r, r);
-        unit[n] = st;
-      }
-#pragma unroll
-      for (int j = 0; j < JG; ++j) {
-        const int at = g * JG + j;
-        const int piece = GPB > 1 ? 4 * at + q4 : 4 * q4 + at;
-        uint4 b[4];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) b[n] = dequant_word(word_of(c[n], at), nz[n]);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const uint4 a = *(const uint4*)(ta + m * 2048 + 8 * (piece ^ r16));
+        }
+        if (__any(none)) {
+          // nothing of a group with step 0 counts: codes and zero as 0
 #pragma unroll
           for (int n = 0; n < 4; ++n) {
-            if (j == 0)
+            const uint32_t p = *(const uint32_t*)(pp + g * (kBN * 4) + n * 64);
+            if ((p & 0x7fffu) == 0) w[n] = nz[n] = 0;
+          }
+        }
+        uint4 b[4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) b[n] = dequant_word(w[n], nz[n]);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const uint4 a = *(const uint4*)(ta + m * 2048 + 16 * ((4 * j2 + q4) ^ (r16 & 7)));
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            if (j % JG == 0)
 #pragma unroll
               for (int r = 0; r < 4; ++r) acc[m][n][r] *= ratio[n];
             acc[m][n] = mfma16<_Float16>(a, b[n], acc[m][n]);
@@ -283,65 +376,51 @@ k_w4_gemm(const _Float16* __restrict__ A, const int* __restrict__ back, int N, i
       }
     }
   }
-  __syncthreads();
-
-  // epilogue, 32 tokens of the wavefront at a time through its own LDS: tokens
-  // by columns, then eight columns of a token per lane
-  float* const ep = (float*)smem + wave * 32 * kEpRow;
-  const int tw = t0 + wm * MT * 16;
-  constexpr int CW = GATED ? 32 : 64;  // outputs of the wavefront
-  const int ob = rb + CW * wn;
 #pragma unroll
-  for (int h = 0; h < MT / 2; ++h) {
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int mm = 0; mm < 2; ++mm)
+    for (int n = 0; n < 4; ++n)
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
+      for (int r = 0; r < 4; ++r) acc[m][n][r] *= unit[n] * kCodeScale;
+  if (un.parts > 1) {
+    floatx4* p = (floatx4*)parts + ((size_t)un.slot * 8 + wave) * (MT * 4 * 64) + lane;
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          ep[(16 * mm + 4 * q4 + r) * kEpRow + 16 * n + r16] =
-              acc[2 * h + mm][n][r] * (unit[n] * kCodeScale);
-    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the wavefront's own writes
-    asm volatile("" ::: "memory");
-    constexpr int LPT = CW / 8;  // lanes per token
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int it = 0; it < 32 * LPT / 64; ++it) {
-      const int tl = it * (64 / LPT) + lane / LPT, c8 = 8 * (lane % LPT);
-      const int token = tw + 32 * h + tl, o = ob + c8;
-      float v[8], u[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v[e] = ep[tl * kEpRow + c8 + e];
-        if (GATED) u[e] = ep[tl * kEpRow + 32 + c8 + e];
-      }
-      if (token >= N || o >= outs) continue;
-      if (back) {
-        const int x = back[token];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          v[e] = ldexpf(v[e], x);
-          if (GATED) u[e] = ldexpf(u[e], x);
-        }
-      }
-      if (GATED) {
-        if (pre) {
-          store8(pre + (size_t)token * O + o, v, outs - o, (F & 7) == 0);
-          store8(pre + (size_t)token * O + F + o, u, outs - o, (F & 7) == 0);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = act_value<ACT>(v[e], nullptr) * u[e];
-      }
-      store8(Y + (size_t)token * outs + o, v, outs - o, (outs & 7) == 0);
-    }
-    asm volatile("" ::: "memory");
+      for (int n = 0; n < 4; ++n) p[(m * 4 + n) * 64] = acc[m][n];
+    return;
   }
+  __syncthreads();
+#pragma unroll
+  for (int m = 0; m < MT; m += 2)
+    finish32<GATED>(acc[m], acc[m + 1], (float*)smem + wave * kEpWave, ep,
+                    t0 + wm * MT * 16 + 16 * m, rb + (GATED ? 32 : 64) * wn, lane);
+}
+
+// Sums of a split tile's parts, in order; a block takes 32 tokens of one
+// wavefront's columns.
+template <bool GATED>
+__global__ void __launch_bounds__(64)
+k_gemm_join(const float* __restrict__ parts, TileSplit sp, Epilogue ep, int mt) {
+  __shared__ float lds[kEpWave];
+  const int lane = threadIdx.x;
+  const int mp = blockIdx.x % (mt / 2), wave = blockIdx.x / (mt / 2) % 8, left = blockIdx.x / (mt * 4);
+  const TileUnit un = tile_unit(sp.full + left, sp.nt, sp.no, sp.full + sp.left);
+  floatx4 v[2][4];
+  join_parts(parts, sp, left, wave, mt, mp, lane, v);
+  finish32<GATED>(v[0], v[1], lds, ep, un.t * 32 * mt + (wave >> 2) * mt * 16 + 32 * mp,
+                  un.o * (GATED ? kBN / 2 : kBN) + (GATED ? 32 : 64) * (wave & 3), lane);
 }
 
 struct GemmPlan {
-  size_t off_prm, off_a, off_back, bytes;
+  int mt;
+  TileSplit sp;
+  size_t off_prm, off_a, off_back, off_parts, bytes;
 };
-static GemmPlan gemm_plan(const W4Args& a) {
+static GemmPlan gemm_plan(W4Op op, const W4Args& a) {
   GemmPlan p;
+  const int64_t outs = op == kOpGated ? a.O / 2 : a.O, per = op == kOpGated ? kBN / 2 : kBN;
+  choose_tiles(a.N, (int)((outs + per - 1) / per), (int)(a.K / 128), kGemmCosts, &p.mt, &p.sp);
   size_t at = 0;
   p.off_prm = at;
   at += align256((size_t)a.O * (a.K / a.group) * 4);
@@ -351,56 +430,51 @@ static GemmPlan gemm_plan(const W4Args& a) {
     p.off_back = at;
     at += align256((size_t)a.N * 4);
   }
+  p.off_parts = at;
+  if (p.sp.parts > 1) at += (size_t)p.sp.left * p.sp.parts * p.mt * 32 * kBN * 4;
   p.bytes = at;
   return p;
 }
-size_t w4_gemm_workspace(const W4Args& a) { return gemm_plan(a).bytes; }
+size_t w4_gemm_workspace(W4Op op, const W4Args& a) { return gemm_plan(op, a).bytes; }
 
-template <typename T, int GROUP, bool GATED, int ACT, int MT, typename TY>
+template <int GROUP, bool GATED, int MT>
 static hipError_t launch(const W4Args& a, const GemmPlan& p, hipStream_t stream) {
-  constexpr int BM = 32 * MT;
-  const int64_t outs = GATED ? a.O / 2 : a.O;
-  const int nt = (int)((a.N + BM - 1) / BM);
-  const int no = (int)((outs + (GATED ? kBN / 2 : kBN) - 1) / (GATED ? kBN / 2 : kBN));
-  const size_t lds = 2 * BM * 256 > kEpBytes ? 2 * BM * 256 : kEpBytes;
-  auto* kernel = &k_w4_gemm<T, GROUP, GATED, ACT, MT, TY>;
-  const hipError_t e = hipFuncSetAttribute((const void*)kernel,
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  auto* kernel = &k_w4_gemm<GROUP, GATED, MT>;
+  const int lds = GemmLds<GROUP, MT>::kBytes;
+  const hipError_t e =
+      hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;
   char* ws = (char*)a.ws;
   const bool bf = a.type == kBF16;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)(nt * no)), dim3(512), lds, stream,
-                     bf ? (const _Float16*)(ws + p.off_a) : (const _Float16*)a.in0,
-                     bf ? (const int*)(ws + p.off_back) : nullptr, (int)a.N, (int)a.K, (int)a.O,
-                     (const uint32_t*)a.qweight, (const uint32_t*)(ws + p.off_prm), (TY*)a.out0,
-                     (T*)a.out1, nt, no);
+  const Epilogue ep{bf ? (const int*)(ws + p.off_back) : nullptr,
+                    a.out0, a.out1, (int)a.N, (int)a.O, a.y_type, a.type, a.act};
+  float* parts = (float*)(ws + p.off_parts);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(p.sp.full + p.sp.left * p.sp.parts)), dim3(512), lds,
+                     stream, bf ? (const _Float16*)(ws + p.off_a) : (const _Float16*)a.in0, (int)a.K,
+                     (const char*)a.qweight, ws + p.off_prm, parts, p.sp, ep);
+  if (p.sp.parts > 1)
+    hipLaunchKernelGGL(k_gemm_join<GATED>, dim3((unsigned)(p.sp.left * 4 * MT)), dim3(64), 0, stream,
+                       parts, p.sp, ep, MT);
   return hipGetLastError();
 }
 
-template <typename T, int GROUP, bool GATED, int ACT, typename TY>
-static hipError_t by_tokens(const W4Args& a, const GemmPlan& p, hipStream_t stream) {
-  if (a.N <= 128) return launch<T, GROUP, GATED, ACT, 4, TY>(a, p, stream);
-  return launch<T, GROUP, GATED, ACT, 8, TY>(a, p, stream);
+template <int GROUP, bool GATED>
+static hipError_t by_tile(const W4Args& a, const GemmPlan& p, hipStream_t stream) {
+  if (p.mt == 2) return launch<GROUP, GATED, 2>(a, p, stream);
+  if (p.mt == 4) return launch<GROUP, GATED, 4>(a, p, stream);
+  if (p.mt == 6) return launch<GROUP, GATED, 6>(a, p, stream);
+  return launch<GROUP, GATED, 8>(a, p, stream);
 }
 
-template <typename T, int GROUP>
-static hipError_t by_op(W4Op op, const W4Args& a, const GemmPlan& p, hipStream_t stream) {
-  if (op == kOpGated)
-    return a.act == kActSilu ? by_tokens<T, GROUP, true, kActSilu, T>(a, p, stream)
-                             : by_tokens<T, GROUP, true, kActGelu, T>(a, p, stream);
-  return a.y_type == kF32 ? by_tokens<T, GROUP, false, 0, float>(a, p, stream)
-                          : by_tokens<T, GROUP, false, 0, T>(a, p, stream);
-}
-
-template <typename T>
-static hipError_t by_group(W4Op op, const W4Args& a, const GemmPlan& p, hipStream_t stream) {
-  if (a.group == 128) return by_op<T, 128>(op, a, p, stream);
-  if (a.group == 64) return by_op<T, 64>(op, a, p, stream);
-  return by_op<T, 32>(op, a, p, stream);
+template <bool GATED>
+static hipError_t by_group(const W4Args& a, const GemmPlan& p, hipStream_t stream) {
+  if (a.group == 128) return by_tile<128, GATED>(a, p, stream);
+  if (a.group == 64) return by_tile<64, GATED>(a, p, stream);
+  return by_tile<32, GATED>(a, p, stream);
 }
 
 hipError_t launch_w4_gemm(W4Op op, const W4Args& a, hipStream_t stream) {
-  const GemmPlan p = gemm_plan(a);
+  const GemmPlan p = gemm_plan(op, a);
   char* ws = (char*)a.ws;
   const int ng = (int)(a.K / a.group);
   hipLaunchKernelGGL(k_w4_params, dim3((unsigned)((a.O + 31) / 32), (unsigned)((ng + 31) / 32)),
@@ -410,9 +484,8 @@ hipError_t launch_w4_gemm(W4Op op, const W4Args& a, hipStream_t stream) {
     const hipError_t e = launch_rows_to_half(a.in0, a.type, a.N, a.K, a.K, ws + p.off_a,
                                              (int*)(ws + p.off_back), stream);
     if (e != hipSuccess) return e;
-    return by_group<__bf16>(op, a, p, stream);
   }
-  return by_group<_Float16>(op, a, p, stream);
+  return op == kOpGated ? by_group<true>(a, p, stream) : by_group<false>(a, p, stream);
 }
 
 }  // namespace awq

@@ -224,29 +224,20 @@ k_w4_dx(const _Float16* __restrict__ A, int lda, const int* __restrict__ back, i
   store_dx<T, MT>(acc, back, N, K, t0 + wm * MT * 16, k0 + 128 * wb + 8 * r16 + 4 * half, lane, dX);
 }
 
-// Sums of a split tile's parts, in order, one wavefront's share per block.
-template <typename T, int MT>
+// Sums of a split tile's parts, in order; a block takes 32 tokens of one
+// wavefront's columns.
+template <typename T>
 __global__ void __launch_bounds__(64)
 k_dx_join(const float* __restrict__ parts, const int* __restrict__ back, int N, int K,
-          T* __restrict__ dX, TileSplit sp) {
-  const int lane = threadIdx.x, wave = blockIdx.x & 7, left = blockIdx.x >> 3;
+          T* __restrict__ dX, TileSplit sp, int mt) {
+  const int lane = threadIdx.x;
+  const int mp = blockIdx.x % (mt / 2), wave = blockIdx.x / (mt / 2) % 8, left = blockIdx.x / (mt * 4);
   const TileUnit un = tile_unit(sp.full + left, sp.nt, sp.no, sp.full + sp.left);
-  const floatx4* p = (const floatx4*)parts + ((size_t)left * sp.parts * 8 + wave) * (MT * 4 * 64) + lane;
-  floatx4 acc[MT][4];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) acc[m][c] = p[(m * 4 + c) * 64];
-  for (int i = 1; i < sp.parts; ++i) {
-    const floatx4* q = p + (size_t)i * 8 * (MT * 4 * 64);
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[m][c] += q[(m * 4 + c) * 64];
-  }
+  floatx4 v[2][4];
+  join_parts(parts, sp, left, wave, mt, mp, lane, v);
   const int wm = wave >> 2, wn = wave & 3;
-  store_dx<T, MT>(acc, back, N, K, un.t * 32 * MT + wm * MT * 16,
-                  un.o * 256 + 128 * (wn >> 1) + 8 * (lane & 15) + 4 * (wn & 1), lane, dX);
+  store_dx<T, 2>(v, back, N, K, un.t * 32 * mt + wm * mt * 16 + 32 * mp,
+                 un.o * 256 + 128 * (wn >> 1) + 8 * (lane & 15) + 4 * (wn & 1), lane, dX);
 }
 
 struct DxPlan {
@@ -260,9 +251,7 @@ static DxPlan dx_plan(const W4Args& a) {
   p.steps = (int)((a.O + 63) / 64);
   p.copy = a.type == kBF16 || a.O % 64;
   p.lda = p.copy ? p.steps * 64 : (int)a.O;
-  p.mt = a.N <= 64 ? 2 : a.N <= 128 ? 4 : 8;
-  const int bm = 32 * p.mt;
-  p.sp = tile_split((int)((a.N + bm - 1) / bm), (int)((a.K + 255) / 256), p.steps, 4);
+  choose_tiles(a.N, (int)((a.K + 255) / 256), p.steps, kDxCosts, &p.mt, &p.sp);
   size_t at = 0;
   p.off_prm = at;
   at += align256((size_t)p.steps * 64 * (a.K / a.group) * 4);
@@ -271,7 +260,7 @@ static DxPlan dx_plan(const W4Args& a) {
   p.off_back = at;
   if (p.copy) at += align256((size_t)a.N * 4);
   p.off_parts = at;
-  if (p.sp.parts > 1) at += (size_t)p.sp.left * p.sp.parts * bm * 256 * 4;
+  if (p.sp.parts > 1) at += (size_t)p.sp.left * p.sp.parts * p.mt * 32 * 256 * 4;
   p.bytes = at;
   return p;
 }
@@ -292,8 +281,8 @@ static hipError_t launch(const W4Args& a, const void* dY, const DxPlan& p, hipSt
                      back, (int)a.N, (int)a.K, (int)a.O, (const char*)a.qweight, ws + p.off_prm,
                      (T*)a.out0, parts, p.sp);
   if (p.sp.parts > 1)
-    hipLaunchKernelGGL((k_dx_join<T, MT>), dim3((unsigned)(p.sp.left * 8)), dim3(64), 0, stream,
-                       parts, back, (int)a.N, (int)a.K, (T*)a.out0, p.sp);
+    hipLaunchKernelGGL((k_dx_join<T>), dim3((unsigned)(p.sp.left * 4 * MT)), dim3(64), 0, stream,
+                       parts, back, (int)a.N, (int)a.K, (T*)a.out0, p.sp, MT);
   return hipGetLastError();
 }
 
@@ -301,6 +290,7 @@ template <typename T, int GROUP>
 static hipError_t by_tokens(const W4Args& a, const void* dY, const DxPlan& p, hipStream_t stream) {
   if (p.mt == 2) return launch<T, GROUP, 2>(a, dY, p, stream);
   if (p.mt == 4) return launch<T, GROUP, 4>(a, dY, p, stream);
+  if (p.mt == 6) return launch<T, GROUP, 6>(a, dY, p, stream);
   return launch<T, GROUP, 8>(a, dY, p, stream);
 }
 

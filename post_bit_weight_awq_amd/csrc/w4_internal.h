@@ -35,21 +35,47 @@ struct TileSplit {
   int nt, no, steps, full, left, parts;
 };
 constexpr int kCUs = 256;
-// A part takes `least` steps or more.
-inline TileSplit tile_split(int nt, int no, int steps, int least) {
-  TileSplit s{nt, no, steps, nt * no, 0, 1};
-  const int left = s.full % kCUs;
-  if (left == 0) return s;
-  int parts = kCUs / left;
-  if (parts > steps / least) parts = steps / least;
-  if (parts < 2) return s;
-  s.left = left;
-  s.full -= left;
-  s.parts = parts;
-  return s;
+
+// Microseconds of a tile of 32 mt tokens by 256 (mt = 2, 4, 6, 8), per step of
+// the sum; the rest is common to all.
+struct TileCosts {
+  float step[4];
+};
+constexpr float kTileStart = 3.0f;            // a tile's first loads and its epilogue
+constexpr float kJoinStart = 4.0f;            // the second launch
+constexpr float kPartRate = 2.0e6f;           // bytes per microsecond of parts, written and read
+
+// Tile height and split with the least estimated time.
+inline void choose_tiles(int64_t N, int no, int steps, const TileCosts& c, int* mt_out, TileSplit* out) {
+  float best = 0.0f;
+  for (int i = 0; i < 4; ++i) {
+    const int mt = 2 * (i + 1);
+    const int nt = (int)((N + 32 * mt - 1) / (32 * mt));
+    const int total = nt * no, left = total % kCUs;
+    const float tile = c.step[i] * steps + kTileStart;
+    for (int parts = 1; parts <= 32 && parts <= steps; ++parts) {
+      if (parts > 1 && left == 0) break;
+      const int whole = total - left;
+      float t = (float)(whole / kCUs) * tile;
+      if (left) {
+        const int rounds = (left * parts + kCUs - 1) / kCUs;
+        t += (float)rounds * (c.step[i] * (float)((steps + parts - 1) / parts) + kTileStart);
+        if (parts > 1) t += kJoinStart + 2.0f * left * parts * mt * 32768.0f / kPartRate;
+      }
+      if (best == 0.0f || t < best) {
+        best = t;
+        *mt_out = mt;
+        *out = parts > 1 ? TileSplit{nt, no, steps, whole, left, parts}
+                         : TileSplit{nt, no, steps, total, 0, 1};
+      }
+    }
+  }
 }
+constexpr TileCosts kGemmCosts = {{1.2f, 1.6f, 2.0f, 2.5f}};
+constexpr TileCosts kDxCosts = {{0.6f, 0.8f, 1.0f, 1.2f}};
+
 struct SplitUnit {
-  int t, o, s0, s1, parts, slot;
+  int t, o, s0, s1, parts, slot;  // steps s0 .. s1 - 1
 };
 __device__ __forceinline__ SplitUnit split_unit(int b, const TileSplit& s) {
   SplitUnit r;
@@ -64,6 +90,22 @@ __device__ __forceinline__ SplitUnit split_unit(int b, const TileSplit& s) {
   r.s1 = (int)((int64_t)s.steps * (part + 1) / r.parts);
   r.slot = i;
   return r;
+}
+
+// The sum, in order, of a split tile's parts for tiles 2 mp and 2 mp + 1 of
+// wavefront `wave`'s mt x 4; parts are kept as the wavefronts' registers.
+__device__ __forceinline__ void join_parts(const float* parts, const TileSplit& sp, int left, int wave,
+                                           int mt, int mp, int lane, floatx4 (&v)[2][4]) {
+  const size_t tile = (size_t)mt * 4 * 64;
+  const floatx4* p = (const floatx4*)parts + ((size_t)left * sp.parts * 8 + wave) * tile +
+                     mp * 8 * 64 + lane;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i >> 2][i & 3] = p[i * 64];
+  for (int k = 1; k < sp.parts; ++k) {
+    p += 8 * tile;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i >> 2][i & 3] += p[i * 64];
+  }
 }
 
 // Direct loads to LDS: 16 (or 4) bytes per lane from base + off to l + 16 (4)
@@ -113,7 +155,7 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8], int n, bool al
 
 hipError_t launch_rows_to_half(const void* in, int type, int64_t rows, int64_t cols, int64_t ld_out, void* out,
                                int* back, hipStream_t stream);
-size_t w4_gemm_workspace(const W4Args& a);
+size_t w4_gemm_workspace(W4Op op, const W4Args& a);
 size_t w4_input_grad_workspace(const W4Args& a);
 // dX of a.out0 from dY
 hipError_t launch_w4_input_grad(const W4Args& a, const void* dY, hipStream_t stream);

@@ -38,7 +38,7 @@ size_t w4_workspace(W4Op op, const W4Args& a) {
   switch (op) {
     case kOpLinear:
     case kOpGated:
-      return w4_skinny_fits(a) ? 0 : w4_gemm_workspace(a);
+      return w4_skinny_fits(a) ? 0 : w4_gemm_workspace(op, a);
     case kOpInputGrad:
     case kOpGatedBackward:
       return w4_input_grad_workspace(a);

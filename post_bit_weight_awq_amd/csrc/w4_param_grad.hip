@@ -235,7 +235,16 @@ static PgPlan pg_plan(const W4Args& a) {
   PgPlan p;
   p.copy = a.O % 8 != 0;
   p.ldy = (int)((a.O + 7) / 8 * 8);
-  p.sp = tile_split((int)((a.O + 255) / 256), (int)((a.K + 255) / 256), (int)((a.N + 63) / 64), 2);
+  // the tiles of a last, partial round are split over tokens into parts that
+  // fill the chip; their sums are small
+  const int steps = (int)((a.N + 63) / 64);
+  TileSplit s{(int)((a.O + 255) / 256), (int)((a.K + 255) / 256), steps, 0, 0, 1};
+  const int total = s.nt * s.no, left = total % kCUs;
+  if (left) s.parts = kCUs / left < steps / 2 ? kCUs / left : steps / 2;
+  if (s.parts < 2) s.parts = 1;
+  if (s.parts > 1) s.left = left;
+  s.full = total - s.left;
+  p.sp = s;
   size_t at = 0;
   p.off_y = at;
   if (p.copy) at += align256((size_t)a.N * p.ldy * 2);
