@@ -53,10 +53,16 @@ __device__ __forceinline__ uint32_t neg_zero_pair(_Float16 z) {
   return b | (b << 16);
 }
 
+// The factors of a nibble in bits 0-3 of the low half and bits 4-7 of the
+// high one, as fp16 pairs.
+constexpr uint32_t kNibbleFactors = 0x68007800u;
+
 // The eight codes of a word, in column order, as (q - z) 2^-9: ten operations.
-__device__ __forceinline__ uint4 dequant_word(uint32_t w, uint32_t nz) {
+// With factors and zero 0 they all become 0.
+__device__ __forceinline__ uint4 dequant_word(uint32_t w, uint32_t nz,
+                                              uint32_t factors = kNibbleFactors) {
   const uint32_t lo = w & 0x0F0F0F0Fu, hi = w & 0xF0F0F0F0u;
-  const half2v m = {(_Float16)32768.0f, (_Float16)2048.0f};
+  const half2v m = __builtin_bit_cast(half2v, factors);
   const half2v z = __builtin_bit_cast(half2v, nz);
   auto pair = [&](uint32_t sel) {
     const half2v c = __builtin_bit_cast(half2v, __builtin_amdgcn_perm(hi, lo, sel));

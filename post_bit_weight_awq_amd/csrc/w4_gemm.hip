@@ -302,6 +302,8 @@ k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[m][n] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
   }
+  uint32_t nz[4], factors[4];
+  float ratio[4];
   const int kend = un.s1;
   load_a(2 * un.s0);
   load_w(un.s0);
@@ -331,37 +333,27 @@ k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
 #pragma unroll
       for (int j2 = 0; j2 < 2; ++j2) {
         const int j = 2 * h + j2, g = j / JG;
-        uint32_t w[4], nz[4];
-        float ratio[4];
+        uint32_t w[4];
 #pragma unroll
         for (int n = 0; n < 4; ++n)
           w[n] = *(const uint32_t*)(pc + n * 1024 + 16 * (j ^ (r16 >> 2)));
-        bool none = false;
+        if (j % JG == 0) {
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const uint32_t p = *(const uint32_t*)(pp + g * (kBN * 4) + n * 64);
-          nz[n] = (p >> 16) | (p & 0xffff0000u);
-          const bool zero = (p & 0x7fffu) == 0;
-          none |= zero;
-          if (j % JG == 0) {
-            const float st = zero ? unit[n] : f16_lo(p);
+          for (int n = 0; n < 4; ++n) {
+            const uint32_t p = *(const uint32_t*)(pp + g * (kBN * 4) + n * 64);
+            const bool none = (p & 0x7fffu) == 0;
+            nz[n] = none ? 0 : (p >> 16) | (p & 0xffff0000u);
+            factors[n] = none ? 0 : kNibbleFactors;
+            const float st = none ? unit[n] : f16_lo(p);
             // 1 / st to the last bit by one Newton step
             const float r = __builtin_amdgcn_rcpf(st);
             ratio[n] = unit[n] * fmaf(fmaf(-st, r, 1.0f), r, r);
             unit[n] = st;
           }
         }
-        if (__any(none)) {
-          // nothing of a group with step 0 counts: codes and zero as 0
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const uint32_t p = *(const uint32_t*)(pp + g * (kBN * 4) + n * 64);
-            if ((p & 0x7fffu) == 0) w[n] = nz[n] = 0;
-          }
-        }
         uint4 b[4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) b[n] = dequant_word(w[n], nz[n]);
+        for (int n = 0; n < 4; ++n) b[n] = dequant_word(w[n], nz[n], factors[n]);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           const uint4 a = *(const uint4*)(ta + m * 2048 + 16 * ((4 * j2 + q4) ^ (r16 & 7)));

@@ -20,16 +20,20 @@
 //   * dY in bf16, or of a width that is no multiple of 64, is copied to fp16
 //     rows of a padded width first (k_rows_to_half; zeros behind the row's
 //     end meet weights of 0).
+#include <type_traits>
+
 #include "w4_internal.h"
 
 namespace awq {
 
-// Group parameters by steps of 64 packed rows: prm[(s * ng + g) * 64 + ..] as
+// Group parameters by steps of 64 packed rows: prm[(s * ng + g) * 128 + ..] as
 // 64 halfs -zero 2^-9 and 64 halfs of the step; 0 for rows past the end.
+// big[s * gridDim.y + block of 32 groups]: whether a step is 128 or more.
 __global__ void __launch_bounds__(256)
 k_dx_params(const _Float16* __restrict__ step16, const _Float16* __restrict__ zero16, int O, int ng,
-            _Float16* __restrict__ prm) {
+            _Float16* __restrict__ prm, int* __restrict__ big) {
   __shared__ uint32_t tile[64][33];
+  int over = 0;
   const int o0 = blockIdx.x * 64, g0 = blockIdx.y * 32;
   for (int e = threadIdx.x; e < 64 * 32; e += 256) {
     const int r = e >> 5, c = e & 31;
@@ -38,10 +42,12 @@ k_dx_params(const _Float16* __restrict__ step16, const _Float16* __restrict__ ze
       const size_t at = (size_t)(o0 + r) * ng + g0 + c;
       v = (neg_zero_pair(zero16[at]) & 0xffffu) |
           ((uint32_t)__builtin_bit_cast(uint16_t, step16[at]) << 16);
+      over |= (v & 0x7fff0000u) >= 0x58000000u;  // 128
     }
     tile[r][c] = v;
   }
-  __syncthreads();
+  over = __syncthreads_or(over);
+  if (threadIdx.x == 0) big[blockIdx.x * gridDim.y + blockIdx.y] = over;
   for (int e = threadIdx.x; e < 64 * 32; e += 256) {
     const int c = e >> 6, r = e & 63;
     if (g0 + c >= ng) continue;
@@ -83,8 +89,8 @@ __device__ __forceinline__ void store_dx(const floatx4 (&acc)[MT][4], const int*
 template <typename T, int GROUP, int MT>
 __global__ void __launch_bounds__(512, 2)
 k_w4_dx(const _Float16* __restrict__ A, int lda, const int* __restrict__ back, int N, int K, int O,
-        const char* __restrict__ qw, const char* __restrict__ prm, T* __restrict__ dX,
-        float* __restrict__ parts, TileSplit sp) {
+        const char* __restrict__ qw, const char* __restrict__ prm, const int* __restrict__ big,
+        T* __restrict__ dX, float* __restrict__ parts, TileSplit sp) {
   using L = DxLds<MT>;
   constexpr int BM = 32 * MT;
   constexpr int AL = MT / 2;           // direct loads of dY per wavefront and step
@@ -141,78 +147,69 @@ k_w4_dx(const _Float16* __restrict__ A, int lda, const int* __restrict__ back, i
 
   load(un.s0);
   if (un.s0 + 1 < un.s1) load(un.s0 + 1);
-  for (int s = un.s0; s < un.s1; ++s) {
-    // the step's loads have landed (the next step's may be in flight), and no
-    // wavefront still reads the stage that is loaded next
-    if (s + 1 < un.s1)
-      wait_vm<AL + 2>();
-    else
-      wait_vm<0>();
-    __syncthreads();
-    if (s + 2 < un.s1) load(s + 2);
-    const char* st = smem + (s % kStages) * L::kStage;
-    const char* pc = st + L::kA + cbase;
-    const char* pp = st + L::kA + L::kC + gl * 256 + 16 * q4;
+  // steps of 128 and more among the block's: 512 step leaves fp16's range, so
+  // the factor goes to the differences, one operation more
+  int over = 0;
+  const int gb = (ng + 31) / 32, gb0 = k0 / GROUP / 32, gb1 = min(k0 + 255, K - 1) / GROUP / 32;
+  for (int s = un.s0 + tid; s < un.s1; s += 512) over |= big[s * gb + gb0] | big[s * gb + gb1];
+  over = __syncthreads_or(over);
+  auto sum = [&](auto plain) {
+    for (int s = un.s0; s < un.s1; ++s) {
+      // the step's loads have landed (the next step's may be in flight), and
+      // no wavefront still reads the stage that is loaded next
+      if (s + 1 < un.s1)
+        wait_vm<AL + 2>();
+      else
+        wait_vm<0>();
+      __syncthreads();
+      if (s + 2 < un.s1) load(s + 2);
+      const char* st = smem + (s % kStages) * L::kStage;
+      const char* pc = st + L::kA + cbase;
+      const char* pp = st + L::kA + L::kC + gl * 256 + 16 * q4;
 #pragma unroll
-    for (int ch = 0; ch < 2; ++ch) {
-      uint32_t w[8];
+      for (int ch = 0; ch < 2; ++ch) {
+        uint32_t w[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = *(const uint32_t*)(pc + ch * 4096 + i * 512);
-      const uint4 zv = *(const uint4*)(pp + ch * 64);
-      const uint4 sv = *(const uint4*)(pp + ch * 64 + 128);
-      uint4 b[4];
-      uint32_t bw[4][4];
-      uint32_t over = 0;
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const uint32_t t = __builtin_amdgcn_perm(w[2 * p + 1], w[2 * p], sel);
-        const uint32_t t8 = t >> 8;
-        const half2v z = __builtin_bit_cast(half2v, word_of(zv, p));
-        const half2v s1 = __builtin_bit_cast(half2v, word_of(sv, p));
-        const half2v m0 = {(_Float16)32768.0f, (_Float16)32768.0f};
-        const half2v m1 = {(_Float16)2048.0f, (_Float16)2048.0f};
-        const half2v k512 = {(_Float16)512.0f, (_Float16)512.0f};
-        const half2v zeros = {(_Float16)0.0f, (_Float16)0.0f};
-        const half2v s5 = s1 * k512;
-        // 0 where 512 step stays finite
-        over |= __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(s5, zeros, zeros));
-        const uint32_t n[4] = {t & 0x000F000Fu, t & 0x00F000F0u, t8 & 0x000F000Fu,
-                               t8 & 0x00F000F0u};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const half2v d = __builtin_elementwise_fma(__builtin_bit_cast(half2v, n[c]),
-                                                     c & 1 ? m1 : m0, z);
-          bw[c][p] = __builtin_bit_cast(uint32_t, d * s5);
-        }
-      }
-      if (__any(over != 0)) {
-        // steps of 128 and more: the factor 512 goes to the differences
+        for (int i = 0; i < 8; ++i) w[i] = *(const uint32_t*)(pc + ch * 4096 + i * 512);
+        const uint4 zv = *(const uint4*)(pp + ch * 64);
+        const uint4 sv = *(const uint4*)(pp + ch * 64 + 128);
+        uint32_t bw[4][4];
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           const uint32_t t = __builtin_amdgcn_perm(w[2 * p + 1], w[2 * p], sel);
+          const uint32_t t8 = t >> 8;
+          const half2v z = __builtin_bit_cast(half2v, word_of(zv, p));
+          const half2v s1 = __builtin_bit_cast(half2v, word_of(sv, p));
+          const half2v m0 = {(_Float16)32768.0f, (_Float16)32768.0f};
+          const half2v m1 = {(_Float16)2048.0f, (_Float16)2048.0f};
+          const half2v k512 = {(_Float16)512.0f, (_Float16)512.0f};
+          const half2v s5 = s1 * k512;
+          const uint32_t n[4] = {t & 0x000F000Fu, t & 0x00F000F0u, t8 & 0x000F000Fu,
+                                 t8 & 0x00F000F0u};
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const uint32_t n = (t >> (4 * c)) & 0x000F000Fu;
-            const half2v m0 = {(_Float16)32768.0f, (_Float16)32768.0f};
-            const half2v k512 = {(_Float16)512.0f, (_Float16)512.0f};
-            const half2v d = __builtin_elementwise_fma(__builtin_bit_cast(half2v, n), m0,
-                                                       __builtin_bit_cast(half2v, word_of(zv, p)));
-            bw[c][p] = __builtin_bit_cast(
-                uint32_t, (d * k512) * __builtin_bit_cast(half2v, word_of(sv, p)));
+            const half2v d = __builtin_elementwise_fma(__builtin_bit_cast(half2v, n[c]),
+                                                       c & 1 ? m1 : m0, z);
+            bw[c][p] = __builtin_bit_cast(uint32_t, plain ? d * s5 : (d * k512) * s1);
           }
         }
-      }
+        uint4 b[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) b[c] = make_uint4(bw[c][0], bw[c][1], bw[c][2], bw[c][3]);
-      const char* ta = st + (wm * MT * 16 + r16) * 128 + 16 * ((4 * ch + q4) ^ (r16 & 7));
+        for (int c = 0; c < 4; ++c) b[c] = make_uint4(bw[c][0], bw[c][1], bw[c][2], bw[c][3]);
+        const char* ta = st + (wm * MT * 16 + r16) * 128 + 16 * ((4 * ch + q4) ^ (r16 & 7));
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const uint4 a = *(const uint4*)(ta + m * 2048);
+        for (int m = 0; m < MT; ++m) {
+          const uint4 a = *(const uint4*)(ta + m * 2048);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[m][c] = mfma16<_Float16>(a, b[c], acc[m][c]);
+          for (int c = 0; c < 4; ++c) acc[m][c] = mfma16<_Float16>(a, b[c], acc[m][c]);
+        }
       }
     }
-  }
+  };
+  if (over)
+    sum(std::false_type{});
+  else
+    sum(std::true_type{});
   if (un.parts > 1) {
     floatx4* p = (floatx4*)parts + ((size_t)un.slot * 8 + wave) * (MT * 4 * 64) + lane;
 #pragma unroll
@@ -244,7 +241,7 @@ struct DxPlan {
   int mt, steps, lda;
   bool copy;
   TileSplit sp;
-  size_t off_prm, off_a, off_back, off_parts, bytes;
+  size_t off_prm, off_big, off_a, off_back, off_parts, bytes;
 };
 static DxPlan dx_plan(const W4Args& a) {
   DxPlan p;
@@ -255,6 +252,8 @@ static DxPlan dx_plan(const W4Args& a) {
   size_t at = 0;
   p.off_prm = at;
   at += align256((size_t)p.steps * 64 * (a.K / a.group) * 4);
+  p.off_big = at;
+  at += align256((size_t)p.steps * ((a.K / a.group + 31) / 32) * 4);
   p.off_a = at;
   if (p.copy) at += align256((size_t)a.N * p.lda * 2);
   p.off_back = at;
@@ -279,7 +278,7 @@ static hipError_t launch(const W4Args& a, const void* dY, const DxPlan& p, hipSt
   hipLaunchKernelGGL(kernel, dim3((unsigned)(p.sp.full + p.sp.left * p.sp.parts)), dim3(512), lds,
                      stream, p.copy ? (const _Float16*)(ws + p.off_a) : (const _Float16*)dY, p.lda,
                      back, (int)a.N, (int)a.K, (int)a.O, (const char*)a.qweight, ws + p.off_prm,
-                     (T*)a.out0, parts, p.sp);
+                     (const int*)(ws + p.off_big), (T*)a.out0, parts, p.sp);
   if (p.sp.parts > 1)
     hipLaunchKernelGGL((k_dx_join<T>), dim3((unsigned)(p.sp.left * 4 * MT)), dim3(64), 0, stream,
                        parts, back, (int)a.N, (int)a.K, (T*)a.out0, p.sp, MT);
@@ -307,7 +306,7 @@ hipError_t launch_w4_input_grad(const W4Args& a, const void* dY, hipStream_t str
   const int ng = (int)(a.K / a.group);
   hipLaunchKernelGGL(k_dx_params, dim3((unsigned)p.steps, (unsigned)((ng + 31) / 32)), dim3(256), 0,
                      stream, (const _Float16*)a.step16, (const _Float16*)a.zero16, (int)a.O, ng,
-                     (_Float16*)(ws + p.off_prm));
+                     (_Float16*)(ws + p.off_prm), (int*)(ws + p.off_big));
   if (p.copy) {
     const hipError_t e = launch_rows_to_half(dY, a.type, a.N, a.O, p.lda, ws + p.off_a,
                                              (int*)(ws + p.off_back), stream);
