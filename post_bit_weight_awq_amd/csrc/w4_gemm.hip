@@ -134,13 +134,6 @@ constexpr int kBN = 256;    // packed rows per block
 constexpr int kEpRow = 68;  // floats per token of a wavefront's 64 columns in the epilogue's LDS
 constexpr int kEpWave = 32 * kEpRow;
 
-// What the last step of a product does with its sums.
-struct Epilogue {
-  const int* back;  // a token's exponent, or NULL
-  void *y, *pre;
-  int N, O, y_type, type, act;
-};
-
 template <bool GATED, typename T>
 __device__ __forceinline__ void store_outputs(const Epilogue& e, int token, int o, int outs,
                                               float (&v)[8], const float (&u)[8], T* y) {

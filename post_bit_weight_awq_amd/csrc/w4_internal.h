@@ -43,7 +43,7 @@ struct TileCosts {
 };
 constexpr float kTileStart = 3.0f;            // a tile's first loads and its epilogue
 constexpr float kJoinStart = 4.0f;            // the second launch
-constexpr float kPartRate = 2.0e6f;           // bytes per microsecond of parts, written and read
+constexpr float kPartRate = 4.5e6f;           // bytes per microsecond of parts, written and read
 
 // Tile height and split with the least estimated time.
 inline void choose_tiles(int64_t N, int no, int steps, const TileCosts& c, int* mt_out, TileSplit* out) {
@@ -71,8 +71,11 @@ inline void choose_tiles(int64_t N, int no, int steps, const TileCosts& c, int* 
     }
   }
 }
-constexpr TileCosts kGemmCosts = {{1.2f, 1.6f, 2.0f, 2.5f}};
-constexpr TileCosts kDxCosts = {{0.6f, 0.8f, 1.0f, 1.2f}};
+// Measured with one tile per unit on 512 x 4096 x 4096 and, for the products,
+// 1024 x 13824 x 5120: 128 columns a step for the products (w4_gemm.hip), 64
+// packed rows a step for the input gradient (w4_input_grad.hip).
+constexpr TileCosts kGemmCosts = {{1.5f, 2.1f, 2.55f, 3.1f}};
+constexpr TileCosts kDxCosts = {{0.9f, 1.15f, 1.35f, 1.65f}};
 
 struct SplitUnit {
   int t, o, s0, s1, parts, slot;  // steps s0 .. s1 - 1
@@ -107,6 +110,13 @@ __device__ __forceinline__ void join_parts(const float* parts, const TileSplit& 
     for (int i = 0; i < 8; ++i) v[i >> 2][i & 3] += p[i * 64];
   }
 }
+
+// What the last step of a product does with its sums.
+struct Epilogue {
+  const int* back;  // a token's exponent, or NULL
+  void *y, *pre;
+  int N, O, y_type, type, act;
+};
 
 // Direct loads to LDS: 16 (or 4) bytes per lane from base + off to l + 16 (4)
 // times the lane.
