@@ -14,7 +14,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libawq_mi355x.so")
 SOURCES = ["act_stats.hip", "search.hip", "search_grid.hip", "search_gemm.hip", "pack.hip",
            "w4a16.hip", "w4_ops.hip", "w4_skinny.hip", "w4_gemm.hip", "w4_input_grad.hip",
-           "w4_param_grad.hip", "fold.hip", "select.hip", "awq_api.hip"]
+           "w4_param_grad.hip", "w4_prepare.hip",
+           "fold.hip", "select.hip", "awq_api.hip"]
 # measured-peak references used by bench.py only (not part of the search library)
 CALIB_LIB = os.path.join(PKG, "libawq_calib.so")
 CALIB_SOURCES = ["calib.hip"]

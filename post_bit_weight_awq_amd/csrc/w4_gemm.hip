@@ -16,119 +16,10 @@
 //   * A group whose step is 0 leaves the unit as it is and takes codes and
 //     zero as 0.
 // bf16 activations are first brought to fp16 by a power of two per row
-// (k_rows_to_half), which the epilogue takes back.
-#include "awq_internal.h"
-#include "w4_device.h"
+// (w4_prepare.hip), which the epilogue takes back.
 #include "w4_internal.h"
 
 namespace awq {
-
-// (step, -zero 2^-9) as fp16 pairs by group: prm[g * O + row].
-__global__ void __launch_bounds__(256)
-k_w4_params(const uint16_t* __restrict__ step16, const uint16_t* __restrict__ zero16, int O, int ng,
-            uint32_t* __restrict__ prm) {
-  __shared__ uint32_t tile[32][33];
-  const int r0 = blockIdx.x * 32, g0 = blockIdx.y * 32;
-  const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
-#pragma unroll
-  for (int i = 0; i < 32; i += 8) {
-    const int row = r0 + r + i, g = g0 + c;
-    if (row < O && g < ng) {
-      const size_t at = (size_t)row * ng + g;
-      const uint32_t nz = neg_zero_pair(__builtin_bit_cast(_Float16, zero16[at]));
-      tile[r + i][c] = (uint32_t)step16[at] | (nz & 0xffff0000u);
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 32; i += 8) {
-    const int row = r0 + c, g = g0 + r + i;
-    if (row < O && g < ng) prm[(size_t)g * O + row] = tile[c][r + i];
-  }
-}
-
-// Rows padded to ld_out with zeros; fp16 rows as they are, back = 0.  Rows of
-// bf16 become fp16 times 2^e, e chosen by the row's largest finite
-// magnitude (which lands in [2^14, 2^15)); back[row] = 2^-e as an exponent.
-// Values down to 2^-32 of the largest stay exact, smaller ones are rounded at
-// 2^-40 of it.
-template <bool BF16>
-__global__ void __launch_bounds__(256)
-k_rows_to_half(const uint16_t* __restrict__ in, int cols, int ld_out, _Float16* __restrict__ out,
-               int* __restrict__ back) {
-  __shared__ uint32_t red[4];
-  const size_t row = blockIdx.x;
-  const uint16_t* src = in + row * cols;
-  const bool vec = (cols & 7) == 0;
-  _Float16* dst = out + row * ld_out;
-  for (int c = cols + threadIdx.x; c < ld_out; c += 256) dst[c] = (_Float16)0.0f;
-  if constexpr (!BF16) {
-    if (vec)
-      for (int c = threadIdx.x * 8; c < cols; c += 2048) *(uint4*)(dst + c) = *(const uint4*)(src + c);
-    else
-      for (int c = threadIdx.x; c < cols; c += 256) dst[c] = __builtin_bit_cast(_Float16, src[c]);
-    if (threadIdx.x == 0) back[row] = 0;
-    return;
-  }
-  uint32_t top = 0;  // largest finite magnitude, as bits
-  auto look = [&](uint32_t b) {
-    b &= 0x7fffu;
-    if (b < 0x7f80u && b > top) top = b;
-  };
-  if (vec) {
-    for (int c = threadIdx.x * 8; c < cols; c += 2048) {
-      const uint4 v = *(const uint4*)(src + c);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        look(w[e]);
-        look(w[e] >> 16);
-      }
-    }
-  } else {
-    for (int c = threadIdx.x; c < cols; c += 256) look(src[c]);
-  }
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) {
-    const uint32_t o = (uint32_t)__shfl_xor((int)top, d, 64);
-    top = o > top ? o : top;
-  }
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
-  __syncthreads();
-  top = max(max(red[0], red[1]), max(red[2], red[3]));
-  // the largest is in [2^(x - 1), 2^x): x from frexp, also for subnormals
-  int x = 0;
-  if (top) (void)frexpf(__uint_as_float(top << 16), &x);
-  const int e = top ? 15 - x : 0;
-  if (threadIdx.x == 0) back[row] = -e;
-  auto half = [&](uint32_t b) -> uint32_t {
-    return __builtin_bit_cast(uint16_t, (_Float16)ldexpf(__uint_as_float(b << 16), e));
-  };
-  if (vec) {
-    for (int c = threadIdx.x * 8; c < cols; c += 2048) {
-      const uint4 v = *(const uint4*)(src + c);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      uint32_t o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = half(w[i] & 0xffffu) | (half(w[i] >> 16) << 16);
-      *(uint4*)(dst + c) = make_uint4(o[0], o[1], o[2], o[3]);
-    }
-  } else {
-    for (int c = threadIdx.x; c < cols; c += 256)
-      dst[c] = __builtin_bit_cast(_Float16, (uint16_t)half(src[c]));
-  }
-}
-
-hipError_t launch_rows_to_half(const void* in, int type, int64_t rows, int64_t cols, int64_t ld_out, void* out,
-                               int* back, hipStream_t stream) {
-  if (type == kBF16)
-    hipLaunchKernelGGL(k_rows_to_half<true>, dim3((unsigned)rows), dim3(256), 0, stream,
-                       (const uint16_t*)in, (int)cols, (int)ld_out, (_Float16*)out, back);
-  else
-    hipLaunchKernelGGL(k_rows_to_half<false>, dim3((unsigned)rows), dim3(256), 0, stream,
-                       (const uint16_t*)in, (int)cols, (int)ld_out, (_Float16*)out, back);
-  return hipGetLastError();
-}
 
 constexpr int kBN = 256;    // packed rows per block
 constexpr int kEpRow = 68;  // floats per token of a wavefront's 64 columns in the epilogue's LDS
@@ -405,7 +296,11 @@ struct GemmPlan {
 static GemmPlan gemm_plan(W4Op op, const W4Args& a) {
   GemmPlan p;
   const int64_t outs = op == kOpGated ? a.O / 2 : a.O, per = op == kOpGated ? kBN / 2 : kBN;
-  choose_tiles(a.N, (int)((outs + per - 1) / per), (int)(a.K / 128), kGemmCosts, &p.mt, &p.sp);
+  // groups of 64 and 32 change the unit two and four times per 128 columns:
+  // a step takes 1.2 and 1.45 times as long (512 x 4096 x 4096)
+  const float scale = a.group == 128 ? 1.0f : a.group == 64 ? 1.2f : 1.45f;
+  choose_tiles(a.N, (int)((outs + per - 1) / per), (int)(a.K / 128), kGemmCosts, scale, &p.mt,
+               &p.sp);
   size_t at = 0;
   p.off_prm = at;
   at += align256((size_t)a.O * (a.K / a.group) * 4);
@@ -461,15 +356,18 @@ static hipError_t by_group(const W4Args& a, const GemmPlan& p, hipStream_t strea
 hipError_t launch_w4_gemm(W4Op op, const W4Args& a, hipStream_t stream) {
   const GemmPlan p = gemm_plan(op, a);
   char* ws = (char*)a.ws;
-  const int ng = (int)(a.K / a.group);
-  hipLaunchKernelGGL(k_w4_params, dim3((unsigned)((a.O + 31) / 32), (unsigned)((ng + 31) / 32)),
-                     dim3(256), 0, stream, (const uint16_t*)a.step16, (const uint16_t*)a.zero16,
-                     (int)a.O, ng, (uint32_t*)(ws + p.off_prm));
-  if (a.type == kBF16) {
-    const hipError_t e = launch_rows_to_half(a.in0, a.type, a.N, a.K, a.K, ws + p.off_a,
-                                             (int*)(ws + p.off_back), stream);
-    if (e != hipSuccess) return e;
-  }
+  Prepare q{};
+  q.step16 = (const _Float16*)a.step16;
+  q.zero16 = (const _Float16*)a.zero16;
+  q.O = (int)a.O;
+  q.ng = (int)(a.K / a.group);
+  q.prm = ws + p.off_prm;
+  q.in0 = a.in0;
+  q.cols = q.ld_out = (int)a.K;
+  q.out = ws + p.off_a;
+  q.back = (int*)(ws + p.off_back);
+  const hipError_t e = launch_w4_prepare(q, a.type, 1, false, a.type == kBF16 ? a.N : 0, stream);
+  if (e != hipSuccess) return e;
   return op == kOpGated ? by_group<true>(a, p, stream) : by_group<false>(a, p, stream);
 }
 

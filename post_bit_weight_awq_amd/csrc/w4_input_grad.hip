@@ -18,44 +18,13 @@
 //     second pair swaps its 64-byte halves: the 64 words of a read then lie
 //     in 64 banks.
 //   * dY in bf16, or of a width that is no multiple of 64, is copied to fp16
-//     rows of a padded width first (k_rows_to_half; zeros behind the row's
-//     end meet weights of 0).
+//     rows of a padded width first (w4_prepare.hip; zeros behind the row's end
+//     meet weights of 0).
 #include <type_traits>
 
 #include "w4_internal.h"
 
 namespace awq {
-
-// Group parameters by steps of 64 packed rows: prm[(s * ng + g) * 128 + ..] as
-// 64 halfs -zero 2^-9 and 64 halfs of the step; 0 for rows past the end.
-// big[s * gridDim.y + block of 32 groups]: whether a step is 128 or more.
-__global__ void __launch_bounds__(256)
-k_dx_params(const _Float16* __restrict__ step16, const _Float16* __restrict__ zero16, int O, int ng,
-            _Float16* __restrict__ prm, int* __restrict__ big) {
-  __shared__ uint32_t tile[64][33];
-  int over = 0;
-  const int o0 = blockIdx.x * 64, g0 = blockIdx.y * 32;
-  for (int e = threadIdx.x; e < 64 * 32; e += 256) {
-    const int r = e >> 5, c = e & 31;
-    uint32_t v = 0;
-    if (o0 + r < O && g0 + c < ng) {
-      const size_t at = (size_t)(o0 + r) * ng + g0 + c;
-      v = (neg_zero_pair(zero16[at]) & 0xffffu) |
-          ((uint32_t)__builtin_bit_cast(uint16_t, step16[at]) << 16);
-      over |= (v & 0x7fff0000u) >= 0x58000000u;  // 128
-    }
-    tile[r][c] = v;
-  }
-  over = __syncthreads_or(over);
-  if (threadIdx.x == 0) big[blockIdx.x * gridDim.y + blockIdx.y] = over;
-  for (int e = threadIdx.x; e < 64 * 32; e += 256) {
-    const int c = e >> 6, r = e & 63;
-    if (g0 + c >= ng) continue;
-    _Float16* p = prm + ((size_t)blockIdx.x * ng + g0 + c) * 128;
-    p[r] = __builtin_bit_cast(_Float16, (uint16_t)(tile[r][c] & 0xffffu));
-    p[64 + r] = __builtin_bit_cast(_Float16, (uint16_t)(tile[r][c] >> 16));
-  }
-}
 
 constexpr int kStages = 3;
 template <int MT>
@@ -248,7 +217,7 @@ static DxPlan dx_plan(const W4Args& a) {
   p.steps = (int)((a.O + 63) / 64);
   p.copy = a.type == kBF16 || a.O % 64;
   p.lda = p.copy ? p.steps * 64 : (int)a.O;
-  choose_tiles(a.N, (int)((a.K + 255) / 256), p.steps, kDxCosts, &p.mt, &p.sp);
+  choose_tiles(a.N, (int)((a.K + 255) / 256), p.steps, kDxCosts, 1.0f, &p.mt, &p.sp);
   size_t at = 0;
   p.off_prm = at;
   at += align256((size_t)p.steps * 64 * (a.K / a.group) * 4);
@@ -300,18 +269,30 @@ static hipError_t by_group(const W4Args& a, const void* dY, const DxPlan& p, hip
   return by_tokens<T, 32>(a, dY, p, stream);
 }
 
-hipError_t launch_w4_input_grad(const W4Args& a, const void* dY, hipStream_t stream) {
+// Of a gated block the preparing launch forms dpre on the way.
+hipError_t launch_w4_input_grad(W4Op op, const W4Args& a, hipStream_t stream) {
+  const bool gated = op == kOpGatedBackward;
   const DxPlan p = dx_plan(a);
   char* ws = (char*)a.ws;
-  const int ng = (int)(a.K / a.group);
-  hipLaunchKernelGGL(k_dx_params, dim3((unsigned)p.steps, (unsigned)((ng + 31) / 32)), dim3(256), 0,
-                     stream, (const _Float16*)a.step16, (const _Float16*)a.zero16, (int)a.O, ng,
-                     (_Float16*)(ws + p.off_prm), (int*)(ws + p.off_big));
-  if (p.copy) {
-    const hipError_t e = launch_rows_to_half(dY, a.type, a.N, a.O, p.lda, ws + p.off_a,
-                                             (int*)(ws + p.off_back), stream);
-    if (e != hipSuccess) return e;
-  }
+  Prepare q{};
+  q.step16 = (const _Float16*)a.step16;
+  q.zero16 = (const _Float16*)a.zero16;
+  q.O = (int)a.O;
+  q.ng = (int)(a.K / a.group);
+  q.prm = ws + p.off_prm;
+  q.big = (int*)(ws + p.off_big);
+  q.in0 = a.in0;
+  q.in1 = a.in1;
+  q.dpre = a.out1;
+  q.cols = (int)a.O;
+  q.ld_out = p.lda;
+  q.act = a.act;
+  q.out = p.copy ? ws + p.off_a : nullptr;
+  q.back = (int*)(ws + p.off_back);
+  const hipError_t e =
+      launch_w4_prepare(q, a.type, 2, gated, p.copy || gated ? a.N : 0, stream);
+  if (e != hipSuccess) return e;
+  const void* dY = gated ? a.out1 : a.in0;
   return a.type == kF16 ? by_group<_Float16>(a, dY, p, stream) : by_group<__bf16>(a, dY, p, stream);
 }
 

@@ -43,23 +43,25 @@ struct TileCosts {
 };
 constexpr float kTileStart = 3.0f;            // a tile's first loads and its epilogue
 constexpr float kJoinStart = 4.0f;            // the second launch
-constexpr float kPartRate = 4.5e6f;           // bytes per microsecond of parts, written and read
+constexpr float kPartRate = 6.0e6f;           // bytes per microsecond of parts, written and read
 
-// Tile height and split with the least estimated time.
-inline void choose_tiles(int64_t N, int no, int steps, const TileCosts& c, int* mt_out, TileSplit* out) {
+// Tile height and split with the least estimated time; `scale` multiplies the
+// steps' cost.
+inline void choose_tiles(int64_t N, int no, int steps, const TileCosts& c, float scale, int* mt_out,
+                         TileSplit* out) {
   float best = 0.0f;
   for (int i = 0; i < 4; ++i) {
     const int mt = 2 * (i + 1);
     const int nt = (int)((N + 32 * mt - 1) / (32 * mt));
     const int total = nt * no, left = total % kCUs;
-    const float tile = c.step[i] * steps + kTileStart;
+    const float step = scale * c.step[i], tile = step * steps + kTileStart;
     for (int parts = 1; parts <= 32 && parts <= steps; ++parts) {
       if (parts > 1 && left == 0) break;
       const int whole = total - left;
       float t = (float)(whole / kCUs) * tile;
       if (left) {
         const int rounds = (left * parts + kCUs - 1) / kCUs;
-        t += (float)rounds * (c.step[i] * (float)((steps + parts - 1) / parts) + kTileStart);
+        t += (float)rounds * (step * (float)((steps + parts - 1) / parts) + kTileStart);
         if (parts > 1) t += kJoinStart + 2.0f * left * parts * mt * 32768.0f / kPartRate;
       }
       if (best == 0.0f || t < best) {
@@ -163,14 +165,32 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8], int n, bool al
   }
 }
 
-hipError_t launch_rows_to_half(const void* in, int type, int64_t rows, int64_t cols, int64_t ld_out, void* out,
-                               int* back, hipStream_t stream);
+// One launch before the tiled kernels (w4_prepare.hip).
+struct Prepare {
+  const _Float16 *step16, *zero16;
+  int O, ng;
+  void* prm;
+  int* big;  // input gradient
+  // rows: cols values of in0 (gated: cols / 2 of dH in in0 and cols of pre in
+  // in1, giving dpre) to out, ld_out apart; out may be NULL with gated
+  const void *in0, *in1;
+  void* dpre;
+  int cols, ld_out, act;
+  void* out;
+  int* back;
+  int param_blocks;
+};
+// params: 0 none, 1 the products', 2 the input gradient's; gated with 2 alone
+hipError_t launch_w4_prepare(const Prepare& p, int type, int params, bool gated, int64_t rows,
+                             hipStream_t stream);
+
+// linear and gated (w4_gemm.hip), input gradient and gated backward
+// (w4_input_grad.hip), parameter gradients (w4_param_grad.hip)
 size_t w4_gemm_workspace(W4Op op, const W4Args& a);
+hipError_t launch_w4_gemm(W4Op op, const W4Args& a, hipStream_t stream);
 size_t w4_input_grad_workspace(const W4Args& a);
-// dX of a.out0 from dY
-hipError_t launch_w4_input_grad(const W4Args& a, const void* dY, hipStream_t stream);
+hipError_t launch_w4_input_grad(W4Op op, const W4Args& a, hipStream_t stream);
 size_t w4_param_grad_workspace(const W4Args& a);
 hipError_t launch_w4_param_grad(const W4Args& a, hipStream_t stream);
-hipError_t launch_w4_gemm(W4Op op, const W4Args& a, hipStream_t stream);
 
 }  // namespace awq

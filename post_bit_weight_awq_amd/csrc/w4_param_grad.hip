@@ -229,7 +229,7 @@ struct PgPlan {
   bool copy;
   int ldy;
   TileSplit sp;
-  size_t off_y, off_back, off_parts, bytes;
+  size_t off_y, off_parts, bytes;
 };
 static PgPlan pg_plan(const W4Args& a) {
   PgPlan p;
@@ -248,8 +248,6 @@ static PgPlan pg_plan(const W4Args& a) {
   size_t at = 0;
   p.off_y = at;
   if (p.copy) at += align256((size_t)a.N * p.ldy * 2);
-  p.off_back = at;
-  if (p.copy) at += align256((size_t)a.N * 4);
   p.off_parts = at;
   if (p.sp.parts > 1) at += (size_t)p.sp.left * p.sp.parts * 256 * (256 / a.group) * 8;
   p.bytes = at;
@@ -289,8 +287,12 @@ hipError_t launch_w4_param_grad(const W4Args& a, hipStream_t stream) {
   char* ws = (char*)a.ws;
   if (p.copy) {
     // the bits as they are, rows padded to whole 16-byte pieces
-    const hipError_t e = launch_rows_to_half(a.in0, kF16, a.N, a.O, p.ldy, ws + p.off_y,
-                                             (int*)(ws + p.off_back), stream);
+    Prepare q{};
+    q.in0 = a.in0;
+    q.cols = (int)a.O;
+    q.ld_out = p.ldy;
+    q.out = ws + p.off_y;
+    const hipError_t e = launch_w4_prepare(q, kF16, 0, false, a.N, stream);
     if (e != hipSuccess) return e;
   }
   return a.type == kF16 ? by_group<_Float16>(a, p, stream) : by_group<__bf16>(a, p, stream);
