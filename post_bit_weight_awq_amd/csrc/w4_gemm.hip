@@ -209,10 +209,6 @@ k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
       else
         wait_vm<0>();
       __syncthreads();
-      if (kb + 1 < kend) {
-        load_a(s + 2);
-        if (h == 0) load_w(kb + 1);
-      }
       const char* ta = smem + (s % 3) * L::kA + (wm * MT * 16 + r16) * 128;
 #pragma unroll
       for (int j2 = 0; j2 < 2; ++j2) {
@@ -248,6 +244,11 @@ k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
               for (int r = 0; r < 4; ++r) acc[m][n][r] *= ratio[n];
             acc[m][n] = mfma16<_Float16>(a, b[n], acc[m][n]);
           }
+        }
+        // between a half's two sets the requests delay the MFMAs least
+        if (j2 == 0 && kb + 1 < kend) {
+          load_a(s + 2);
+          if (h == 0) load_w(kb + 1);
         }
       }
     }

@@ -4,7 +4,7 @@
 // Block tile 32 MT tokens x 256 columns, eight wavefronts as 2 (tokens) x 4
 // (columns), each 16 MT x 64 as MT x 4 tiles of v_mfma_f32_16x16x32_f16, 64
 // packed rows a step.  dY, the codes and the group parameters move to LDS by
-// direct loads, three stages, two steps ahead.
+// direct loads, two (codes: three) steps ahead.
 //   * An MFMA needs eight consecutive rows of one column per lane, while a
 //     word holds eight columns of one row.  So lane l reads the word l % 16 of
 //     each of its eight rows (8 (l / 16) ..), pairs the rows' halves with one
@@ -26,13 +26,14 @@
 
 namespace awq {
 
-constexpr int kStages = 3;
+// Three stages of dY, four of codes and parameters.
 template <int MT>
 struct DxLds {
   static constexpr int kA = 32 * MT * 128;  // bytes of dY per stage
   static constexpr int kC = 64 * 128;       // codes
   static constexpr int kP = 2048;           // group parameters
-  static constexpr int kStage = kA + kC + kP;
+  static constexpr int kOffC = 3 * kA, kOffP = kOffC + 4 * kC;
+  static constexpr int kBytes = kOffP + 4 * kP;
 };
 
 // Values of one token's four neighbouring columns per lane, tile by tile.
@@ -93,16 +94,19 @@ k_w4_dx(const _Float16* __restrict__ A, int lda, const int* __restrict__ back, i
   const int pg = min(k0 / GROUP + pbyte / 256, ng - 1);
   const uint32_t op = (uint32_t)pg * 256u + (pbyte & 255);
 
-  auto load = [&](int s) {
-    const uint32_t l = (uint32_t)(uintptr_t)smem + (uint32_t)(s % kStages) * L::kStage;
+  const uint32_t lds = (uint32_t)(uintptr_t)smem;
+  auto load_a = [&](int s) {
 #pragma unroll
     for (int i = 0; i < AL; ++i)
-      dma16(a0 + s * 128, oa[i], l + (wave * AL + i) * 1024);
+      dma16(a0 + s * 128, oa[i], lds + (s % 3) * L::kA + (wave * AL + i) * 1024);
+  };
+  auto load_c = [&](int s) {
     // each lane's row, the last one where the step passes the end
     const int row = min(64 * s + crow, O - 1);
     dma16(qw + (size_t)(64 * s) * (K / 2), (uint32_t)(row - 64 * s) * (uint32_t)(K / 2) + oc,
-          l + L::kA + wave * 1024);
-    if (lane < PB / 4) dma4(prm + (size_t)s * ng * 256, op, l + L::kA + L::kC + wave * PB);
+          lds + L::kOffC + (s & 3) * L::kC + wave * 1024);
+    if (lane < PB / 4)
+      dma4(prm + (size_t)s * ng * 256, op, lds + L::kOffP + (s & 3) * L::kP + wave * PB);
   };
 
   floatx4 acc[MT][4];
@@ -114,63 +118,93 @@ k_w4_dx(const _Float16* __restrict__ A, int lda, const int* __restrict__ back, i
   const int gl = (128 * wb + 8 * r16) / GROUP;  // the lane's group among the block's
   const uint32_t sel = half ? 0x07060302u : 0x05040100u;
 
-  load(un.s0);
-  if (un.s0 + 1 < un.s1) load(un.s0 + 1);
+  const int send = un.s1;
+  load_c(un.s0);
+  load_a(un.s0);
+  if (un.s0 + 1 < send) {
+    load_c(un.s0 + 1);
+    load_a(un.s0 + 1);
+  }
+  if (un.s0 + 2 < send) load_c(un.s0 + 2);
   // steps of 128 and more among the block's: 512 step leaves fp16's range, so
   // the factor goes to the differences, one operation more
   int over = 0;
   const int gb = (ng + 31) / 32, gb0 = k0 / GROUP / 32, gb1 = min(k0 + 255, K - 1) / GROUP / 32;
   for (int s = un.s0 + tid; s < un.s1; s += 512) over |= big[s * gb + gb0] | big[s * gb + gb1];
   over = __syncthreads_or(over);
+  // Half a step (32 packed rows) at a time; while one half multiplies, the
+  // next one's codes are read and converted a row pair after each few
+  // fragments, so that the conversion fills the gaps between MFMAs.
   auto sum = [&](auto plain) {
-    for (int s = un.s0; s < un.s1; ++s) {
-      // the step's loads have landed (the next step's may be in flight), and
-      // no wavefront still reads the stage that is loaded next
-      if (s + 1 < un.s1)
+    uint32_t w[8];
+    uint4 zv, sv, b[4];
+    uint32_t bn[4][4];
+    auto read_codes = [&](int s, int ch) {
+      const char* pc = smem + L::kOffC + (s & 3) * L::kC + cbase + ch * 4096;
+      const char* pp = smem + L::kOffP + (s & 3) * L::kP + gl * 256 + 16 * q4 + ch * 64;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = *(const uint32_t*)(pc + i * 512);
+      zv = *(const uint4*)pp;
+      sv = *(const uint4*)(pp + 128);
+    };
+    // rows 2 p and 2 p + 1 of the lane's eight: both halves of a dword in each
+    // of the four tiles' fragments
+    auto convert = [&](int p) {
+      const uint32_t t = __builtin_amdgcn_perm(w[2 * p + 1], w[2 * p], sel);
+      const uint32_t t8 = t >> 8;
+      const half2v z = __builtin_bit_cast(half2v, word_of(zv, p));
+      const half2v s1 = __builtin_bit_cast(half2v, word_of(sv, p));
+      const half2v m0 = {(_Float16)32768.0f, (_Float16)32768.0f};
+      const half2v m1 = {(_Float16)2048.0f, (_Float16)2048.0f};
+      const half2v k512 = {(_Float16)512.0f, (_Float16)512.0f};
+      const half2v s5 = s1 * k512;
+      const uint32_t n[4] = {t & 0x000F000Fu, t & 0x00F000F0u, t8 & 0x000F000Fu, t8 & 0x00F000F0u};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const half2v d =
+            __builtin_elementwise_fma(__builtin_bit_cast(half2v, n[c]), c & 1 ? m1 : m0, z);
+        bn[c][p] = __builtin_bit_cast(uint32_t, plain ? d * s5 : (d * k512) * s1);
+      }
+    };
+    auto take = [&]() {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) b[c] = make_uint4(bn[c][0], bn[c][1], bn[c][2], bn[c][3]);
+    };
+    wait_vm<0>();
+    __syncthreads();
+    read_codes(un.s0, 0);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) convert(p);
+    take();
+    for (int s = un.s0; s < send; ++s) {
+      // the step's dY and the next step's codes have landed (what the last
+      // step requested may be in flight), and no wavefront still reads the
+      // stages that are requested next
+      if (s + 2 < send && s > un.s0)
         wait_vm<AL + 2>();
       else
         wait_vm<0>();
       __syncthreads();
-      if (s + 2 < un.s1) load(s + 2);
-      const char* st = smem + (s % kStages) * L::kStage;
-      const char* pc = st + L::kA + cbase;
-      const char* pp = st + L::kA + L::kC + gl * 256 + 16 * q4;
 #pragma unroll
       for (int ch = 0; ch < 2; ++ch) {
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = *(const uint32_t*)(pc + ch * 4096 + i * 512);
-        const uint4 zv = *(const uint4*)(pp + ch * 64);
-        const uint4 sv = *(const uint4*)(pp + ch * 64 + 128);
-        uint32_t bw[4][4];
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          const uint32_t t = __builtin_amdgcn_perm(w[2 * p + 1], w[2 * p], sel);
-          const uint32_t t8 = t >> 8;
-          const half2v z = __builtin_bit_cast(half2v, word_of(zv, p));
-          const half2v s1 = __builtin_bit_cast(half2v, word_of(sv, p));
-          const half2v m0 = {(_Float16)32768.0f, (_Float16)32768.0f};
-          const half2v m1 = {(_Float16)2048.0f, (_Float16)2048.0f};
-          const half2v k512 = {(_Float16)512.0f, (_Float16)512.0f};
-          const half2v s5 = s1 * k512;
-          const uint32_t n[4] = {t & 0x000F000Fu, t & 0x00F000F0u, t8 & 0x000F000Fu,
-                                 t8 & 0x00F000F0u};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const half2v d = __builtin_elementwise_fma(__builtin_bit_cast(half2v, n[c]),
-                                                       c & 1 ? m1 : m0, z);
-            bw[c][p] = __builtin_bit_cast(uint32_t, plain ? d * s5 : (d * k512) * s1);
-          }
-        }
-        uint4 b[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) b[c] = make_uint4(bw[c][0], bw[c][1], bw[c][2], bw[c][3]);
-        const char* ta = st + (wm * MT * 16 + r16) * 128 + 16 * ((4 * ch + q4) ^ (r16 & 7));
+        const char* ta = smem + (s % 3) * L::kA + (wm * MT * 16 + r16) * 128 +
+                         16 * ((4 * ch + q4) ^ (r16 & 7));
+        // past the end the stage holds old values: read, not used
+        read_codes(s + ch, 1 - ch);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           const uint4 a = *(const uint4*)(ta + m * 2048);
 #pragma unroll
           for (int c = 0; c < 4; ++c) acc[m][c] = mfma16<_Float16>(a, b[c], acc[m][c]);
+#pragma unroll
+          for (int p = 0; p < 4; ++p)
+            if (m == 1 + p * (MT - 1) / 4) convert(p);
+        }
+        take();
+        // between the halves the requests delay the MFMAs least
+        if (ch == 0) {
+          if (s + 3 < send) load_c(s + 3);
+          if (s + 2 < send) load_a(s + 2);
         }
       }
     }
@@ -237,7 +271,7 @@ size_t w4_input_grad_workspace(const W4Args& a) { return dx_plan(a).bytes; }
 template <typename T, int GROUP, int MT>
 static hipError_t launch(const W4Args& a, const void* dY, const DxPlan& p, hipStream_t stream) {
   auto* kernel = &k_w4_dx<T, GROUP, MT>;
-  const int lds = kStages * DxLds<MT>::kStage;
+  const int lds = DxLds<MT>::kBytes;
   hipError_t e =
       hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;

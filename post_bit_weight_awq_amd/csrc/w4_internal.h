@@ -106,10 +106,19 @@ __device__ __forceinline__ void join_parts(const float* parts, const TileSplit& 
                      mp * 8 * 64 + lane;
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i >> 2][i & 3] = p[i * 64];
-  for (int k = 1; k < sp.parts; ++k) {
-    p += 8 * tile;
+  // four parts' loads in flight at a time (past the end the last part's,
+  // which are not added)
+  for (int k = 1; k < sp.parts; k += 4) {
+    floatx4 t[4][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i >> 2][i & 3] += p[i * 64];
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[j][i] = p[(size_t)min(k + j, sp.parts - 1) * 8 * tile + i * 64];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (k + j < sp.parts)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i >> 2][i & 3] += t[j][i];
   }
 }
 

@@ -37,7 +37,9 @@ __device__ __forceinline__ void gradient_params(const Prepare& a, int block) {
   __shared__ uint32_t tile[64][33];
   const int gb = (a.ng + 31) / 32, s = block / gb, o0 = s * 64, g0 = block % gb * 32;
   int over = 0;
-  for (int e = threadIdx.x; e < 64 * 32; e += 256) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int e = threadIdx.x + 256 * i;
     const int r = e >> 5, c = e & 31;
     uint32_t v = 0;
     if (o0 + r < a.O && g0 + c < a.ng) {
@@ -50,7 +52,9 @@ __device__ __forceinline__ void gradient_params(const Prepare& a, int block) {
   }
   over = __syncthreads_or(over);
   if (threadIdx.x == 0) a.big[block] = over;
-  for (int e = threadIdx.x; e < 64 * 32; e += 256) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int e = threadIdx.x + 256 * i;
     const int c = e >> 6, r = e & 63;
     if (g0 + c >= a.ng) continue;
     _Float16* p = (_Float16*)a.prm + ((size_t)s * a.ng + g0 + c) * 128;
