@@ -58,9 +58,8 @@ __device__ __forceinline__ uint32_t neg_zero_pair(_Float16 z) {
 constexpr uint32_t kNibbleFactors = 0x68007800u;
 
 // The eight codes of a word, in column order, as (q - z) 2^-9: ten operations.
-// With factors and zero 0 they all become 0.
-__device__ __forceinline__ uint4 dequant_word(uint32_t w, uint32_t nz,
-                                              uint32_t factors = kNibbleFactors) {
+// With factors and zero 0 they all become 0.  The first or last four alone:
+__device__ __forceinline__ uint2 dequant_half(uint32_t w, uint32_t nz, uint32_t factors, int half) {
   const uint32_t lo = w & 0x0F0F0F0Fu, hi = w & 0xF0F0F0F0u;
   const half2v m = __builtin_bit_cast(half2v, factors);
   const half2v z = __builtin_bit_cast(half2v, nz);
@@ -68,7 +67,13 @@ __device__ __forceinline__ uint4 dequant_word(uint32_t w, uint32_t nz,
     const half2v c = __builtin_bit_cast(half2v, __builtin_amdgcn_perm(hi, lo, sel));
     return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(c, m, z));
   };
-  return make_uint4(pair(0x0c040c00u), pair(0x0c050c01u), pair(0x0c060c02u), pair(0x0c070c03u));
+  return half ? make_uint2(pair(0x0c060c02u), pair(0x0c070c03u))
+              : make_uint2(pair(0x0c040c00u), pair(0x0c050c01u));
+}
+__device__ __forceinline__ uint4 dequant_word(uint32_t w, uint32_t nz,
+                                              uint32_t factors = kNibbleFactors) {
+  const uint2 a = dequant_half(w, nz, factors, 0), b = dequant_half(w, nz, factors, 1);
+  return make_uint4(a.x, a.y, b.x, b.y);
 }
 
 // Words of four lane groups of 16: word j of group q becomes word q of group

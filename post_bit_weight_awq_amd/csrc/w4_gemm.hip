@@ -100,8 +100,8 @@ struct GemmLds {
   static constexpr int kA = 32 * MT * 128;            // 64 columns of the activations
   static constexpr int kC = kBN * 64;                 // 128 columns of codes
   static constexpr int kP = kBN * 4 * (128 / GROUP);  // their group parameters
-  static constexpr int kOffC = 3 * kA, kOffP = kOffC + 2 * kC;
-  static constexpr int kMain = kOffP + 2 * kP;
+  static constexpr int kOffC = 3 * kA, kOffP = kOffC + 3 * kC;
+  static constexpr int kMain = kOffP + 3 * kP;
   static constexpr int kBytes = kMain > 8 * kEpWave * 4 ? kMain : 8 * kEpWave * 4;
 };
 
@@ -167,9 +167,9 @@ k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
   auto load_w = [&](int kb) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      dma16(c0[i] + 64 * kb, oc[i], lds + L::kOffC + (kb & 1) * L::kC + (2 * wave + i) * 1024);
+      dma16(c0[i] + 64 * kb, oc[i], lds + L::kOffC + (kb % 3) * L::kC + (2 * wave + i) * 1024);
     const char* p = prm + (size_t)kb * GPB * O * 4;
-    const uint32_t l = lds + L::kOffP + (kb & 1) * L::kP;
+    const uint32_t l = lds + L::kOffP + (kb % 3) * L::kP;
     if (GPB == 1) {
       if (lane < 32) dma4(p, op[0], l + wave * 128);
     } else {
@@ -186,54 +186,74 @@ k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[m][n] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  uint32_t nz[4], factors[4];
-  float ratio[4];
+  // One set of 32 columns at a time; while set j multiplies, the next one's
+  // codes (its group's parameters where it begins one) are read and converted
+  // after each few fragments, so that the conversion fills the gaps between
+  // MFMAs.
+  uint4 b[4];
+  uint32_t w[4], pv[4], nz[4], factors[4];
+  float ratio[4], next_ratio[4];
+  auto read_codes = [&](int kb, int j) {
+    const char* pc = smem + L::kOffC + (kb % 3) * L::kC + (64 * wn + r16) * 64 + 4 * q4;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) w[n] = *(const uint32_t*)(pc + n * 1024 + 16 * (j ^ (r16 >> 2)));
+    const char* pp = smem + L::kOffP + (kb % 3) * L::kP + (64 * wn + r16) * 4;
+    if (j % JG == 0)
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        pv[n] = *(const uint32_t*)(pp + (j / JG) * (kBN * 4) + n * 64);
+  };
+  // of tile column n; `more` false: behind the last set the unit stays
+  auto take_params = [&](int n, bool more) {
+    const bool none = (pv[n] & 0x7fffu) == 0;
+    nz[n] = none ? 0 : (pv[n] >> 16) | (pv[n] & 0xffff0000u);
+    factors[n] = none ? 0 : kNibbleFactors;
+    const float st = none || !more ? unit[n] : f16_lo(pv[n]);
+    // 1 / st to the last bit by one Newton step
+    const float r = __builtin_amdgcn_rcpf(st);
+    next_ratio[n] = unit[n] * fmaf(fmaf(-st, r, 1.0f), r, r);
+    unit[n] = st;
+  };
   const int kend = un.s1;
-  load_a(2 * un.s0);
   load_w(un.s0);
+  load_a(2 * un.s0);
+  if (un.s0 + 1 < kend) load_w(un.s0 + 1);
   load_a(2 * un.s0 + 1);
+  if (un.s0 + 1 < kend)
+    wait_vm<2 * AL + 2 + PL>();  // the first codes
+  else
+    wait_vm<2 * AL>();
+  __syncthreads();
+  read_codes(un.s0, 0);
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    take_params(n, true);
+    b[n] = dequant_word(w[n], nz[n], factors[n]);
+    ratio[n] = next_ratio[n];
+  }
   for (int kb = un.s0; kb < kend; ++kb) {
-    const char* pc = smem + L::kOffC + (kb & 1) * L::kC + (64 * wn + r16) * 64 + 4 * q4;
-    const char* pp = smem + L::kOffP + (kb & 1) * L::kP + (64 * wn + r16) * 4;
+    const bool more = kb + 1 < kend;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int s = 2 * kb + h;
-      // first half: its activations and the block's codes have landed (the
-      // second half's activations may be in flight); second half: its
-      // activations have (what the first half requested may be in flight).
-      // No wavefront still reads the stages requested next.
-      if (h == 0)
-        wait_vm<AL>();
-      else if (kb + 1 < kend)
+      // This half's activations have landed, and in the second half the next
+      // block's codes, which its last set reads ahead.  What may be in flight:
+      // the next half's activations and one block's codes, as far as there
+      // are any.  No wavefront still reads the stages requested next.
+      if (kb + 1 + h < kend)
         wait_vm<AL + 2 + PL>();
+      else if (kb + h < kend)
+        wait_vm<AL>();
       else
         wait_vm<0>();
       __syncthreads();
       const char* ta = smem + (s % 3) * L::kA + (wm * MT * 16 + r16) * 128;
 #pragma unroll
       for (int j2 = 0; j2 < 2; ++j2) {
-        const int j = 2 * h + j2, g = j / JG;
-        uint32_t w[4];
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-          w[n] = *(const uint32_t*)(pc + n * 1024 + 16 * (j ^ (r16 >> 2)));
-        if (j % JG == 0) {
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const uint32_t p = *(const uint32_t*)(pp + g * (kBN * 4) + n * 64);
-            const bool none = (p & 0x7fffu) == 0;
-            nz[n] = none ? 0 : (p >> 16) | (p & 0xffff0000u);
-            factors[n] = none ? 0 : kNibbleFactors;
-            const float st = none ? unit[n] : f16_lo(p);
-            // 1 / st to the last bit by one Newton step
-            const float r = __builtin_amdgcn_rcpf(st);
-            ratio[n] = unit[n] * fmaf(fmaf(-st, r, 1.0f), r, r);
-            unit[n] = st;
-          }
-        }
-        uint4 b[4];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) b[n] = dequant_word(w[n], nz[n], factors[n]);
+        const int j = 2 * h + j2, jn = (j + 1) & 3;
+        // past the last block the stage holds an old one: read, not used
+        read_codes(j == 3 ? kb + 1 : kb, jn);
+        uint4 bn[4];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           const uint4 a = *(const uint4*)(ta + m * 2048 + 16 * ((4 * j2 + q4) ^ (r16 & 7)));
@@ -244,11 +264,22 @@ k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
               for (int r = 0; r < 4; ++r) acc[m][n][r] *= ratio[n];
             acc[m][n] = mfma16<_Float16>(a, b[n], acc[m][n]);
           }
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+            if (m == 1 + n * (MT - 1) / 4) {
+              if (jn % JG == 0) take_params(n, j != 3 || more);
+              bn[n] = dequant_word(w[n], nz[n], factors[n]);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          b[n] = bn[n];
+          if (jn % JG == 0) ratio[n] = next_ratio[n];
         }
         // between a half's two sets the requests delay the MFMAs least
-        if (j2 == 0 && kb + 1 < kend) {
+        if (j2 == 0 && more) {
           load_a(s + 2);
-          if (h == 0) load_w(kb + 1);
+          if (h == 0 && kb + 2 < kend) load_w(kb + 2);
         }
       }
     }
