@@ -54,7 +54,10 @@ def _on(stream):
     """Context in which the binding allocates its outputs and workspaces: the
     stream the kernels run on, so torch's caching allocator hands the memory
     to no other stream while they may still be pending."""
-    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+    return torch.cuda.stream(stream) if stream is not None else _NOTHING
+
+
+_NOTHING = contextlib.nullcontext()
 
 
 def _dev(t: torch.Tensor, name: str, dtype: torch.dtype, shape) -> int:
@@ -241,56 +244,75 @@ def awq_w4a16_matmul(X: torch.Tensor, qweight: torch.Tensor, step: torch.Tensor,
 
 
 # -------------------------------------------------- packed-weight operators
+# A decode call runs for about ten microseconds, so these bindings keep to the
+# cheap checks: an argument that is as expected costs a few attribute reads,
+# and only one that is not goes through _dev, which says what is wrong.
 _DTYPES = {torch.float16: _lib.DTYPE_F16, torch.bfloat16: _lib.DTYPE_BF16}
 _ACTS = {"silu": _lib.ACT_SILU, "gelu": _lib.ACT_GELU_TANH}
+_REFUSED = ctypes.c_size_t(-1).value
+
+
+def _w4_ptr(t, name: str, dtype: torch.dtype, shape, dev: int) -> int:
+    """_dev's checks, and that the tensor is on GPU ``dev``."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.shape == shape
+            and t.is_contiguous()):
+        _dev(t, name, dtype, shape)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}: all tensors must be on one device, "
+                         f"the current one (cuda:{dev})")
+    return t.data_ptr()
 
 
 def _w4_layer(lead: torch.Tensor, name: str, qweight, step, zero):
     """Checks a packed layer against the activations or gradients ``lead`` and
-    returns (dtype code, tokens, in_features, rows, group size, pointers)."""
+    returns (dtype code, tokens, in_features, rows, group size, the layer's
+    pointers, device index)."""
     if not isinstance(lead, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if lead.dim() != 2 or qweight.dim() != 2 or step.dim() != 2:
-        raise ValueError(f"{name}, qweight and step must be 2-D")
     dt = _DTYPES.get(lead.dtype)
     if dt is None:
         raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {lead.dtype}")
+    if lead.dim() != 2 or qweight.dim() != 2 or step.dim() != 2:
+        raise ValueError(f"{name}, qweight and step must be 2-D")
     o, words = qweight.shape
     k, ng = 8 * words, step.shape[1]
     if ng == 0 or k % ng:
         raise ValueError(f"step has {ng} groups for in_features={k}")
-    ptrs = (_dev(qweight, "qweight", torch.int32, (o, words)),
-            _dev(step, "step", torch.float16, (o, ng)),
-            _dev(zero, "zero", torch.float16, (o, ng)))
-    dev = lead.device
-    if not (qweight.device == step.device == zero.device == dev):
-        raise ValueError(f"{name}, qweight, step and zero must be on one device")
-    if lead.is_cuda and dev.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {dev}, the current device is {torch.cuda.current_device()}")
-    return dt, lead.shape[0], k, o, k // ng, ptrs
+    if not lead.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+    dev = torch._C._cuda_getDevice()
+    if lead.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{lead.get_device()}, the current device is cuda:{dev}")
+    ptrs = (_w4_ptr(qweight, "qweight", torch.int32, (o, words), dev),
+            _w4_ptr(step, "step", torch.float16, (o, ng), dev),
+            _w4_ptr(zero, "zero", torch.float16, (o, ng), dev))
+    return dt, lead.shape[0], k, o, k // ng, ptrs, dev
 
 
-def _w4_workspace(op: str, n, k, rows, group, dt, dev, workspace):
-    """(pointer, bytes) of the workspace, allocated where the call needs one."""
-    need = getattr(load(), f"awq_w4a16_{op}_workspace_size")(n, k, rows, group, dt)
-    if need == ctypes.c_size_t(-1).value:
-        raise AwqError(_lib.AWQ_ERR_INVALID_ARG, load().awq_last_error().decode())
-    if workspace is None:
-        if need == 0:
-            return None, 0, None
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    if not workspace.is_cuda or workspace.device != dev:
-        raise ValueError(f"workspace must be on {dev}")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
-
-
-def _w4_out(t, name, dtype, shape, dev):
+def _w4_out(t, name: str, dtype: torch.dtype, shape, lead, dev: int):
+    """(tensor, pointer) of an output, allocated where the caller gave none."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _dev(t, name, dtype, shape)
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}")
-    return t
+        t = torch.empty(shape, dtype=dtype, device=lead.device)
+        return t, t.data_ptr()
+    return t, _w4_ptr(t, name, dtype, shape, dev)
+
+
+def _w4_workspace(query, sizes, lead, workspace):
+    """(tensor, pointer, bytes) of the workspace, allocated where the call needs one."""
+    if workspace is None:
+        need = query(*sizes)
+        if need == 0 or need == _REFUSED:  # the call itself says what it refuses
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=lead.device)
+    elif workspace.device != lead.device:
+        raise ValueError(f"workspace must be on {lead.device}")
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _w4_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def awq_w4a16_linear(X: torch.Tensor, qweight: torch.Tensor, step: torch.Tensor,
@@ -300,18 +322,22 @@ def awq_w4a16_linear(X: torch.Tensor, qweight: torch.Tensor, step: torch.Tensor,
     """Y = X W^T with the packed layer (qweight, step, zero) of awq_pack, any of
     its group sizes; X [n_tokens, in_features] fp16 or bf16, Y in out_dtype
     (X's type by default, or torch.float32)."""
-    dt, n, k, o, group, ptrs = _w4_layer(X, "X", qweight, step, zero)
+    lib = load()
+    dt, n, k, o, group, layer, dev = _w4_layer(X, "X", qweight, step, zero)
     if out_dtype is None:
-        out_dtype = out.dtype if out is not None else X.dtype
-    if out_dtype != X.dtype and out_dtype != torch.float32:
+        out_dtype = X.dtype if out is None else out.dtype
+    if out_dtype is not X.dtype and out_dtype is not torch.float32:
         raise TypeError(f"out_dtype must be {X.dtype} or torch.float32, got {out_dtype}")
-    x = _dev(X, "X", X.dtype, (n, k))
+    x = _w4_ptr(X, "X", X.dtype, (n, k), dev)
     with _on(stream):
-        out = _w4_out(out, "out", out_dtype, (n, o), X.device)
-        ws, size, _keep = _w4_workspace("linear", n, k, o, group, dt, X.device, workspace)
-    check(load().awq_w4a16_linear(x, dt, n, k, o, group, *ptrs, out.data_ptr(),
-                                  _lib.DTYPE_F32 if out_dtype == torch.float32 else dt, ws, size,
-                                  _stream(stream)))
+        out, y = _w4_out(out, "out", out_dtype, (n, o), X, dev)
+        workspace, ws, size = _w4_workspace(lib.awq_w4a16_linear_workspace_size, (n, k, o, group, dt),
+                                            X, workspace)
+    rc = lib.awq_w4a16_linear(x, dt, n, k, o, group, *layer, y,
+                              _lib.DTYPE_F32 if out_dtype is torch.float32 else dt, ws, size,
+                              _w4_stream(stream, dev))
+    if rc:
+        check(rc)
     return out
 
 
@@ -334,17 +360,21 @@ def awq_w4a16_gated(X: torch.Tensor, qweight: torch.Tensor, step: torch.Tensor,
     """H = act(X Wg^T) * (X Wu^T) in one kernel; the packed layer holds the
     gate's rows and then the up rows.  With keep_pre (or a pre buffer) returns
     (H, pre), pre = [G | U] in X's type, which the backward pass reads."""
-    dt, n, k, o, group, ptrs = _w4_layer(X, "X", qweight, step, zero)
+    lib = load()
+    dt, n, k, o, group, layer, dev = _w4_layer(X, "X", qweight, step, zero)
     f, code = _w4_half(o), _w4_act(act)
-    x = _dev(X, "X", X.dtype, (n, k))
+    x = _w4_ptr(X, "X", X.dtype, (n, k), dev)
+    p = None
     with _on(stream):
-        out = _w4_out(out, "out", X.dtype, (n, f), X.device)
+        out, h = _w4_out(out, "out", X.dtype, (n, f), X, dev)
         if keep_pre or pre is not None:
-            pre = _w4_out(pre, "pre", X.dtype, (n, o), X.device)
-        ws, size, _keep = _w4_workspace("gated", n, k, f, group, dt, X.device, workspace)
-    check(load().awq_w4a16_gated(x, dt, n, k, f, group, code, *ptrs, out.data_ptr(),
-                                 None if pre is None else pre.data_ptr(), ws, size,
-                                 _stream(stream)))
+            pre, p = _w4_out(pre, "pre", X.dtype, (n, o), X, dev)
+        workspace, ws, size = _w4_workspace(lib.awq_w4a16_gated_workspace_size, (n, k, f, group, dt),
+                                            X, workspace)
+    rc = lib.awq_w4a16_gated(x, dt, n, k, f, group, code, *layer, h, p, ws, size,
+                             _w4_stream(stream, dev))
+    if rc:
+        check(rc)
     return out if pre is None else (out, pre)
 
 
@@ -352,13 +382,17 @@ def awq_w4a16_input_grad(dY: torch.Tensor, qweight: torch.Tensor, step: torch.Te
                          zero: torch.Tensor, *, out: Optional[torch.Tensor] = None,
                          workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """dX = dY W [n_tokens, in_features] in dY's type, the packed codes frozen."""
-    dt, n, k, o, group, ptrs = _w4_layer(dY, "dY", qweight, step, zero)
-    d = _dev(dY, "dY", dY.dtype, (n, o))
+    lib = load()
+    dt, n, k, o, group, layer, dev = _w4_layer(dY, "dY", qweight, step, zero)
+    d = _w4_ptr(dY, "dY", dY.dtype, (n, o), dev)
     with _on(stream):
-        out = _w4_out(out, "out", dY.dtype, (n, k), dY.device)
-        ws, size, _keep = _w4_workspace("input_grad", n, k, o, group, dt, dY.device, workspace)
-    check(load().awq_w4a16_input_grad(d, dt, n, k, o, group, *ptrs, out.data_ptr(), ws, size,
-                                      _stream(stream)))
+        out, dx = _w4_out(out, "out", dY.dtype, (n, k), dY, dev)
+        workspace, ws, size = _w4_workspace(lib.awq_w4a16_input_grad_workspace_size,
+                                            (n, k, o, group, dt), dY, workspace)
+    rc = lib.awq_w4a16_input_grad(d, dt, n, k, o, group, *layer, dx, ws, size,
+                                  _w4_stream(stream, dev))
+    if rc:
+        check(rc)
     return out
 
 
@@ -369,18 +403,20 @@ def awq_w4a16_gated_backward(dH: torch.Tensor, pre: torch.Tensor, qweight: torch
                              workspace: Optional[torch.Tensor] = None, stream=None):
     """(dX, dpre) of awq_w4a16_gated from the gradient of H and the kept pre;
     dpre = [dG | dU] is what awq_w4a16_param_grad takes as dY."""
-    dt, n, k, o, group, ptrs = _w4_layer(dH, "dH", qweight, step, zero)
+    lib = load()
+    dt, n, k, o, group, layer, dev = _w4_layer(dH, "dH", qweight, step, zero)
     f, code = _w4_half(o), _w4_act(act)
-    d = _dev(dH, "dH", dH.dtype, (n, f))
-    p = _dev(pre, "pre", dH.dtype, (n, o))
-    if pre.device != dH.device:
-        raise ValueError(f"pre must be on {dH.device}")
+    d = _w4_ptr(dH, "dH", dH.dtype, (n, f), dev)
+    p = _w4_ptr(pre, "pre", dH.dtype, (n, o), dev)
     with _on(stream):
-        out = _w4_out(out, "out", dH.dtype, (n, k), dH.device)
-        dpre = _w4_out(dpre, "dpre", dH.dtype, (n, o), dH.device)
-        ws, size, _keep = _w4_workspace("gated_backward", n, k, f, group, dt, dH.device, workspace)
-    check(load().awq_w4a16_gated_backward(d, p, dt, n, k, f, group, code, *ptrs, dpre.data_ptr(),
-                                          out.data_ptr(), ws, size, _stream(stream)))
+        out, dx = _w4_out(out, "out", dH.dtype, (n, k), dH, dev)
+        dpre, dp = _w4_out(dpre, "dpre", dH.dtype, (n, o), dH, dev)
+        workspace, ws, size = _w4_workspace(lib.awq_w4a16_gated_backward_workspace_size,
+                                            (n, k, f, group, dt), dH, workspace)
+    rc = lib.awq_w4a16_gated_backward(d, p, dt, n, k, f, group, code, *layer, dp, dx, ws, size,
+                                      _w4_stream(stream, dev))
+    if rc:
+        check(rc)
     return out, dpre
 
 
@@ -391,17 +427,19 @@ def awq_w4a16_param_grad(dY: torch.Tensor, X: torch.Tensor, qweight: torch.Tenso
                          workspace: Optional[torch.Tensor] = None, stream=None):
     """(dstep, dzero), fp32 in step's shape: gradients of the group parameters
     of Y = X W^T for the output gradient dY, the packed codes frozen."""
-    dt, n, k, o, group, ptrs = _w4_layer(dY, "dY", qweight, step, zero)
-    d = _dev(dY, "dY", dY.dtype, (n, o))
-    x = _dev(X, "X", dY.dtype, (n, k))
-    if X.device != dY.device:
-        raise ValueError(f"X must be on {dY.device}")
+    lib = load()
+    dt, n, k, o, group, layer, dev = _w4_layer(dY, "dY", qweight, step, zero)
+    d = _w4_ptr(dY, "dY", dY.dtype, (n, o), dev)
+    x = _w4_ptr(X, "X", dY.dtype, (n, k), dev)
     with _on(stream):
-        dstep = _w4_out(dstep, "dstep", torch.float32, tuple(step.shape), dY.device)
-        dzero = _w4_out(dzero, "dzero", torch.float32, tuple(step.shape), dY.device)
-        ws, size, _keep = _w4_workspace("param_grad", n, k, o, group, dt, dY.device, workspace)
-    check(load().awq_w4a16_param_grad(d, x, dt, n, k, o, group, *ptrs, dstep.data_ptr(),
-                                      dzero.data_ptr(), ws, size, _stream(stream)))
+        dstep, ds = _w4_out(dstep, "dstep", torch.float32, tuple(step.shape), dY, dev)
+        dzero, dz = _w4_out(dzero, "dzero", torch.float32, tuple(step.shape), dY, dev)
+        workspace, ws, size = _w4_workspace(lib.awq_w4a16_param_grad_workspace_size,
+                                            (n, k, o, group, dt), dY, workspace)
+    rc = lib.awq_w4a16_param_grad(d, x, dt, n, k, o, group, *layer, ds, dz, ws, size,
+                                  _w4_stream(stream, dev))
+    if rc:
+        check(rc)
     return dstep, dzero
 
 

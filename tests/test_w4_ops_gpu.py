@@ -419,3 +419,45 @@ def test_steps_of_any_size(awq, n, t, group):
     ws_, es, wz, ez = P.param_grad(dy, x, *layer)
     close(ds, ws_, P.rounded(ws_, es, F32), "dstep")
     close(dz, wz, P.rounded(wz, ez.abs(), F32), "dzero")
+
+
+# shapes that take each way through the kernels: the streaming kernel with two,
+# four and eight groups of wavefronts at every token count, tiles of every
+# height, whole tiles followed by split ones, rows whose parameters do not fit
+# the streaming kernel
+WAYS = [(1, 256, 24700), (4, 128, 14400), (5, 128, 14400), (16, 128, 14337), (17, 128, 24600), (32, 256, 24577),
+        (33, 128, 25000), (48, 128, 24576), (49, 128, 20500), (64, 256, 20481), (20, 256, 4096), (47, 384, 200),
+        (49, 640, 4099), (64, 4096, 512), (10, 17408, 40), (80, 1024, 4096), (190, 2048, 2100), (700, 512, 5000),
+        (2100, 512, 8200)]
+
+
+@pytest.mark.parametrize("t,group", [(F16, 128), (F16, 64), (BF16, 128), (BF16, 32)], ids=str)
+@pytest.mark.parametrize("n,k,o", WAYS)
+def test_products_every_way(awq, n, k, o, t, group):
+    _say(f"ways {n}x{k}->{o} {t} g{group}")
+    layer = P.make_layer(o, k, group, n + k + o, "cuda")
+    check_linear(awq, rnd(n, k, t, n), layer, t if n % 2 else F32, "Y")
+    check_gated(awq, n, k, o // 2, t, group, "silu" if n % 2 else "gelu")
+
+
+GRAD_WAYS = [(40, 2048, 4100), (100, 4096, 640), (300, 4096, 1000), (700, 1024, 3000), (2100, 8192, 256),
+             (513, 128, 9000), (33, 4480, 4400), (300, 4480, 4400)]
+
+
+@pytest.mark.parametrize("t,group", [(F16, 128), (F16, 32), (BF16, 64)], ids=str)
+@pytest.mark.parametrize("n,k,o", GRAD_WAYS)
+def test_gradients_every_way(awq, n, k, o, t, group):
+    _say(f"gradient ways {n}x{k}<-{o} {t} g{group}")
+    layer = P.make_layer(o, k, group, n + k + o, "cuda")
+    w = P.weights(*layer)
+    dy, x = rnd(n, o, t, n + 2, 0.01), rnd(n, k, t, n + 3)
+    out = Guarded((n, k), t)
+    awq.awq_w4a16_input_grad(dy, *layer, out=out.t, workspace=poisoned(awq, "input_grad", n, k, o, group, t))
+    want, e = P.input_grad(dy, w, t)
+    close(out.check(), want, P.rounded(want, e, t), "dX")
+    ds, dz = Guarded((o, k // group), F32), Guarded((o, k // group), F32)
+    awq.awq_w4a16_param_grad(dy, x, *layer, dstep=ds.t, dzero=dz.t,
+                             workspace=poisoned(awq, "param_grad", n, k, o, group, t))
+    ws_, es, wz, ez = P.param_grad(dy, x, *layer)
+    close(ds.check(), ws_, P.rounded(ws_, es, F32), "dstep")
+    close(dz.check(), wz, P.rounded(wz, ez, F32), "dzero")
