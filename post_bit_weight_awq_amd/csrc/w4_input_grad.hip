@@ -1,9 +1,14 @@
 // dX = dY W on packed weights: W[o, k] = (q[o, k] - z[o, g]) step[o, g], the
 // sum running over the packed rows o.
 //
-// Block tile 32 MT tokens x 256 columns, eight wavefronts as 2 (tokens) x 4
+// Block tile of up to 256 tokens x 256 columns, eight wavefronts as 2 x 4
 // (columns), each 16 MT x 64 as MT x 4 tiles of v_mfma_f32_16x16x32_f16, 64
-// packed rows a step.  dY, the codes and the group parameters move to LDS by
+// packed rows a step.  For tiles of 192 and 256 tokens the two halves of the
+// wavefronts take half of the tokens each; for 64 and 128 both take all, each
+// every second step (SPLIT), and add their sums through LDS at the end: a
+// wavefront then converts codes for twice as many tokens.  One
+// 64- or 128-token tile per unit, 512 x 4096 <- 4096: 53 and 59 us against 67
+// and 83 with halved tokens.  dY, the codes and the group parameters move to LDS by
 // direct loads, two (codes: three) steps ahead.
 //   * An MFMA needs eight consecutive rows of one column per lane, while a
 //     word holds eight columns of one row.  So lane l reads the word l % 16 of
@@ -26,14 +31,18 @@
 
 namespace awq {
 
-// Three stages of dY, four of codes and parameters.
-template <int MT>
+// An iteration is one step, or two (SPLIT), whose operands lie side by side.
+// Three stages of dY and four of codes and parameters, three where four do not
+// fit.
+template <int MT, bool SPLIT>
 struct DxLds {
-  static constexpr int kA = 32 * MT * 128;  // bytes of dY per stage
-  static constexpr int kC = 64 * 128;       // codes
-  static constexpr int kP = 2048;           // group parameters
-  static constexpr int kOffC = 3 * kA, kOffP = kOffC + 4 * kC;
-  static constexpr int kBytes = kOffP + 4 * kP;
+  static constexpr int kA = 32 * MT * 128;            // bytes of dY per stage
+  static constexpr int kC = (SPLIT ? 2 : 1) * 64 * 128;  // codes
+  static constexpr int kP = (SPLIT ? 2 : 1) * 2048;      // group parameters
+  static constexpr int kNC = SPLIT && MT == 8 ? 3 : 4;
+  static constexpr int kOffC = 3 * kA, kOffP = kOffC + kNC * kC;
+  static constexpr int kBytes = kOffP + kNC * kP;
+  static_assert(kBytes <= 160 * 1024);
 };
 
 // Values of one token's four neighbouring columns per lane, tile by tile.
@@ -56,15 +65,33 @@ __device__ __forceinline__ void store_dx(const floatx4 (&acc)[MT][4], const int*
     }
 }
 
-template <typename T, int GROUP, int MT>
+// A whole tile's values to dX, a part's to the workspace as they lie.
+template <typename T, int MT>
+__device__ __forceinline__ void leave(const floatx4 (&acc)[MT][4], float* parts, const SplitUnit& un,
+                                      int wave, const int* back, int N, int K, int t0, int col,
+                                      int lane, T* dX) {
+  if (un.parts == 1) {
+    store_dx<T, MT>(acc, back, N, K, t0, col, lane, dX);
+    return;
+  }
+  floatx4* p = (floatx4*)parts + ((size_t)un.slot * 8 + wave) * (MT * 4 * 64) + lane;
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) p[(m * 4 + c) * 64] = acc[m][c];
+}
+
+template <typename T, int GROUP, int MT, bool SPLIT>
 __global__ void __launch_bounds__(512, 2)
 k_w4_dx(const _Float16* __restrict__ A, int lda, const int* __restrict__ back, int N, int K, int O,
         const char* __restrict__ qw, const char* __restrict__ prm, const int* __restrict__ big,
         T* __restrict__ dX, float* __restrict__ parts, TileSplit sp) {
-  using L = DxLds<MT>;
-  constexpr int BM = 32 * MT;
-  constexpr int AL = MT / 2;           // direct loads of dY per wavefront and step
-  constexpr int PB = 8192 / GROUP;     // parameter bytes per wavefront and step
+  using L = DxLds<MT, SPLIT>;
+  constexpr int BM = (SPLIT ? 16 : 32) * MT;
+  constexpr int AL = MT / 2;           // direct loads of dY per wavefront and iteration
+  constexpr int CL = SPLIT ? 2 : 1;    // of codes
+  constexpr int PB = CL * 8192 / GROUP;  // parameter bytes per wavefront and iteration
+  constexpr int PL = PB > 256 ? 2 : 1;   // their loads
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -72,41 +99,65 @@ k_w4_dx(const _Float16* __restrict__ A, int lda, const int* __restrict__ back, i
   const int r16 = lane & 15, q4 = lane >> 4;
   const SplitUnit un = split_unit(blockIdx.x, sp);
   const int t0 = un.t * BM, k0 = un.o * 256;
-  const int ng = K / GROUP;
+  const int ng = K / GROUP, steps = (O + 63) >> 6;
+  // With SPLIT wavefronts 0-3 load and take the even steps, 4-7 the odd ones;
+  // an odd one past the end loads the last step, which is not used.
+  auto step_of = [&](int it) {
+    return __builtin_amdgcn_readfirstlane(SPLIT ? min(2 * it + wm, steps - 1) : it);
+  };
+  const int lw = SPLIT ? wn : wave;  // the wavefront among those that load a step
 
   // dY: load i brings 8 rows of 128 bytes; 16-byte piece p of row r at p ^ (r % 8)
   uint32_t oa[AL];
 #pragma unroll
   for (int i = 0; i < AL; ++i) {
-    const int r = 8 * (wave * AL + i) + (lane >> 3);
+    const int r = 8 * (lw * AL + i) + (lane >> 3);
     oa[i] = 2u * ((uint32_t)(min(t0 + r, N - 1) - t0) * (uint32_t)lda + 8 * ((lane & 7) ^ (r & 7)));
   }
   const char* a0 = (const char*)(A + (size_t)t0 * lda);
-  // codes: one load of 8 LDS rows of 128 bytes; LDS row 32 c + 4 i + q is
+  // codes: a load brings 8 LDS rows of 128 bytes; LDS row 32 c + 4 i + q is
   // packed row 32 c + 8 q + i of the step
-  const int lr = 8 * wave + (lane >> 3);
-  const int crow = 32 * (lr >> 5) + 8 * (lr & 3) + ((lr & 31) >> 2);
-  int piece = (lane & 7) ^ (((lr >> 1) & 1) << 2);
-  if (k0 + 32 * piece >= K) piece -= 4;  // a last tile of 128 columns
-  const uint32_t oc = (uint32_t)(k0 / 2 + 16 * piece);
+  int crow[CL];
+  uint32_t oc[CL];
+#pragma unroll
+  for (int i = 0; i < CL; ++i) {
+    const int lr = 8 * (lw * CL + i) + (lane >> 3);
+    crow[i] = 32 * (lr >> 5) + 8 * (lr & 3) + ((lr & 31) >> 2);
+    int piece = (lane & 7) ^ (((lr >> 1) & 1) << 2);
+    if (k0 + 32 * piece >= K) piece -= 4;  // a last tile of 128 columns
+    oc[i] = (uint32_t)(k0 / 2 + 16 * piece);
+  }
   // parameters: PB bytes of the block's groups per wavefront
-  const int pbyte = wave * PB + 4 * lane;
-  const int pg = min(k0 / GROUP + pbyte / 256, ng - 1);
-  const uint32_t op = (uint32_t)pg * 256u + (pbyte & 255);
+  uint32_t op[PL];
+#pragma unroll
+  for (int i = 0; i < PL; ++i) {
+    const int at = lw * PB + 256 * i + 4 * lane;
+    op[i] = (uint32_t)min(k0 / GROUP + at / 256, ng - 1) * 256u + (at & 255);
+  }
 
   const uint32_t lds = (uint32_t)(uintptr_t)smem;
-  auto load_a = [&](int s) {
+  auto load_a = [&](int it) {
+    const char* base = a0 + (size_t)step_of(it) * 128;
 #pragma unroll
     for (int i = 0; i < AL; ++i)
-      dma16(a0 + s * 128, oa[i], lds + (s % 3) * L::kA + (wave * AL + i) * 1024);
+      dma16(base, oa[i], lds + (it % 3) * L::kA + (wave * AL + i) * 1024);
   };
-  auto load_c = [&](int s) {
+  auto load_c = [&](int it) {
+    const int s = step_of(it);
     // each lane's row, the last one where the step passes the end
-    const int row = min(64 * s + crow, O - 1);
-    dma16(qw + (size_t)(64 * s) * (K / 2), (uint32_t)(row - 64 * s) * (uint32_t)(K / 2) + oc,
-          lds + L::kOffC + (s & 3) * L::kC + wave * 1024);
-    if (lane < PB / 4)
-      dma4(prm + (size_t)s * ng * 256, op, lds + L::kOffP + (s & 3) * L::kP + wave * PB);
+#pragma unroll
+    for (int i = 0; i < CL; ++i)
+      dma16(qw + (size_t)(64 * s) * (K / 2),
+            (uint32_t)(min(64 * s + crow[i], O - 1) - 64 * s) * (uint32_t)(K / 2) + oc[i],
+            lds + L::kOffC + (it % L::kNC) * L::kC + (wave * CL + i) * 1024);
+    const char* p = prm + (size_t)s * ng * 256;
+    const uint32_t l = lds + L::kOffP + (it % L::kNC) * L::kP + (SPLIT ? wm * 2048 : 0) + lw * PB;
+    if (PB >= 256) {
+#pragma unroll
+      for (int i = 0; i < PL; ++i) dma4(p, op[i], l + 256 * i);
+    } else if (lane < PB / 4) {
+      dma4(p, op[0], l);
+    }
   };
 
   floatx4 acc[MT][4];
@@ -114,7 +165,7 @@ k_w4_dx(const _Float16* __restrict__ A, int lda, const int* __restrict__ back, i
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int c = 0; c < 4; ++c) acc[m][c] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-  const int cbase = q4 * 128 + ((wb ^ (q4 >> 1)) * 64) + 4 * r16;
+  const int cbase = (SPLIT ? wm * 8192 : 0) + q4 * 128 + ((wb ^ (q4 >> 1)) * 64) + 4 * r16;
   const int gl = (128 * wb + 8 * r16) / GROUP;  // the lane's group among the block's
   const uint32_t sel = half ? 0x07060302u : 0x05040100u;
 
@@ -125,12 +176,13 @@ k_w4_dx(const _Float16* __restrict__ A, int lda, const int* __restrict__ back, i
     load_c(un.s0 + 1);
     load_a(un.s0 + 1);
   }
-  if (un.s0 + 2 < send) load_c(un.s0 + 2);
+  if (L::kNC == 4 && un.s0 + 2 < send) load_c(un.s0 + 2);
   // steps of 128 and more among the block's: 512 step leaves fp16's range, so
   // the factor goes to the differences, one operation more
   int over = 0;
   const int gb = (ng + 31) / 32, gb0 = k0 / GROUP / 32, gb1 = min(k0 + 255, K - 1) / GROUP / 32;
-  for (int s = un.s0 + tid; s < un.s1; s += 512) over |= big[s * gb + gb0] | big[s * gb + gb1];
+  for (int s = CL * un.s0 + tid; s < min(CL * un.s1, steps); s += 512)
+    over |= big[s * gb + gb0] | big[s * gb + gb1];
   over = __syncthreads_or(over);
   // Half a step (32 packed rows) at a time; while one half multiplies, the
   // next one's codes are read and converted a row pair after each few
@@ -140,8 +192,9 @@ k_w4_dx(const _Float16* __restrict__ A, int lda, const int* __restrict__ back, i
     uint4 zv, sv, b[4];
     uint32_t bn[4][4];
     auto read_codes = [&](int s, int ch) {
-      const char* pc = smem + L::kOffC + (s & 3) * L::kC + cbase + ch * 4096;
-      const char* pp = smem + L::kOffP + (s & 3) * L::kP + gl * 256 + 16 * q4 + ch * 64;
+      const char* pc = smem + L::kOffC + (s % L::kNC) * L::kC + cbase + ch * 4096;
+      const char* pp = smem + L::kOffP + (s % L::kNC) * L::kP + (SPLIT ? wm * 2048 : 0) +
+                       gl * 256 + 16 * q4 + ch * 64;
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = *(const uint32_t*)(pc + i * 512);
       zv = *(const uint4*)pp;
@@ -177,33 +230,39 @@ k_w4_dx(const _Float16* __restrict__ A, int lda, const int* __restrict__ back, i
     for (int p = 0; p < 4; ++p) convert(p);
     take();
     for (int s = un.s0; s < send; ++s) {
-      // the step's dY and the next step's codes have landed (what the last
-      // step requested may be in flight), and no wavefront still reads the
-      // stages that are requested next
-      if (s + 2 < send && s > un.s0)
-        wait_vm<AL + 2>();
+      // the iteration's dY and the next one's codes have landed (what was
+      // requested after them may be in flight), and no wavefront still reads
+      // the stages that are requested next
+      if (L::kNC == 4 && s + 2 < send && s > un.s0)
+        wait_vm<AL + CL + PL>();
+      else if (L::kNC == 3 && s + 1 < send && s > un.s0)
+        wait_vm<AL>();
       else
         wait_vm<0>();
       __syncthreads();
+      // the odd step past the last one
+      const bool live = !SPLIT || 2 * s + wm < steps;
 #pragma unroll
       for (int ch = 0; ch < 2; ++ch) {
-        const char* ta = smem + (s % 3) * L::kA + (wm * MT * 16 + r16) * 128 +
-                         16 * ((4 * ch + q4) ^ (r16 & 7));
-        // past the end the stage holds old values: read, not used
-        read_codes(s + ch, 1 - ch);
+        if (live) {
+          const char* ta = smem + (s % 3) * L::kA + (wm * MT * 16 + r16) * 128 +
+                           16 * ((4 * ch + q4) ^ (r16 & 7));
+          // past the end the stage holds old values: read, not used
+          read_codes(s + ch, 1 - ch);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const uint4 a = *(const uint4*)(ta + m * 2048);
+          for (int m = 0; m < MT; ++m) {
+            const uint4 a = *(const uint4*)(ta + m * 2048);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) acc[m][c] = mfma16<_Float16>(a, b[c], acc[m][c]);
+            for (int c = 0; c < 4; ++c) acc[m][c] = mfma16<_Float16>(a, b[c], acc[m][c]);
 #pragma unroll
-          for (int p = 0; p < 4; ++p)
-            if (m == 1 + p * (MT - 1) / 4) convert(p);
+            for (int p = 0; p < 4; ++p)
+              if (m == 1 + p * (MT - 1) / 4) convert(p);
+          }
+          take();
         }
-        take();
         // between the halves the requests delay the MFMAs least
         if (ch == 0) {
-          if (s + 3 < send) load_c(s + 3);
+          if (s + L::kNC - 1 < send) load_c(s + L::kNC - 1);
           if (s + 2 < send) load_a(s + 2);
         }
       }
@@ -213,15 +272,30 @@ k_w4_dx(const _Float16* __restrict__ A, int lda, const int* __restrict__ back, i
     sum(std::false_type{});
   else
     sum(std::true_type{});
-  if (un.parts > 1) {
-    floatx4* p = (floatx4*)parts + ((size_t)un.slot * 8 + wave) * (MT * 4 * 64) + lane;
+  const int col = k0 + 128 * wb + 8 * r16 + 4 * half;
+  if constexpr (!SPLIT) {
+    leave<T, MT>(acc, parts, un, wave, back, N, K, t0 + wm * MT * 16, col, lane, dX);
+  } else {
+    // each half of the wavefronts hands half of its tokens' sums to the other
+    constexpr int H = MT / 2;
+    floatx4 keep[H][4];
+    floatx4* const mine = (floatx4*)smem + wave * (H * 4 * 64) + lane;
+    const floatx4* const other = (const floatx4*)smem + (wave ^ 4) * (H * 4 * 64) + lane;
+    __syncthreads();
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < H; ++m)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) p[(m * 4 + c) * 64] = acc[m][c];
-    return;
+      for (int c = 0; c < 4; ++c) {
+        mine[(m * 4 + c) * 64] = wm ? acc[m][c] : acc[H + m][c];
+        keep[m][c] = wm ? acc[H + m][c] : acc[m][c];
+      }
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < H; ++m)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) keep[m][c] += other[(m * 4 + c) * 64];
+    leave<T, H>(keep, parts, un, wave, back, N, K, t0 + wm * H * 16, col, lane, dX);
   }
-  store_dx<T, MT>(acc, back, N, K, t0 + wm * MT * 16, k0 + 128 * wb + 8 * r16 + 4 * half, lane, dX);
 }
 
 // Sums of a split tile's parts, in order; a block takes 32 tokens of one
@@ -268,10 +342,13 @@ static DxPlan dx_plan(const W4Args& a) {
 }
 size_t w4_input_grad_workspace(const W4Args& a) { return dx_plan(a).bytes; }
 
+// The tile is 32 MT tokens high.
 template <typename T, int GROUP, int MT>
 static hipError_t launch(const W4Args& a, const void* dY, const DxPlan& p, hipStream_t stream) {
-  auto* kernel = &k_w4_dx<T, GROUP, MT>;
-  const int lds = DxLds<MT>::kBytes;
+  constexpr bool SPLIT = MT <= 4;
+  constexpr int W = SPLIT ? 2 * MT : MT;  // token tiles of a wavefront
+  auto* kernel = &k_w4_dx<T, GROUP, W, SPLIT>;
+  const int lds = DxLds<W, SPLIT>::kBytes;
   hipError_t e =
       hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;

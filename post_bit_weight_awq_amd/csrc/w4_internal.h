@@ -36,22 +36,24 @@ struct TileSplit {
 };
 constexpr int kCUs = 256;
 
-// Microseconds of a tile of 32 mt tokens by 256 (mt = 2, 4, 6, 8), per step of
-// the sum; the rest is common to all.
+// Microseconds of a tile of 32 mt tokens by 256 (mt = 2, 4, 6, 8) per
+// iteration of its kernel, which takes `per` steps of the sum; the rest is
+// common to all.
 struct TileCosts {
   float step[4];
+  int per[4];
 };
-constexpr float kTileStart = 3.0f;            // a tile's first loads and its epilogue
+constexpr float kTileStart = 5.0f;            // a tile's first loads and its epilogue
 constexpr float kJoinStart = 4.0f;            // the second launch
 constexpr float kPartRate = 6.0e6f;           // bytes per microsecond of parts, written and read
 
 // Tile height and split with the least estimated time; `scale` multiplies the
 // steps' cost.
-inline void choose_tiles(int64_t N, int no, int steps, const TileCosts& c, float scale, int* mt_out,
+inline void choose_tiles(int64_t N, int no, int all_steps, const TileCosts& c, float scale, int* mt_out,
                          TileSplit* out) {
   float best = 0.0f;
   for (int i = 0; i < 4; ++i) {
-    const int mt = 2 * (i + 1);
+    const int mt = 2 * (i + 1), steps = (all_steps + c.per[i] - 1) / c.per[i];
     const int nt = (int)((N + 32 * mt - 1) / (32 * mt));
     const int total = nt * no, left = total % kCUs;
     const float step = scale * c.step[i], tile = step * steps + kTileStart;
@@ -73,11 +75,11 @@ inline void choose_tiles(int64_t N, int no, int steps, const TileCosts& c, float
     }
   }
 }
-// Measured with one tile per unit on 512 x 4096 x 4096 and, for the products,
-// 1024 x 13824 x 5120: 128 columns a step for the products (w4_gemm.hip), 64
-// packed rows a step for the input gradient (w4_input_grad.hip).
-constexpr TileCosts kGemmCosts = {{1.5f, 2.1f, 2.55f, 3.1f}};
-constexpr TileCosts kDxCosts = {{0.9f, 1.15f, 1.35f, 1.65f}};
+// Measured with one tile per unit on 512 x 4096 x 4096, 1024 x 13824 -> 5120
+// for the products (w4_gemm.hip, 128 columns a step) and 128 x 4096 <- 11008
+// for the input gradient (w4_input_grad.hip, 64 packed rows a step).
+constexpr TileCosts kGemmCosts = {{1.5f, 2.1f, 2.55f, 3.1f}, {1, 1, 1, 1}};
+constexpr TileCosts kDxCosts = {{1.15f, 1.42f, 1.25f, 1.45f}, {2, 2, 1, 1}};
 
 struct SplitUnit {
   int t, o, s0, s1, parts, slot;  // steps s0 .. s1 - 1
