@@ -1,9 +1,14 @@
 // Y = X W^T and H = act(X Wg^T) * (X Wu^T) on packed weights for many tokens:
 // a tiled MFMA product that reads the codes as they are packed.
 //
-// Block tile 32 MT tokens x 256 packed rows (gated: 128 rows of the gate and
-// the same features' 128 up rows), eight wavefronts as 2 (tokens) x 4 (rows),
-// each 16 MT x 64 as MT x 4 tiles of v_mfma_f32_16x16x32_f16.
+// Block tile of up to 256 tokens x 256 packed rows (gated: 128 rows of the gate
+// and the same features' 128 up rows), eight wavefronts as 2 x 4 (rows), each
+// 16 MT x 64 as MT x 4 tiles of v_mfma_f32_16x16x32_f16.  For tiles of 192 and
+// 256 tokens the two halves of the wavefronts take half of the tokens each; for
+// 64 and 128 both take all, each every second block of 128 columns (SPLIT), and
+// add their sums through LDS at the end: each weight is then converted once per
+// block.  One 64- or 128-token tile per unit, 512 x 4096 -> 4096: 48 and 61 us
+// against 58 and 75 with halved tokens.
 //   * Activations move to LDS 64 columns at a time, codes and group parameters
 //     128 columns at a time, by direct loads up to two steps ahead; 16-byte
 //     pieces are permuted by row so that reads hit every bank once.
@@ -95,25 +100,47 @@ __device__ __forceinline__ void finish32(const floatx4 (&v0)[4], const floatx4 (
   asm volatile("" ::: "memory");
 }
 
-template <int GROUP, int MT>
+// A whole tile's values to the outputs, a part's to the workspace as they lie.
+template <bool GATED, int MT>
+__device__ __forceinline__ void leave(const floatx4 (&acc)[MT][4], float* parts, const SplitUnit& un,
+                                      int wave, float* own, const Epilogue& ep, int t0, int ob,
+                                      int lane) {
+  if (un.parts == 1) {
+#pragma unroll
+    for (int m = 0; m < MT; m += 2) finish32<GATED>(acc[m], acc[m + 1], own, ep, t0 + 16 * m, ob, lane);
+    return;
+  }
+  floatx4* p = (floatx4*)parts + ((size_t)un.slot * 8 + wave) * (MT * 4 * 64) + lane;
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < 4; ++n) p[(m * 4 + n) * 64] = acc[m][n];
+}
+
+// Three stages of the activations and of the codes; the codes of 128 columns
+// (SPLIT: 64 of each of two blocks of 128), parameters three (two) stages.
+template <int GROUP, int MT, bool SPLIT>
 struct GemmLds {
-  static constexpr int kA = 32 * MT * 128;            // 64 columns of the activations
-  static constexpr int kC = kBN * 64;                 // 128 columns of codes
-  static constexpr int kP = kBN * 4 * (128 / GROUP);  // their group parameters
+  static constexpr int kA = 32 * MT * 128;                           // 64 columns of activations
+  static constexpr int kC = kBN * 64;                                // codes
+  static constexpr int kP1 = kBN * 4 * (128 / GROUP);                // parameters of 128 columns
+  static constexpr int kP = (SPLIT ? 2 : 1) * kP1, kNP = SPLIT ? 2 : 3;
   static constexpr int kOffC = 3 * kA, kOffP = kOffC + 3 * kC;
-  static constexpr int kMain = kOffP + 3 * kP;
+  static constexpr int kMain = kOffP + kNP * kP;
   static constexpr int kBytes = kMain > 8 * kEpWave * 4 ? kMain : 8 * kEpWave * 4;
+  static_assert(kBytes <= 160 * 1024);
 };
 
-template <int GROUP, bool GATED, int MT>
+template <int GROUP, bool GATED, int MT, bool SPLIT>
 __global__ void __launch_bounds__(512, 2)
 k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
           const char* __restrict__ prm, float* __restrict__ parts, TileSplit sp, Epilogue ep) {
-  using L = GemmLds<GROUP, MT>;
-  constexpr int BM = 32 * MT;
+  using L = GemmLds<GROUP, MT, SPLIT>;
+  constexpr int BM = (SPLIT ? 16 : 32) * MT;
   constexpr int GPB = 128 / GROUP, JG = 4 / GPB;
-  constexpr int AL = MT / 2;                  // direct loads of activations per wavefront and step
-  constexpr int PL = GPB == 4 ? 2 : 1;        // of group parameters per 128 columns
+  constexpr int AL = MT / 2;  // direct loads of activations per wavefront and half
+  // of group parameters per iteration
+  constexpr int PL = SPLIT ? GPB : GPB == 4 ? 2 : 1;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -123,20 +150,29 @@ k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
   const int N = ep.N, O = ep.O, F = O >> 1;
   const int t0 = un.t * BM, rb = un.o * (GATED ? kBN / 2 : kBN);
   const uint32_t lds = (uint32_t)(uintptr_t)smem;
+  // An iteration takes 128 columns, or two such blocks (SPLIT), of which
+  // wavefronts 0-3 load and take the even ones and 4-7 the odd ones; an odd one
+  // past the end loads the last block, which is not used.
+  const int nkb = K >> 7;
+  auto block_of = [&](int it) {
+    return __builtin_amdgcn_readfirstlane(SPLIT ? min(2 * it + wm, nkb - 1) : it);
+  };
+  const int lw = SPLIT ? wn : wave;  // the wavefront among those that load a block
 
   // activations: load i brings 8 rows of 128 bytes; 16-byte piece p of row r
   // at p ^ (r % 8)
   uint32_t oa[AL];
 #pragma unroll
   for (int i = 0; i < AL; ++i) {
-    const int r = 8 * (wave * AL + i) + (lane >> 3);
+    const int r = 8 * (lw * AL + i) + (lane >> 3);
     oa[i] = 2u * ((uint32_t)(min(t0 + r, N - 1) - t0) * (uint32_t)K + 8 * ((lane & 7) ^ (r & 7)));
   }
   const char* a0 = (const char*)(A + (size_t)t0 * K);
-  auto load_a = [&](int s) {
+  auto load_a = [&](int s) {  // half s & 1 of iteration s / 2
+    const char* base = a0 + (size_t)(2 * block_of(s >> 1) + (s & 1)) * 128;
 #pragma unroll
     for (int i = 0; i < AL; ++i)
-      dma16(a0 + s * 128, oa[i], lds + (s % 3) * L::kA + (wave * AL + i) * 1024);
+      dma16(base, oa[i], lds + (s % 3) * L::kA + (wave * AL + i) * 1024);
   };
   // Block row i: wavefront column i / 64; gated, its first 32 rows are the
   // gate's and the next 32 the same features' up rows.  Past the end the last
@@ -145,36 +181,41 @@ k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
     if (GATED) return min(rb + 32 * (i >> 6) + (i & 31), F - 1) + (i & 32 ? F : 0);
     return min(rb + i, O - 1);
   };
-  // codes: a load brings 16 rows of 64 bytes; 16-byte piece p of row r at
-  // p ^ (r / 4 % 4)
+  // codes: a load brings 16 rows of 64 bytes, 16-byte piece p of row r at
+  // p ^ (r / 4 % 4); or 32 rows of 32 bytes, at p ^ (r / 8 % 2).  A load's rows
+  // lie in one half of the packed rows.
+  constexpr int RB = SPLIT ? 32 : 64, RL = 1024 / RB;  // bytes of a row, rows of a load
   uint32_t oc[2];
   const char* c0[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    // a load's 16 rows lie in one half of the packed rows
-    const int r = 16 * (2 * wave + i), row = packed_row(r);
+    const int r = RL * (2 * lw + i), row = packed_row(r);
+    const int at = SPLIT ? (lane & 1) ^ ((lane >> 4) & 1) : (lane & 3) ^ ((lane >> 4) & 3);
     c0[i] = qw + (size_t)row * (K >> 1);
-    oc[i] = (uint32_t)(packed_row(r + (lane >> 2)) - row) * (uint32_t)(K >> 1) +
-            16 * ((lane & 3) ^ ((lane >> 4) & 3));
+    oc[i] = (uint32_t)(packed_row(r + lane / (RB / 16)) - row) * (uint32_t)(K >> 1) + 16 * at;
   }
-  // parameters: 64 rows of one group (32 with one group per 128 columns)
+  auto load_c = [&](int s) {  // SPLIT: of a half; else of iteration s
+    const int off = SPLIT ? 64 * block_of(s >> 1) + 32 * (s & 1) : 64 * s;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      dma16(c0[i] + off, oc[i], lds + L::kOffC + (s % 3) * L::kC + (2 * wave + i) * 1024);
+  };
+  // parameters: 64 rows of one group (32 with one group and all wavefronts)
+  constexpr bool PHALF = !SPLIT && GPB == 1;
   uint32_t op[PL];
 #pragma unroll
   for (int i = 0; i < PL; ++i) {
-    const int at = GPB == 1 ? 32 * wave + (lane & 31) : 64 * (wave * PL + i) + lane;
+    const int at = PHALF ? 32 * wave + (lane & 31) : 64 * (lw * PL + i) + lane;
     op[i] = 4u * ((uint32_t)(at / kBN) * (uint32_t)O + (uint32_t)packed_row(at % kBN));
   }
-  auto load_w = [&](int kb) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      dma16(c0[i] + 64 * kb, oc[i], lds + L::kOffC + (kb % 3) * L::kC + (2 * wave + i) * 1024);
-    const char* p = prm + (size_t)kb * GPB * O * 4;
-    const uint32_t l = lds + L::kOffP + (kb % 3) * L::kP;
-    if (GPB == 1) {
+  auto load_p = [&](int it) {
+    const char* p = prm + (size_t)block_of(it) * GPB * O * 4;
+    const uint32_t l = lds + L::kOffP + (it % L::kNP) * L::kP + (SPLIT ? wm * L::kP1 : 0);
+    if (PHALF) {
       if (lane < 32) dma4(p, op[0], l + wave * 128);
     } else {
 #pragma unroll
-      for (int i = 0; i < PL; ++i) dma4(p, op[i], l + (wave * PL + i) * 256);
+      for (int i = 0; i < PL; ++i) dma4(p, op[i], l + (lw * PL + i) * 256);
     }
   };
 
@@ -193,11 +234,15 @@ k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
   uint4 b[4];
   uint32_t w[4], pv[4], nz[4], factors[4];
   float ratio[4], next_ratio[4];
-  auto read_codes = [&](int kb, int j) {
-    const char* pc = smem + L::kOffC + (kb % 3) * L::kC + (64 * wn + r16) * 64 + 4 * q4;
+  auto read_codes = [&](int it, int j) {
+    const char* pc = smem + L::kOffC + (64 * wn + r16) * RB + 4 * q4;
 #pragma unroll
-    for (int n = 0; n < 4; ++n) w[n] = *(const uint32_t*)(pc + n * 1024 + 16 * (j ^ (r16 >> 2)));
-    const char* pp = smem + L::kOffP + (kb % 3) * L::kP + (64 * wn + r16) * 4;
+    for (int n = 0; n < 4; ++n)
+      w[n] = SPLIT ? *(const uint32_t*)(pc + (2 * it + (j >> 1)) % 3 * L::kC + wm * 8192 + n * 512 +
+                                        16 * ((j & 1) ^ (r16 >> 3)))
+                   : *(const uint32_t*)(pc + it % 3 * L::kC + n * 1024 + 16 * (j ^ (r16 >> 2)));
+    const char* pp = smem + L::kOffP + (it % L::kNP) * L::kP + (SPLIT ? wm * L::kP1 : 0) +
+                     (64 * wn + r16) * 4;
     if (j % JG == 0)
 #pragma unroll
       for (int n = 0; n < 4; ++n)
@@ -214,15 +259,28 @@ k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
     next_ratio[n] = unit[n] * fmaf(fmaf(-st, r, 1.0f), r, r);
     unit[n] = st;
   };
-  const int kend = un.s1;
-  load_w(un.s0);
-  load_a(2 * un.s0);
-  if (un.s0 + 1 < kend) load_w(un.s0 + 1);
-  load_a(2 * un.s0 + 1);
-  if (un.s0 + 1 < kend)
-    wait_vm<2 * AL + 2 + PL>();  // the first codes
-  else
-    wait_vm<2 * AL>();
+  const int end = un.s1, send = 2 * end;
+  if constexpr (SPLIT) {
+    load_p(un.s0);
+    load_c(2 * un.s0);
+    load_a(2 * un.s0);
+    load_c(2 * un.s0 + 1);
+    load_a(2 * un.s0 + 1);
+    wait_vm<2 * AL + 2>();  // the first parameters and codes
+  } else {
+    load_c(un.s0);
+    load_p(un.s0);
+    load_a(2 * un.s0);
+    if (un.s0 + 1 < end) {
+      load_c(un.s0 + 1);
+      load_p(un.s0 + 1);
+    }
+    load_a(2 * un.s0 + 1);
+    if (un.s0 + 1 < end)
+      wait_vm<2 * AL + 2 + PL>();
+    else
+      wait_vm<2 * AL>();
+  }
   __syncthreads();
   read_codes(un.s0, 0);
 #pragma unroll
@@ -231,19 +289,22 @@ k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
     b[n] = dequant_word(w[n], nz[n], factors[n]);
     ratio[n] = next_ratio[n];
   }
-  for (int kb = un.s0; kb < kend; ++kb) {
-    const bool more = kb + 1 < kend;
+  for (int it = un.s0; it < end; ++it) {
+    // whether this wavefront has this block and another one
+    const bool live = !SPLIT || 2 * it + wm < nkb;
+    const bool more = it + 1 < end && (!SPLIT || 2 * it + 2 + wm < nkb);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int s = 2 * kb + h;
-      // This half's activations have landed, and in the second half the next
-      // block's codes, which its last set reads ahead.  What may be in flight:
-      // the next half's activations and one block's codes, as far as there
-      // are any.  No wavefront still reads the stages requested next.
-      if (kb + 1 + h < kend)
-        wait_vm<AL + 2 + PL>();
-      else if (kb + h < kend)
+      const int s = 2 * it + h;
+      // This half's activations have landed, and the codes and parameters that
+      // its last set reads ahead.  What may be in flight was requested after
+      // them: the next half's activations, without SPLIT also one block's
+      // codes, as far as there are any.  No wavefront still reads the stages
+      // requested next.
+      if (SPLIT ? s + 1 < send && s > 2 * un.s0 : it + h < end && it + 1 + h >= end)
         wait_vm<AL>();
+      else if (!SPLIT && it + 1 + h < end)
+        wait_vm<AL + 2 + PL>();
       else
         wait_vm<0>();
       __syncthreads();
@@ -251,35 +312,48 @@ k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
 #pragma unroll
       for (int j2 = 0; j2 < 2; ++j2) {
         const int j = 2 * h + j2, jn = (j + 1) & 3;
-        // past the last block the stage holds an old one: read, not used
-        read_codes(j == 3 ? kb + 1 : kb, jn);
-        uint4 bn[4];
+        if (live) {
+          // past the last block the stage holds an old one: read, not used
+          read_codes(j == 3 ? it + 1 : it, jn);
+          uint4 bn[4];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const uint4 a = *(const uint4*)(ta + m * 2048 + 16 * ((4 * j2 + q4) ^ (r16 & 7)));
+          for (int m = 0; m < MT; ++m) {
+            const uint4 a = *(const uint4*)(ta + m * 2048 + 16 * ((4 * j2 + q4) ^ (r16 & 7)));
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            if (j % JG == 0)
+            for (int n = 0; n < 4; ++n) {
+              if (j % JG == 0)
 #pragma unroll
-              for (int r = 0; r < 4; ++r) acc[m][n][r] *= ratio[n];
-            acc[m][n] = mfma16<_Float16>(a, b[n], acc[m][n]);
+                for (int r = 0; r < 4; ++r) acc[m][n][r] *= ratio[n];
+              acc[m][n] = mfma16<_Float16>(a, b[n], acc[m][n]);
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+              if (m == 1 + n * (MT - 1) / 4) {
+                if (jn % JG == 0) take_params(n, j != 3 || more);
+                bn[n] = dequant_word(w[n], nz[n], factors[n]);
+              }
           }
 #pragma unroll
-          for (int n = 0; n < 4; ++n)
-            if (m == 1 + n * (MT - 1) / 4) {
-              if (jn % JG == 0) take_params(n, j != 3 || more);
-              bn[n] = dequant_word(w[n], nz[n], factors[n]);
-            }
-        }
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          b[n] = bn[n];
-          if (jn % JG == 0) ratio[n] = next_ratio[n];
+          for (int n = 0; n < 4; ++n) {
+            b[n] = bn[n];
+            if (jn % JG == 0) ratio[n] = next_ratio[n];
+          }
         }
         // between a half's two sets the requests delay the MFMAs least
-        if (j2 == 0 && more) {
-          load_a(s + 2);
-          if (h == 0 && kb + 2 < kend) load_w(kb + 2);
+        if (j2 == 0) {
+          if constexpr (SPLIT) {
+            if (h == 0 && it + 1 < end) load_p(it + 1);
+            if (s + 2 < send) {
+              load_c(s + 2);
+              load_a(s + 2);
+            }
+          } else if (it + 1 < end) {
+            load_a(s + 2);
+            if (h == 0 && it + 2 < end) {
+              load_c(it + 2);
+              load_p(it + 2);
+            }
+          }
         }
       }
     }
@@ -290,19 +364,33 @@ k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
     for (int n = 0; n < 4; ++n)
 #pragma unroll
       for (int r = 0; r < 4; ++r) acc[m][n][r] *= unit[n] * kCodeScale;
-  if (un.parts > 1) {
-    floatx4* p = (floatx4*)parts + ((size_t)un.slot * 8 + wave) * (MT * 4 * 64) + lane;
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int n = 0; n < 4; ++n) p[(m * 4 + n) * 64] = acc[m][n];
-    return;
-  }
   __syncthreads();
+  const int ow = rb + (GATED ? 32 : 64) * wn;
+  if constexpr (!SPLIT) {
+    leave<GATED, MT>(acc, parts, un, wave, (float*)smem + wave * kEpWave, ep, t0 + wm * MT * 16, ow,
+                     lane);
+  } else {
+    // each half of the wavefronts hands half of its tokens' sums to the other
+    constexpr int H = MT / 2;
+    floatx4 keep[H][4];
+    floatx4* const mine = (floatx4*)smem + wave * (H * 4 * 64) + lane;
+    const floatx4* const other = (const floatx4*)smem + (wave ^ 4) * (H * 4 * 64) + lane;
 #pragma unroll
-  for (int m = 0; m < MT; m += 2)
-    finish32<GATED>(acc[m], acc[m + 1], (float*)smem + wave * kEpWave, ep,
-                    t0 + wm * MT * 16 + 16 * m, rb + (GATED ? 32 : 64) * wn, lane);
+    for (int m = 0; m < H; ++m)
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        mine[(m * 4 + n) * 64] = wm ? acc[m][n] : acc[H + m][n];
+        keep[m][n] = wm ? acc[H + m][n] : acc[m][n];
+      }
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < H; ++m)
+#pragma unroll
+      for (int n = 0; n < 4; ++n) keep[m][n] += other[(m * 4 + n) * 64];
+    __syncthreads();
+    leave<GATED, H>(keep, parts, un, wave, (float*)smem + wave * kEpWave, ep, t0 + wm * H * 16, ow,
+                    lane);
+  }
 }
 
 // Sums of a split tile's parts, in order; a block takes 32 tokens of one
@@ -329,8 +417,8 @@ static GemmPlan gemm_plan(W4Op op, const W4Args& a) {
   GemmPlan p;
   const int64_t outs = op == kOpGated ? a.O / 2 : a.O, per = op == kOpGated ? kBN / 2 : kBN;
   // groups of 64 and 32 change the unit two and four times per 128 columns:
-  // a step takes 1.2 and 1.45 times as long (512 x 4096 x 4096)
-  const float scale = a.group == 128 ? 1.0f : a.group == 64 ? 1.2f : 1.45f;
+  // a step takes 1.2 and 1.5 times as long (512 x 4096 x 4096)
+  const float scale = a.group == 128 ? 1.0f : a.group == 64 ? 1.2f : 1.5f;
   choose_tiles(a.N, (int)((outs + per - 1) / per), (int)(a.K / 128), kGemmCosts, scale, &p.mt,
                &p.sp);
   size_t at = 0;
@@ -349,10 +437,13 @@ static GemmPlan gemm_plan(W4Op op, const W4Args& a) {
 }
 size_t w4_gemm_workspace(W4Op op, const W4Args& a) { return gemm_plan(op, a).bytes; }
 
+// The tile is 32 MT tokens high.
 template <int GROUP, bool GATED, int MT>
 static hipError_t launch(const W4Args& a, const GemmPlan& p, hipStream_t stream) {
-  auto* kernel = &k_w4_gemm<GROUP, GATED, MT>;
-  const int lds = GemmLds<GROUP, MT>::kBytes;
+  constexpr bool SPLIT = MT <= 4;
+  constexpr int W = SPLIT ? 2 * MT : MT;  // token tiles of a wavefront
+  auto* kernel = &k_w4_gemm<GROUP, GATED, W, SPLIT>;
+  const int lds = GemmLds<GROUP, W, SPLIT>::kBytes;
   const hipError_t e =
       hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;

@@ -78,7 +78,7 @@ inline void choose_tiles(int64_t N, int no, int all_steps, const TileCosts& c, f
 // Measured with one tile per unit on 512 x 4096 x 4096, 1024 x 13824 -> 5120
 // for the products (w4_gemm.hip, 128 columns a step) and 128 x 4096 <- 11008
 // for the input gradient (w4_input_grad.hip, 64 packed rows a step).
-constexpr TileCosts kGemmCosts = {{1.5f, 2.1f, 2.55f, 3.1f}, {1, 1, 1, 1}};
+constexpr TileCosts kGemmCosts = {{2.2f, 3.05f, 2.4f, 2.95f}, {2, 2, 1, 1}};
 constexpr TileCosts kDxCosts = {{1.15f, 1.42f, 1.25f, 1.45f}, {2, 2, 1, 1}};
 
 struct SplitUnit {
