@@ -100,21 +100,23 @@ __device__ __forceinline__ void finish32(const floatx4 (&v0)[4], const floatx4 (
   asm volatile("" ::: "memory");
 }
 
-// A whole tile's values to the outputs, a part's to the workspace as they lie.
+// A part's sums to the workspace as they lie, a whole tile's values to the
+// outputs through LDS once no wavefront reads it any more.
 template <bool GATED, int MT>
 __device__ __forceinline__ void leave(const floatx4 (&acc)[MT][4], float* parts, const SplitUnit& un,
                                       int wave, float* own, const Epilogue& ep, int t0, int ob,
                                       int lane) {
-  if (un.parts == 1) {
+  if (un.parts > 1) {
+    floatx4* p = (floatx4*)parts + ((size_t)un.slot * 8 + wave) * (MT * 4 * 64) + lane;
 #pragma unroll
-    for (int m = 0; m < MT; m += 2) finish32<GATED>(acc[m], acc[m + 1], own, ep, t0 + 16 * m, ob, lane);
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < 4; ++n) p[(m * 4 + n) * 64] = acc[m][n];
     return;
   }
-  floatx4* p = (floatx4*)parts + ((size_t)un.slot * 8 + wave) * (MT * 4 * 64) + lane;
+  __syncthreads();
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int n = 0; n < 4; ++n) p[(m * 4 + n) * 64] = acc[m][n];
+  for (int m = 0; m < MT; m += 2) finish32<GATED>(acc[m], acc[m + 1], own, ep, t0 + 16 * m, ob, lane);
 }
 
 // Three stages of the activations and of the codes; the codes of 128 columns
@@ -155,7 +157,7 @@ k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
   // past the end loads the last block, which is not used.
   const int nkb = K >> 7;
   auto block_of = [&](int it) {
-    return __builtin_amdgcn_readfirstlane(SPLIT ? min(2 * it + wm, nkb - 1) : it);
+    return SPLIT ? __builtin_amdgcn_readfirstlane(min(2 * it + wm, nkb - 1)) : it;
   };
   const int lw = SPLIT ? wn : wave;  // the wavefront among those that load a block
 
@@ -169,7 +171,9 @@ k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
   }
   const char* a0 = (const char*)(A + (size_t)t0 * K);
   auto load_a = [&](int s) {  // half s & 1 of iteration s / 2
-    const char* base = a0 + (size_t)(2 * block_of(s >> 1) + (s & 1)) * 128;
+    // halves follow each other where blocks do
+    const int col = SPLIT ? 2 * block_of(s >> 1) + (s & 1) : s;
+    const char* base = a0 + col * 128;
 #pragma unroll
     for (int i = 0; i < AL; ++i)
       dma16(base, oa[i], lds + (s % 3) * L::kA + (wave * AL + i) * 1024);
@@ -301,12 +305,19 @@ k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
       // them: the next half's activations, without SPLIT also one block's
       // codes, as far as there are any.  No wavefront still reads the stages
       // requested next.
-      if (SPLIT ? s + 1 < send && s > 2 * un.s0 : it + h < end && it + 1 + h >= end)
-        wait_vm<AL>();
-      else if (!SPLIT && it + 1 + h < end)
-        wait_vm<AL + 2 + PL>();
-      else
-        wait_vm<0>();
+      if constexpr (SPLIT) {
+        if (s + 1 < send && s > 2 * un.s0)
+          wait_vm<AL>();
+        else
+          wait_vm<0>();
+      } else {
+        if (it + 1 + h < end)
+          wait_vm<AL + 2 + PL>();
+        else if (it + h < end)
+          wait_vm<AL>();
+        else
+          wait_vm<0>();
+      }
       __syncthreads();
       const char* ta = smem + (s % 3) * L::kA + (wm * MT * 16 + r16) * 128;
 #pragma unroll
@@ -364,13 +375,13 @@ k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
     for (int n = 0; n < 4; ++n)
 #pragma unroll
       for (int r = 0; r < 4; ++r) acc[m][n][r] *= unit[n] * kCodeScale;
-  __syncthreads();
   const int ow = rb + (GATED ? 32 : 64) * wn;
   if constexpr (!SPLIT) {
     leave<GATED, MT>(acc, parts, un, wave, (float*)smem + wave * kEpWave, ep, t0 + wm * MT * 16, ow,
                      lane);
   } else {
     // each half of the wavefronts hands half of its tokens' sums to the other
+    __syncthreads();
     constexpr int H = MT / 2;
     floatx4 keep[H][4];
     floatx4* const mine = (floatx4*)smem + wave * (H * 4 * 64) + lane;
@@ -387,7 +398,6 @@ k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
     for (int m = 0; m < H; ++m)
 #pragma unroll
       for (int n = 0; n < 4; ++n) keep[m][n] += other[(m * 4 + n) * 64];
-    __syncthreads();
     leave<GATED, H>(keep, parts, un, wave, (float*)smem + wave * kEpWave, ep, t0 + wm * H * 16, ow,
                     lane);
   }

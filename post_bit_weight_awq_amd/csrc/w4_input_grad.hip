@@ -65,20 +65,20 @@ __device__ __forceinline__ void store_dx(const floatx4 (&acc)[MT][4], const int*
     }
 }
 
-// A whole tile's values to dX, a part's to the workspace as they lie.
+// A part's sums to the workspace as they lie, a whole tile's values to dX.
 template <typename T, int MT>
 __device__ __forceinline__ void leave(const floatx4 (&acc)[MT][4], float* parts, const SplitUnit& un,
                                       int wave, const int* back, int N, int K, int t0, int col,
                                       int lane, T* dX) {
-  if (un.parts == 1) {
-    store_dx<T, MT>(acc, back, N, K, t0, col, lane, dX);
+  if (un.parts > 1) {
+    floatx4* p = (floatx4*)parts + ((size_t)un.slot * 8 + wave) * (MT * 4 * 64) + lane;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) p[(m * 4 + c) * 64] = acc[m][c];
     return;
   }
-  floatx4* p = (floatx4*)parts + ((size_t)un.slot * 8 + wave) * (MT * 4 * 64) + lane;
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) p[(m * 4 + c) * 64] = acc[m][c];
+  store_dx<T, MT>(acc, back, N, K, t0, col, lane, dX);
 }
 
 template <typename T, int GROUP, int MT, bool SPLIT>
@@ -103,7 +103,7 @@ k_w4_dx(const _Float16* __restrict__ A, int lda, const int* __restrict__ back, i
   // With SPLIT wavefronts 0-3 load and take the even steps, 4-7 the odd ones;
   // an odd one past the end loads the last step, which is not used.
   auto step_of = [&](int it) {
-    return __builtin_amdgcn_readfirstlane(SPLIT ? min(2 * it + wm, steps - 1) : it);
+    return SPLIT ? __builtin_amdgcn_readfirstlane(min(2 * it + wm, steps - 1)) : it;
   };
   const int lw = SPLIT ? wn : wave;  // the wavefront among those that load a step
 
@@ -137,7 +137,7 @@ k_w4_dx(const _Float16* __restrict__ A, int lda, const int* __restrict__ back, i
 
   const uint32_t lds = (uint32_t)(uintptr_t)smem;
   auto load_a = [&](int it) {
-    const char* base = a0 + (size_t)step_of(it) * 128;
+    const char* base = a0 + step_of(it) * 128;
 #pragma unroll
     for (int i = 0; i < AL; ++i)
       dma16(base, oa[i], lds + (it % 3) * L::kA + (wave * AL + i) * 1024);

@@ -122,6 +122,28 @@ def check_gated(awq, n, k, f, t, group, act):
     assert torch.equal(alone.view(torch.int16), h.t.view(torch.int16)), "H with and without pre"
 
 
+def odd_shapes():
+    """Sums of an odd number of 64- and 128-wide steps, whose last one has no
+    partner, in tiles of every height, whole and split; then any shapes."""
+    g = torch.Generator().manual_seed(31)
+    draw = lambda lo, hi: int(torch.randint(lo, hi, (), generator=g))
+    return ([(70, 512, 320), (100, 256, 192), (128, 640, 64), (128, 128, 64), (120, 1152, 1600), (66, 2176, 832),
+             (129, 384, 320), (250, 1408, 448), (90, 4224, 4160), (400, 896, 960)] +
+            [(draw(65, 700), 128 * draw(1, 20), draw(1, 900)) for _ in range(8)])
+
+
+@pytest.mark.parametrize("n,k,o", odd_shapes())
+@by_type
+def test_odd_numbers_of_steps(awq, n, k, o, t, group):
+    """The product, both forms' gradient for the input and the gated form."""
+    _say(f"odd steps {n}x{k},{o} {t} g{group}")
+    check_linear(awq, rnd(n, k, t, n), P.make_layer(o, k, group, n + k + o, "cuda"), t, "Y")
+    test_input_grad(awq, n, k, o, t, group)
+    half = (o + 1) // 2
+    check_gated(awq, n, k, half, t, group, "silu")
+    test_gated_backward(awq, n, k, half, t, group)
+
+
 @by_shape
 @by_type
 def test_gated(awq, n, k, o, t, group):
