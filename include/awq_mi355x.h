@@ -276,15 +276,18 @@ int awq_w4a16_matmul(const void* X, int64_t n_tokens, int64_t in_features, int64
  *   workspace:  scratch of at least the matching *_workspace_size bytes; its
  *               contents on entry do not matter.  A size of 0 means that none
  *               is used and workspace may be NULL; (size_t)-1 means that the
- *               arguments are refused (awq_last_error says why)
+ *               arguments are refused (awq_last_error says why).  It serves
+ *               one call at a time: calls or captured graphs that may run at
+ *               once need one each
  * All pointers are 16-byte aligned, all arrays dense and row-major; an output
  * or the workspace must not overlap an input or another output.  Sums are
  * held in binary32 from exact products of 16-bit values; outputs are rounded
  * once, to nearest even.  bf16 rows are brought to fp16 by a power of two per
- * row where a product needs it: values below 2^-32 of their row's largest
- * finite magnitude are then rounded at 2^-40 of it, others stay exact.
+ * row where a product needs it: values below 2^-31 of their row's largest
+ * finite magnitude may then be off by up to 2^-39 of it, others stay exact.
  * Infinities and NaN in a token's row follow IEEE arithmetic on the formula
- * and stay in that token's outputs.  Results do not depend on what runs
+ * and stay in that token's outputs; sums run in units of 512 steps and
+ * overflow where that leaves binary32's range.  Results do not depend on what runs
  * beside a call: sums have a fixed order and no atomics are used.
  * Errors: AWQ_ERR_INVALID_ARG for NULL, misaligned or overlapping pointers and
  * sizes out of range; AWQ_ERR_UNSUPPORTED for another group size, type or

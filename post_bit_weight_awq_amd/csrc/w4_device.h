@@ -105,6 +105,12 @@ __device__ __forceinline__ uint32_t half2_minus_bf16x2(uint32_t v, uint32_t b) {
                     (__bf16)(f16_hi(v) - __uint_as_float(b & 0xffff0000u))};
   return __builtin_bit_cast(uint32_t, r);
 }
+// Two bf16 values, 0 in the place of infinities and NaN.
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t v) {
+  if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
+  if ((v & 0x7f800000u) == 0x7f800000u) v &= 0xffffu;
+  return v;
+}
 
 template <typename T>
 __device__ __forceinline__ floatx4 mfma16(uint4 a, uint4 b, floatx4 c) {

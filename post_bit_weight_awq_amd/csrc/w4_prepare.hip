@@ -100,8 +100,8 @@ __device__ __forceinline__ uint32_t f32_to_bits(float v) {
 // dpre; the row that follows is dpre's.  Then, where `out` is given, the row as
 // fp16 with zeros behind it up to ld_out: fp16 as it is; bf16 times 2^e, e
 // from the row's largest finite magnitude (which lands in [2^14, 2^15)) and
-// back[row] = -e.  Values down to 2^-32 of the largest stay exact, smaller
-// ones are rounded at 2^-40 of it.
+// back[row] = -e.  Values down to 2^-31 of the largest stay exact,
+// smaller ones may be off by 2^-39 of it (half of fp16's last place, 2^-25).
 template <typename T, bool GATED, int N>
 __device__ __forceinline__ void prepare_row(const Prepare& a, int row) {
   constexpr bool SCALE = !__is_same(T, _Float16);

@@ -20,7 +20,9 @@
 //     LDS once, laid out by group, behind the first codes.
 //   * bf16 activations: differences are brought to bf16, exactly for integer
 //     zeros up to 240 in magnitude; where a wavefront sees others it multiplies
-//     the remainders too.
+//     the remainders too, by the finite activations: an infinity is whole in
+//     the first product (a difference is 0 in bf16 only if it is 0), and times
+//     a remainder of 0 it would make a NaN of it.
 #include "w4_internal.h"
 
 namespace awq {
@@ -174,7 +176,16 @@ k_w4_skinny(const T* __restrict__ X, int M, int K, int O, const char* __restrict
                   half2_minus_bf16x2(d[j].x, b[j].x), half2_minus_bf16x2(d[j].y, b[j].y),
                   half2_minus_bf16x2(d[j].z, b[j].z), half2_minus_bf16x2(d[j].w, b[j].w));
 #pragma unroll
-              for (int m = 0; m < MT; ++m) t[m] = mfma16<T>(x[g * JG + j][m], e, t[m]);
+              for (int m = 0; m < MT; ++m) {
+                uint4 a = x[g * JG + j][m];
+                // taken here each time: kept for both rows' tiles, the masked
+                // ones cost the common path registers (48 tokens gated, 5120
+                // -> 2 x 13824: 57 against 39 us)
+                asm volatile("" : "+v"(a.x), "+v"(a.y), "+v"(a.z), "+v"(a.w));
+                t[m] = mfma16<T>(make_uint4(finite_bf16x2(a.x), finite_bf16x2(a.y),
+                                            finite_bf16x2(a.z), finite_bf16x2(a.w)),
+                                 e, t[m]);
+              }
             }
           }
         }

@@ -253,6 +253,26 @@ def test_non_finite_tokens_stay_in_their_rows(awq, n, t, group):
         assert torch.equal(got[r][inf].to(P.F64), want[r][inf])
 
 
+@pytest.mark.parametrize("n", [1, 4, 30, 64, 300])
+@pytest.mark.parametrize("far", [False, True])
+@by_type
+def test_infinities_meet_any_zero(awq, n, far, t, group):
+    """Fractional zeros, or large ones that bf16 does not hold, beside rows of
+    integers: an infinity times a weight of either kind is an infinity, times 0
+    a NaN."""
+    _say(f"infinities {n} far={far} {t} g{group}")
+    k, o = 256, 100
+    q, s, z = P.make_layer(o, k, group, 16, "cuda", "far" if far else "any")
+    z[::3] = z[::3].round().clamp(0, 15)
+    x = rnd(n, k, t, 17)
+    x[0, 7], x[n // 2, 130], x[n - 1, 255] = float("inf"), float("-inf"), float("inf")
+    want = x.to(P.F64) @ P.weights(q, s, z).T
+    got = awq.awq_w4a16_linear(x, q, s, z, out_dtype=F32).to(P.F64)
+    assert torch.equal(got.isnan(), want.isnan())
+    inf = want.isinf()
+    assert torch.equal(got.isinf(), inf) and torch.equal(got[inf], want[inf])
+
+
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 @pytest.mark.parametrize("t", [F16, BF16])
 def test_gate_extremes(awq, t, act):
