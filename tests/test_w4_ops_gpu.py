@@ -503,3 +503,93 @@ def test_gradients_every_way(awq, n, k, o, t, group):
     ws_, es, wz, ez = P.param_grad(dy, x, *layer)
     close(ds.check(), ws_, P.rounded(ws_, es, F32), "dstep")
     close(dz.check(), wz, P.rounded(wz, ez, F32), "dzero")
+
+
+# ------------------------------------------------- arrays past 2^31 elements
+MANY = 1 << 20
+
+
+def on_gpu(n, m, t, seed, whole=False):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    if whole:
+        return torch.randint(-1, 2, (n, m), generator=g, device="cuda", dtype=torch.int8).to(t)
+    return torch.randn(n, m, generator=g, device="cuda", dtype=F32).to(t)
+
+
+def some_rows():
+    """The ends, and both sides of element 2^31 of 2304 columns."""
+    at = (1 << 31) // 2304
+    return torch.tensor([*range(4), *range(at - 3, at + 4), *range(MANY - 70, MANY)], device="cuda")
+
+
+@pytest.mark.parametrize("t,group", [(F16, 128), (BF16, 32)], ids=str)
+def test_products_past_2_31_elements(awq, t, group):
+    _say(f"many rows {t} g{group}")
+    rows = some_rows()
+    x = on_gpu(MANY, 128, t, 1)
+    layer = P.make_layer(2304, 128, group, 2, "cuda")
+    y = awq.awq_w4a16_linear(x, *layer)
+    w = P.weights(*layer)
+    want, e = P.linear(x[rows], w)
+    close(y[rows], want, P.rounded(want, e, t), "Y")
+    del y
+    h, pre = awq.awq_w4a16_gated(x, *layer, keep_pre=True)
+    want, e, wpre, epre = P.gated(x[rows], w, "silu")
+    close(h[rows], want, P.rounded(want, e, t), "H")
+    close(pre[rows], wpre, P.rounded(wpre, epre, t), "pre")
+    dx, dpre = awq.awq_w4a16_gated_backward(h, pre, *layer)
+    want, e = P.gated_grad(h[rows], pre[rows], "silu")
+    close(dpre[rows], want, P.rounded(want, e, t), "dpre")
+    want, e = P.input_grad(dpre[rows], w, t)
+    close(dx[rows], want, P.rounded(want, e, t), "dX from many rows")
+    del pre, dpre, h, dx
+    wide = P.make_layer(65, 2304, group, 3, "cuda")
+    dy = on_gpu(MANY, 65, t, 4)
+    dx = awq.awq_w4a16_input_grad(dy, *wide)
+    want, e = P.input_grad(dy[rows], P.weights(*wide), t)
+    close(dx[rows], want, P.rounded(want, e, t), "dX")
+
+
+@pytest.mark.parametrize("t,group", [(F16, 32), (BF16, 128)], ids=str)
+def test_param_grad_past_2_31_elements(awq, t, group):
+    """Values of -1, 0 and 1: every product and sum is a whole number that
+    binary32 holds, so any order gives the same."""
+    _say(f"many rows, parameters {t} g{group}")
+    layer = P.make_layer(2304, 128, group, 5, "cuda")
+    dy, x = on_gpu(MANY, 2304, t, 6, True), on_gpu(MANY, 128, t, 7, True)
+    ds, dz = awq.awq_w4a16_param_grad(dy, x, *layer)
+    d = torch.zeros(2304, 128, dtype=P.F64, device="cuda")
+    for i in range(0, MANY, 1 << 17):
+        d += dy[i:i + (1 << 17)].to(F32).T.contiguous() @ x[i:i + (1 << 17)].to(F32)
+    d = d.view(2304, 128 // group, group)
+    q = P.differences(layer[0], layer[2]).view(d.shape)
+    assert torch.equal(ds.to(P.F64), (d * q).sum(-1))
+    sums = d.sum(-1)
+    assert bool(((dz + layer[1].float() * sums.float()).abs() <= P.U32 * dz.abs()).all())
+
+
+@pytest.mark.parametrize("n,t", [(1, F16), (20, BF16), (100, F16), (600, BF16)], ids=str)
+def test_codes_past_2_31_bytes(awq, n, t):
+    _say(f"codes {n} {t}")
+    o, k, group = 131200, 32896, 128
+    g = torch.Generator(device="cuda").manual_seed(n)
+    q = torch.randint(-2 ** 31, 2 ** 31, (o, k // 8), generator=g, device="cuda", dtype=torch.int64).to(torch.int32)
+    s = (0.002 + 0.01 * torch.rand(o, k // group, generator=g, device="cuda")).to(F16)
+    z = torch.randint(0, 16, s.shape, generator=g, device="cuda").to(F16)
+    x = on_gpu(n, k, t, n + 1)
+    rows = torch.tensor([*range(3), 65599, 65600, 65601, *range(130556, 130562), *range(o - 70, o)], device="cuda")
+    w = P.weights(q[rows], s[rows], z[rows])
+    y = awq.awq_w4a16_linear(x, q, s, z)
+    want, e = P.linear(x, w)
+    close(y[:, rows], want, P.rounded(want, e, t), "Y")
+    words = torch.tensor([0, 1, k // 16, k // 8 - 1], device="cuda")
+    cols = (8 * words[:, None] + torch.arange(8, device="cuda")).flatten()
+    d = P.codes(q[:, words].contiguous()) - z[:, cols // group].to(P.F64)
+    dy = on_gpu(n, o, t, n + 2)
+    dx = awq.awq_w4a16_input_grad(dy, q, s, z)
+    want, e = P.input_grad(dy, d * s[:, cols // group].to(P.F64), t)
+    close(dx[:, cols], want, P.rounded(want, e, t), "dX")
+    ds, dz = awq.awq_w4a16_param_grad(dy, x, q, s, z)
+    ws_, es, wz, ez = P.param_grad(dy[:, rows], x, q[rows], s[rows], z[rows])
+    close(ds[rows], ws_, P.rounded(ws_, es, F32), "dstep")
+    close(dz[rows], wz, P.rounded(wz, ez, F32), "dzero")
