@@ -21,9 +21,11 @@
 //     LDS once, laid out by group, behind the first codes.
 //   * bf16 activations: differences are brought to bf16, exactly for integer
 //     zeros up to 240 in magnitude; where a wavefront sees others it multiplies
-//     the remainders too, by the finite activations: an infinity is whole in
-//     the first product (a difference is 0 in bf16 only if it is 0), and times
-//     a remainder of 0 it would make a NaN of it.
+//     the remainders too (16 tokens, 13824 -> 5120: 20 and 28 us), by the
+//     finite activations alone: an infinity is whole in the product with the
+//     bf16 differences (one is 0 only if it is 0 itself), and times a remainder
+//     of 0 it would make a NaN of it.  Masking the activations only where a
+//     sum shows that it has to be takes 28 us of the 39 with all masked.
 #include "w4_internal.h"
 
 namespace awq {
@@ -163,7 +165,7 @@ k_w4_skinny(const T* __restrict__ X, int M, int K, int O, const char* __restrict
         if constexpr (!__is_same(T, _Float16)) {
           const float zf = (float)z;
           const bool odd = !(fabsf(zf) <= 240.0f) || zf != __builtin_rintf(zf);
-          uint4 d[JG];
+          uint4 d[JG], e[JG];
 #pragma unroll
           for (int j = 0; j < JG; ++j) {
             d[j] = b[j];
@@ -171,22 +173,32 @@ k_w4_skinny(const T* __restrict__ X, int M, int K, int O, const char* __restrict
                               half2_to_bf16x2(d[j].z), half2_to_bf16x2(d[j].w));
           }
           if (__any(odd)) {
+            // as if all were finite first; sums that are not are taken again
+            bool again = false;
 #pragma unroll
             for (int j = 0; j < JG; ++j) {
-              const uint4 e = make_uint4(
+              e[j] = make_uint4(
                   half2_minus_bf16x2(d[j].x, b[j].x), half2_minus_bf16x2(d[j].y, b[j].y),
                   half2_minus_bf16x2(d[j].z, b[j].z), half2_minus_bf16x2(d[j].w, b[j].w));
 #pragma unroll
-              for (int m = 0; m < MT; ++m) {
-                uint4 a = x[g * JG + j][m];
-                // taken here each time: kept for both rows' tiles, the masked
-                // ones cost the common path registers (48 tokens gated, 5120
-                // -> 2 x 13824: 57 against 39 us)
-                asm volatile("" : "+v"(a.x), "+v"(a.y), "+v"(a.z), "+v"(a.w));
-                t[m] = mfma16<T>(make_uint4(finite_bf16x2(a.x), finite_bf16x2(a.y),
-                                            finite_bf16x2(a.z), finite_bf16x2(a.w)),
-                                 e, t[m]);
-              }
+              for (int m = 0; m < MT; ++m) t[m] = mfma16<T>(x[g * JG + j][m], e[j], t[m]);
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) again |= !(fabsf(t[m][r]) < __builtin_inff());
+            if (__any(again)) {
+#pragma unroll
+              for (int m = 0; m < MT; ++m) t[m] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+              for (int j = 0; j < JG; ++j)
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                  const uint4 a = x[g * JG + j][m];
+                  t[m] = mfma16<T>(make_uint4(finite_bf16x2(a.x), finite_bf16x2(a.y),
+                                              finite_bf16x2(a.z), finite_bf16x2(a.w)),
+                                   e[j], t[m]);
+                }
             }
           }
         }
