@@ -43,3 +43,44 @@ def test_chain_of_gradients(awq, n, k, f, group, t, act):
     chain = E.Chain(x, dh, layer, act)
     for name, got in (("x", dx), ("step", ds), ("zero", dz)):
         assert chain.agrees(name, got), name
+
+
+def close(got, want, bound, what):
+    got = got.to(P.F64)
+    ok = ((got - want).abs() <= bound) | (got == want)
+    if not bool(ok.all()):
+        at = (~ok).nonzero()[0].tolist()
+        worst = ((got - want).abs() / bound.clamp_min(1e-300))[~ok].max()
+        pytest.fail(f"{what}: {int((~ok).sum())} of {ok.numel()} off, worst {float(worst):.3g} bounds, first at {at}: "
+                    f"{float(got[tuple(at)])} for {float(want[tuple(at)])}")
+
+
+# ------------------------------------------------------------------- long sums
+@pytest.mark.parametrize("n,o", [(4096, 4096), (1024, 4096)])
+@pytest.mark.parametrize("steps", ["one", "equal", "none between"])
+def test_units_do_not_drift(awq, steps, n, o):
+    """What the first of 432 groups adds goes unchanged through the others, whose units are the same (one step for all
+    rows, one per row, groups without a step between).  Whole tiles, so that the sum is not split.  The first group's
+    32 products are positive: their sum and the last product by the unit are off by 33 half steps at most, and by
+    sqrt(33) of them or less in the mean square; twice that, as the matrix unit may cut a sum rather than round it."""
+    _say("drift", steps, n, o)
+    k, group = 13824, 32
+    ng = k // group
+    q, s, z = P.make_layer(o, k, group, 3, "cuda")
+    z.zero_()
+    g = torch.Generator().manual_seed(4)
+    own = ((1024 + torch.randint(0, 1024, (o, 1), generator=g)).to(torch.float64) * 2.0 ** -18).to(F16).cuda()
+    if steps == "one":
+        s.fill_(1312 * 2.0 ** -18)
+    else:
+        s.copy_(own.expand(o, ng))
+        if steps == "none between":
+            s[:, 1::2] = 0
+    x = torch.zeros(n, k, dtype=F16, device="cuda")
+    x[:, :group] = torch.rand(n, group, generator=g).to(F16).cuda()
+    got = awq.awq_w4a16_linear(x, q, s, z, out_dtype=F32).to(P.F64)
+    w = E.weights(q[:, :group // 8].contiguous(), s[:, :1].contiguous(), z[:, :1].contiguous())
+    want = x[:, :group].to(P.F64) @ w.T
+    off = (got - want) / want.clamp_min(1e-9)
+    assert float(off.abs().max()) <= 2 * 33 * P.U32
+    assert float(off.square().mean().sqrt()) <= 2 * 33 ** 0.5 * P.U32
