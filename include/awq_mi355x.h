@@ -353,7 +353,7 @@ int awq_w4a16_gated_backward(const void* dH, const void* pre, int dtype, int64_t
 /* Gradients of the group parameters, the codes frozen: with D = dY^T X,
  *   dstep[o, g] = sum over k in g of D[o, k] (q[o, k] - zero[o, g])
  *   dzero[o, g] = -step[o, g] * sum over k in g of D[o, k]
- * D is formed tile by tile and never stored.
+ * D is formed tile by tile and never stored; q - zero is taken in binary32.
  *   dY: [n_tokens, out_features], X: [n_tokens, in_features] dtype;
  *   dstep, dzero: [out_features, in_features / group_size] fp32, overwritten */
 size_t awq_w4a16_param_grad_workspace_size(int64_t n_tokens, int64_t in_features,

@@ -12,7 +12,8 @@
 // u ^ (t % 4 + 4 (t / 8 % 2)), so the eight row pieces of half a wavefront's
 // read lie in different banks.
 // Epilogue: 16 rows at a time through the wavefront's own LDS, each lane then
-// takes 32 columns of a row with their four words of codes.
+// takes 32 columns of a row with their four words of codes.  q - z is formed in
+// fp32, for any fp16 zero.
 // The result is linear in D, so a split tile's parts are split over tokens and
 // write their group sums, 256 x groups pairs, which a second launch adds.
 // Bound by MFMA issue: 4096 tokens, 13824 -> 5120, 0.49 ms (1.17 PFLOP/s);
@@ -156,10 +157,10 @@ k_w4_param_grad(const _Float16* __restrict__ dY, int ldy, const _Float16* __rest
     const int o = o0 + wm * 64 + m * 16 + er;
     const bool live = o < O && kc < K;
     uint4 w = make_uint4(0, 0, 0, 0);
-    uint32_t nz = 0;
+    float z = 0.0f;
     if (live) {
       w = *(const uint4*)(qw + (size_t)o * (K >> 3) + (kc >> 3));
-      nz = neg_zero_pair(zero16[(size_t)o * ng + g]);
+      z = (float)zero16[(size_t)o * ng + g];
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -172,15 +173,17 @@ k_w4_param_grad(const _Float16* __restrict__ dY, int ldy, const _Float16* __rest
     for (int j = 0; j < 4; ++j) {
       const float4 lo = *(const float4*)(ep + er * kPgEpRow + ec + 8 * j);
       const float4 hi = *(const float4*)(ep + er * kPgEpRow + ec + 8 * j + 4);
-      const uint4 d = dequant_word(word_of(w, j), nz);
-      ds = fmaf(f16_lo(d.x), lo.x, ds);
-      ds = fmaf(f16_hi(d.x), lo.y, ds);
-      ds = fmaf(f16_lo(d.y), lo.z, ds);
-      ds = fmaf(f16_hi(d.y), lo.w, ds);
-      ds = fmaf(f16_lo(d.z), hi.x, ds);
-      ds = fmaf(f16_hi(d.z), hi.y, ds);
-      ds = fmaf(f16_lo(d.w), hi.z, ds);
-      ds = fmaf(f16_hi(d.w), hi.w, ds);
+      // even columns' codes in the bytes of one word, odd ones' in the other's
+      const uint32_t even = word_of(w, j) & 0x0F0F0F0Fu, odd = (word_of(w, j) >> 4) & 0x0F0F0F0Fu;
+      auto diff = [&](uint32_t codes, int b) { return (float)((codes >> (8 * b)) & 0xffu) - z; };
+      ds = fmaf(diff(even, 0), lo.x, ds);
+      ds = fmaf(diff(odd, 0), lo.y, ds);
+      ds = fmaf(diff(even, 1), lo.z, ds);
+      ds = fmaf(diff(odd, 1), lo.w, ds);
+      ds = fmaf(diff(even, 2), hi.x, ds);
+      ds = fmaf(diff(odd, 2), hi.y, ds);
+      ds = fmaf(diff(even, 3), hi.z, ds);
+      ds = fmaf(diff(odd, 3), hi.w, ds);
       dz += ((lo.x + lo.y) + (lo.z + lo.w)) + ((hi.x + hi.y) + (hi.z + hi.w));
     }
     asm volatile("" ::: "memory");
@@ -190,7 +193,6 @@ k_w4_param_grad(const _Float16* __restrict__ dY, int ldy, const _Float16* __rest
       dz += __shfl_xor(dz, d, 64);
     }
     if (!live || (lane & (GROUP / 32 - 1))) continue;
-    ds *= kCodeScale;
     if (un.parts > 1) {
       float* p = parts + ((size_t)un.slot * 256 + wm * 64 + m * 16 + er) * (2 * GT) +
                  2 * ((wn * 128 + ec) / GROUP);

@@ -39,3 +39,27 @@ def test_the_directional_check_bites(n, k, f, group, t, act):
         for bad in [0 * got, -got, 1.05 * got, 0.95 * got] + mistakes[name]:
             if not torch.equal(bad, got):
                 assert not chain.agrees(name, bad), name
+
+
+def rnd(n, m, t, seed, scale=1.0):
+    """test_w4_ops_gpu.py's inputs, on the CPU."""
+    g = torch.Generator().manual_seed(seed)
+    x = scale * torch.randn(n, m, generator=g)
+    x[:, torch.rand(m, generator=g) < 0.02] *= 16
+    return x.to(t)
+
+
+TYPES = (torch.float16, torch.bfloat16)
+
+
+@pytest.mark.parametrize("n,k,o", E.ROUNDED_PARAM_GRAD, ids=str)
+@pytest.mark.parametrize("t", TYPES, ids=str)
+def test_rounded_reference_of_param_grad(n, k, o, t):
+    """The definition's own value, rounded once to binary32, is out of the named cases' bounds."""
+    for group in E.ROUNDED_PARAM_GRAD[n, k, o]:
+        layer = P.make_layer(o, k, group, n + k + o, zeros="any")
+        dy, x = rnd(n, o, t, n + 5, 0.01), rnd(n, k, t, n + 6)
+        want, e, _, _ = P.param_grad(dy, x, *layer)
+        d = (dy.to(P.F64).T @ x.to(P.F64)).view(o, k // group, group)
+        right = (d * E.differences(layer[0], layer[2]).view(d.shape)).sum(-1).float().to(P.F64)
+        assert bool(((right - want).abs() > P.rounded(want, e, torch.float32)).any()), group

@@ -84,3 +84,47 @@ def test_units_do_not_drift(awq, steps, n, o):
     off = (got - want) / want.clamp_min(1e-9)
     assert float(off.abs().max()) <= 2 * 33 * P.U32
     assert float(off.square().mean().sqrt()) <= 2 * 33 ** 0.5 * P.U32
+
+
+# ------------------------------------------------------------ zeros of any value
+ODD_ZEROS = [0.001, -0.001, 2.0 ** -24, 2.998, 3.002, 0.3333, 1.001, 7.004, 7.996, 11.99, 14.99, -0.3, -5.7, -16.98,
+             17.02, 20.3, 31.97, 240.5, 300.6, 1023.5, 2032, 2040, -2047, 2049, 5000, -5008, 65504, -65504, 0, 15]
+
+
+def odd_layer(o, k, group, seed):
+    """Zeros of every kind, a different one per group, among them a row of fractions in 0..15 and one of whole ones."""
+    q, s, z = P.make_layer(o, k, group, seed, "cuda")
+    g = torch.Generator().manual_seed(seed)
+    v = torch.tensor(ODD_ZEROS, dtype=torch.float64)
+    z.copy_(v[torch.randint(0, len(v), z.shape, generator=g)].to(F16))
+    z[0] = (15 * torch.rand(z.shape[1], generator=g)).to(F16).cuda()
+    z[1] = 7
+    return q, s, z
+
+
+def size(q, z, k):
+    """|q - z| and what a split of z into a part that the codes' differences hold and a remainder adds: at most a
+    quarter, beyond 240 |z|."""
+    z = P.spread(z, k).abs()
+    return q.abs() + torch.where(z > 240, 2 * z, 0.25)
+
+
+BY_TYPE = pytest.mark.parametrize("t,group", [(F16, 128), (F16, 64), (F16, 32), (BF16, 128), (BF16, 64), (BF16, 32)],
+                                  ids=lambda v: str(v).replace("torch.", ""))
+
+
+@pytest.mark.parametrize("n,k,o", [(1, 256, 300), (3, 640, 17), (33, 512, 130), (129, 384, 193), (600, 1024, 260)])
+@BY_TYPE
+def test_param_grad_with_any_zero(awq, n, k, o, t, group):
+    _say(f"dstep {n}x{k},{o} {t} g{group}")
+    layer = odd_layer(o, k, group, n + k)
+    g = torch.Generator().manual_seed(n)
+    dy, x = (0.01 * torch.randn(n, o, generator=g)).to(t).cuda(), torch.randn(n, k, generator=g).to(t).cuda()
+    ds, dz = awq.awq_w4a16_param_grad(dy, x, *layer)
+    d = (dy.to(P.F64).T @ x.to(P.F64)).view(o, k // group, group)
+    da = (dy.to(P.F64).abs().T @ x.to(P.F64).abs()).view(d.shape)
+    q = E.differences(layer[0], layer[2]).view(d.shape)
+    e = 2 * (n + group + 64) * P.U32
+    close(ds, (d * q).sum(-1), e * (da * q.abs()).sum(-1) + 2.0 ** -149, "dstep")
+    s = layer[1].to(P.F64)
+    close(dz, -s * d.sum(-1), e * s * da.sum(-1) + 2.0 ** -149, "dzero")

@@ -67,3 +67,16 @@ def a_chain(n, k, f, group, t, act, seed, dev="cpu"):
     x = torch.randn(n, k, generator=g).to(t).to(dev)
     dh = (0.1 * torch.randn(n, f, generator=g)).to(t).to(dev)
     return layer, x, dh
+
+
+#: Cases of test_w4_ops_gpu.py whose reference value is not the definition's: w4_plain.differences rounds q - zero to
+#: 11 bits, which takes a result with fractional zeros further off than the case's own bound (it counts binary32's
+#: roundings alone).  An operator that holds zeros whole fails them; test_w4_exact.py shows it for each.
+ALL = (128, 64, 32)
+ROUNDED_PARAM_GRAD = {(1, 128, 1): (64,), (1, 512, 512): ALL, (1, 1152, 333): ALL, (3, 640, 17): ALL, (5, 384, 96): ALL,
+                      (17, 256, 65): ALL, (33, 640, 130): ALL, (65, 128, 257): (64, 32), (129, 1280, 193): (64, 32)}
+
+
+def holds_rounded_zeros(test, p):
+    """Whether the case `p` (its parameters) of a test is one of them."""
+    return test == "test_param_grad" and p["group"] in ROUNDED_PARAM_GRAD.get((p["n"], p["k"], p["o"]), ())
