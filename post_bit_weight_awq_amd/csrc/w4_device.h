@@ -53,6 +53,25 @@ __device__ __forceinline__ uint32_t neg_zero_pair(_Float16 z) {
   return b | (b << 16);
 }
 
+// A zero as high + low: q - high is exact in 16 bits for all 16 codes (BF16: in
+// bf16's 8 bits, else in fp16's 11) and is 0 or of the other sign only where
+// q - z is, so that an infinity times it is what the formula gives; low
+// multiplies the tokens' sums over the group, in fp32.
+//   |z| <= 17: |q - high| <= 32, so high is a multiple of 2^-6 (2^-3), the lower
+//   neighbour's odd one where z is none: never a code unless z is one.
+//   Beyond, no code is near: a whole number, of magnitude up to 2032 (240).
+struct ZeroParts {
+  float high, low;
+};
+template <bool BF16>
+__device__ __forceinline__ ZeroParts split_zero(float z) {
+  constexpr float kParts = BF16 ? 8.0f : 64.0f, kTop = BF16 ? 240.0f : 2032.0f;
+  const float v = z * kParts, f = floorf(v);
+  const int i = (int)f | (f != v ? 1 : 0);
+  const float high = fabsf(z) <= 17.0f ? (float)i * (1.0f / kParts)
+                                       : fminf(fmaxf(__builtin_rintf(z), -kTop), kTop);
+  return {high, z - high};
+}
 // The factors of a nibble in bits 0-3 of the low half and bits 4-7 of the
 // high one, as fp16 pairs.
 constexpr uint32_t kNibbleFactors = 0x68007800u;
@@ -92,26 +111,12 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int j) {
   return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
 }
 
-// Packed fp16 to packed bf16, rounded to nearest even, and what that
-// rounding leaves.
+// Packed fp16 to packed bf16, rounded to nearest even.
 __device__ __forceinline__ uint32_t half2_to_bf16x2(uint32_t v) {
   typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
   const bf16x2 r = {(__bf16)f16_lo(v), (__bf16)f16_hi(v)};
   return __builtin_bit_cast(uint32_t, r);
 }
-__device__ __forceinline__ uint32_t half2_minus_bf16x2(uint32_t v, uint32_t b) {
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  const bf16x2 r = {(__bf16)(f16_lo(v) - __uint_as_float(b << 16)),
-                    (__bf16)(f16_hi(v) - __uint_as_float(b & 0xffff0000u))};
-  return __builtin_bit_cast(uint32_t, r);
-}
-// Two bf16 values, 0 in the place of infinities and NaN.
-__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t v) {
-  if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
-  if ((v & 0x7f800000u) == 0x7f800000u) v &= 0xffffu;
-  return v;
-}
-
 template <typename T>
 __device__ __forceinline__ floatx4 mfma16(uint4 a, uint4 b, floatx4 c) {
   if constexpr (sizeof(T) == 2 && __is_same(T, _Float16))

@@ -19,13 +19,18 @@
 //     formed by itself and enters the output with one fp32 fma by its step.
 //   * Steps and zeros of the block's rows are contiguous; they are copied to
 //     LDS once, laid out by group, behind the first codes.
-//   * bf16 activations: differences are brought to bf16, exactly for integer
-//     zeros up to 240 in magnitude; where a wavefront sees others it multiplies
-//     the remainders too (16 tokens, 13824 -> 5120: 20 and 28 us), by the
-//     finite activations alone: an infinity is whole in the product with the
-//     bf16 differences (one is 0 only if it is 0 itself), and times a remainder
-//     of 0 it would make a NaN of it.  Masking the activations only where a
-//     sum shows that it has to be takes 28 us of the 39 with all masked.
+//   * A zero is taken as a high part, from which the codes' differences are
+//     exact (in bf16 for bf16 activations), and a low one, 0 for the zeros that
+//     packing writes.  A block that has any other runs a second form of the
+//     loop, which adds the tokens' sums over the group, one MFMA by ones for
+//     both tiles, times the low parts (16 tokens, 13824 -> 5120 in bf16: 18.7
+//     us with whole zeros, 21.4 with fractional ones; one token, 5120 -> 15360
+//     in fp16: 10.5 and 12.3).  The ones are 2^-9, the
+//     differences' unit: a sum of 128 finite values stays finite.  One that is
+//     not holds an infinity or a NaN, which the product of the high parts has
+//     whole, and is left out.
+#include <type_traits>
+
 #include "w4_internal.h"
 
 namespace awq {
@@ -52,6 +57,7 @@ __global__ void __launch_bounds__(512, 2)
 k_w4_skinny(const T* __restrict__ X, int M, int K, int O, const char* __restrict__ qw,
             const _Float16* __restrict__ step16, const _Float16* __restrict__ zero16, Epilogue ep,
             int off_ring) {
+  constexpr bool BF = !__is_same(T, _Float16);
   constexpr int WR = 8 / KS, R = 32 * WR;  // packed rows per block
   constexpr int GPB = 128 / GROUP;         // groups per block of 128 columns
   constexpr int JG = 4 / GPB;              // MFMAs per group
@@ -108,110 +114,132 @@ k_w4_skinny(const T* __restrict__ X, int M, int K, int O, const char* __restrict
       dma16((const char*)X + 256 * kb, ox[i], l + kg * XB + (FEW ? 0 : (wr + i * WR) * 1024));
   };
   load(0);
-  for (int e = tid; e < R * ng; e += 512) {
-    const int i = e / ng, g = e - i * ng;
+  uint16_t part = 0;  // of the zeros: bits of what they have behind the point,
+  _Float16 top = 0;   // and the largest magnitude
+  const int di = 512 / ng, dg = 512 - di * ng;
+  for (int e = tid, i = tid / ng, g = tid - i * ng; e < R * ng; e += 512) {
     const size_t at = (size_t)row_of(i) * ng + g;
+    const _Float16 z = zero16[at];
+    part |= __builtin_bit_cast(uint16_t, (_Float16)(z - __builtin_floorf16(z)));
+    top = __builtin_fmaxf16(top, __builtin_fabsf16(z));
     pairs[g * R + i] = (uint32_t)__builtin_bit_cast(uint16_t, step16[at]) |
-                       ((uint32_t)__builtin_bit_cast(uint16_t, zero16[at]) << 16);
+                       ((uint32_t)__builtin_bit_cast(uint16_t, z) << 16);
+    i += di;
+    g += dg;
+    if (g >= ng) {
+      g -= ng;
+      ++i;
+    }
   }
+  // whether any of the block is to be taken apart: each wavefront's answer goes
+  // through its own codes of the second stage, requested behind the loop's
+  // first barrier or, without one, this one
+  const bool odd = __any(part != 0 || !((float)top <= (BF ? 240.0f : 2032.0f)));
+  int* const seen = (int*)(smem + off_ring + STAGE + KS * XB);
+  if (lane == 0) seen[512 * wave] = odd;
   __syncthreads();
+  int apart = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) apart |= seen[512 * i];
+  apart = __builtin_amdgcn_readfirstlane(apart);
+  if (WR == 1) __syncthreads();
 
   floatx4 acc[MT][2];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int u = 0; u < 2; ++u) acc[m][u] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int it = 0; it < its; ++it) {
-    // the stage has landed, and every wavefront of the group has read the
-    // other one (with WR = 1 its own reads have returned)
-    wait_vm<0>();
-    if (WR > 1)
-      __syncthreads();
-    else
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if (it + 1 < its) load(it + 1);
-    const int kb = it * KS + kg;
-    const char* st = smem + off_ring + (it & 1) * STAGE;
-    if (kb >= nkb) continue;
-    const int tx = FEW ? r16 & 3 : r16;  // rows past the fourth repeat it
-    const char* px = st + kg * XB + tx * 256;
-    const char* pc = st + KS * XB + wave * 2048 + r16 * 64 + 4 * q4;
-    uint32_t w[2][4];
+  auto sum = [&](auto parted) {
+    for (int it = 0; it < its; ++it) {
+      // the stage has landed, and every wavefront of the group has read the
+      // other one (with WR = 1 its own reads have returned)
+      wait_vm<0>();
+      if (WR > 1)
+        __syncthreads();
+      else
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (it + 1 < its) load(it + 1);
+      const int kb = it * KS + kg;
+      const char* st = smem + off_ring + (it & 1) * STAGE;
+      if (kb >= nkb) continue;
+      const int tx = FEW ? r16 & 3 : r16;  // rows past the fourth repeat it
+      const char* px = st + kg * XB + tx * 256;
+      const char* pc = st + KS * XB + wave * 2048 + r16 * 64 + 4 * q4;
+      uint32_t w[2][4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          w[u][j] = *(const uint32_t*)(pc + u * 1024 + 16 * (j ^ (r16 >> 2)));
+      uint4 x[4][MT];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        w[u][j] = *(const uint32_t*)(pc + u * 1024 + 16 * (j ^ (r16 >> 2)));
-    uint4 x[4][MT];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+        for (int m = 0; m < MT; ++m)
+          x[j][m] = *(const uint4*)(px + m * 4096 + 16 * ((4 * j + q4) ^ tx));
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-        x[j][m] = *(const uint4*)(px + m * 4096 + 16 * ((4 * j + q4) ^ tx));
+      for (int g = 0; g < GPB; ++g) {
+        float stp[2];
+        _Float16 z[2];
 #pragma unroll
-    for (int g = 0; g < GPB; ++g)
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t sz = pairs[(kb * GPB + g) * R + 32 * wr + 16 * u + r16];
+          z[u] = __builtin_bit_cast(_Float16, (uint16_t)(sz >> 16));
+          stp[u] = f16_lo(sz) * kCodeScale;
+        }
+        if constexpr (parted) {
+          constexpr uint32_t kOnes = BF ? 0x3b003b00u : 0x18001800u;  // 2^-9
+          const uint4 ones = make_uint4(kOnes, kOnes, kOnes, kOnes);
+          float low[2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint32_t sz = pairs[(kb * GPB + g) * R + 32 * wr + 16 * u + r16];
-        const _Float16 z = __builtin_bit_cast(_Float16, (uint16_t)(sz >> 16));
-        const uint32_t nz = neg_zero_pair(z);
-        const float stp = f16_lo(sz) * kCodeScale;
-        floatx4 t[MT];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) t[m] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-        uint4 b[JG];
-#pragma unroll
-        for (int j = 0; j < JG; ++j) b[j] = dequant_word(w[u][g * JG + j], nz);
-        if constexpr (!__is_same(T, _Float16)) {
-          const float zf = (float)z;
-          const bool odd = !(fabsf(zf) <= 240.0f) || zf != __builtin_rintf(zf);
-          uint4 d[JG], e[JG];
-#pragma unroll
-          for (int j = 0; j < JG; ++j) {
-            d[j] = b[j];
-            b[j] = make_uint4(half2_to_bf16x2(d[j].x), half2_to_bf16x2(d[j].y),
-                              half2_to_bf16x2(d[j].z), half2_to_bf16x2(d[j].w));
+          for (int u = 0; u < 2; ++u) {
+            const ZeroParts p = split_zero<BF>((float)z[u]);
+            z[u] = (_Float16)p.high;
+            low[u] = -p.low * stp[u];
           }
-          if (__any(odd)) {
-            // as if all were finite first; sums that are not are taken again
-            bool again = false;
 #pragma unroll
-            for (int j = 0; j < JG; ++j) {
-              e[j] = make_uint4(
-                  half2_minus_bf16x2(d[j].x, b[j].x), half2_minus_bf16x2(d[j].y, b[j].y),
-                  half2_minus_bf16x2(d[j].z, b[j].z), half2_minus_bf16x2(d[j].w, b[j].w));
+          for (int m = 0; m < MT; ++m) {
+            floatx4 s = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-              for (int m = 0; m < MT; ++m) t[m] = mfma16<T>(x[g * JG + j][m], e[j], t[m]);
-            }
+            for (int j = 0; j < JG; ++j) s = mfma16<T>(x[g * JG + j][m], ones, s);
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int r = 0; r < 4; ++r) {
+              const float v = fabsf(s[r]) < INFINITY ? s[r] : 0.0f;
 #pragma unroll
-              for (int r = 0; r < 4; ++r) again |= !(fabsf(t[m][r]) < __builtin_inff());
-            if (__any(again)) {
-#pragma unroll
-              for (int m = 0; m < MT; ++m) t[m] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-              for (int j = 0; j < JG; ++j)
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                  const uint4 a = x[g * JG + j][m];
-                  t[m] = mfma16<T>(make_uint4(finite_bf16x2(a.x), finite_bf16x2(a.y),
-                                              finite_bf16x2(a.z), finite_bf16x2(a.w)),
-                                   e[j], t[m]);
-                }
+              for (int u = 0; u < 2; ++u) acc[m][u][r] = fmaf(low[u], v, acc[m][u][r]);
             }
           }
         }
 #pragma unroll
-        for (int j = 0; j < JG; ++j)
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t nz = neg_zero_pair(z[u]);
+          floatx4 t[MT];
 #pragma unroll
-          for (int m = 0; m < MT; ++m) t[m] = mfma16<T>(x[g * JG + j][m], b[j], t[m]);
+          for (int m = 0; m < MT; ++m) t[m] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+          uint4 b[JG];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+          for (int j = 0; j < JG; ++j) {
+            b[j] = dequant_word(w[u][g * JG + j], nz);
+            if constexpr (BF)
+              b[j] = make_uint4(half2_to_bf16x2(b[j].x), half2_to_bf16x2(b[j].y),
+                                half2_to_bf16x2(b[j].z), half2_to_bf16x2(b[j].w));
+          }
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[m][u][r] = fmaf(stp, t[m][r], acc[m][u][r]);
+          for (int j = 0; j < JG; ++j)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) t[m] = mfma16<T>(x[g * JG + j][m], b[j], t[m]);
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[m][u][r] = fmaf(stp[u], t[m][r], acc[m][u][r]);
+        }
       }
-  }
+    }
+  };
+  if (apart)
+    sum(std::true_type{});
+  else
+    sum(std::false_type{});
   __syncthreads();
 
   // the groups' sums: register r of lane l is token 4 (l / 16) + r, row l % 16

@@ -63,3 +63,14 @@ def test_rounded_reference_of_param_grad(n, k, o, t):
         d = (dy.to(P.F64).T @ x.to(P.F64)).view(o, k // group, group)
         right = (d * E.differences(layer[0], layer[2]).view(d.shape)).sum(-1).float().to(P.F64)
         assert bool(((right - want).abs() > P.rounded(want, e, torch.float32)).any()), group
+
+
+@pytest.mark.parametrize("n", E.ROUNDED_LINEAR_ZEROS)
+@pytest.mark.parametrize("t", TYPES, ids=str)
+@pytest.mark.parametrize("group", E.ALL)
+def test_rounded_reference_of_linear_zeros(n, t, group):
+    layer = P.make_layer(200, 512, group, 5, zeros="any")
+    x = rnd(n, 512, t, 9)
+    want, e = P.linear(x, P.weights(*layer))
+    right = (x.to(P.F64) @ E.weights(*layer).T).float().to(P.F64)
+    assert bool(((right - want).abs() > P.rounded(want, e, torch.float32)).any())

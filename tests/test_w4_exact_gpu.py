@@ -113,6 +113,78 @@ BY_TYPE = pytest.mark.parametrize("t,group", [(F16, 128), (F16, 64), (F16, 32), 
                                   ids=lambda v: str(v).replace("torch.", ""))
 
 
+@pytest.mark.parametrize("n", [1, 4, 12, 30, 48])
+@BY_TYPE
+def test_each_weight_alone(awq, n, t, group):
+    """One column per token, all others 0: the output is one weight times a power of two, the fp32 output off by the
+    few roundings of its own operations."""
+    _say(f"each weight {n} {t} g{group}")
+    k, o = 384, 75
+    layer = odd_layer(o, k, group, n + group)
+    x = torch.zeros(n, k, dtype=t, device="cuda")
+    at = (torch.arange(n, device="cuda") * 7 + 3) % k
+    x[torch.arange(n, device="cuda"), at] = torch.exp2((torch.arange(n, device="cuda") % 5 - 2).float()).to(t)
+    d, s = E.differences(layer[0], layer[2]), P.spread(layer[1], k)
+    xd = x.to(P.F64)
+    close(awq.awq_w4a16_linear(x, *layer, out_dtype=F32), xd @ (d * s).T,
+          8 * P.U32 * (xd.abs() @ (size(d, layer[2], k) * s).T), "Y")
+
+
+@pytest.mark.parametrize("n,k,o", [(1, 512, 200), (3, 1152, 40), (16, 640, 333), (40, 512, 200), (64, 256, 20481)])
+@BY_TYPE
+def test_products_with_any_zero(awq, n, k, o, t, group):
+    _say(f"any zero {n}x{k}->{o} {t} g{group}")
+    layer = odd_layer(2 * o, k, group, n + o)
+    layer[2].clamp_(-300, 300)
+    g = torch.Generator().manual_seed(n)
+    x = torch.randn(n, k, generator=g).to(t).cuda()
+    w = E.weights(*layer)
+    xd = x.to(P.F64)
+    sums = xd.abs() @ (size(E.differences(layer[0], layer[2]), layer[2], k) * P.spread(layer[1], k)).T
+    want, e = xd @ w.T, 2 * (k + 128) * P.U32 * sums
+    close(awq.awq_w4a16_linear(x, *layer, out_dtype=F32), want, e, "fp32")
+    close(awq.awq_w4a16_linear(x, *layer), want, P.rounded(want, e, t), "16 bits")
+    h, pre = awq.awq_w4a16_gated(x, *layer, keep_pre=True)
+    close(pre, want, P.rounded(want, e, t), "pre")
+    a, u, ea, eu = P.act(want[:, :o], "silu")[0], want[:, o:], e[:, :o], e[:, o:]
+    ea = 1.13 * ea + 16 * P.U32 * want[:, :o].abs()
+    close(h, a * u, P.rounded(a * u, (a.abs() + ea) * eu + ea * u.abs() + 2 * P.U32 * (a * u).abs(), t), "H")
+
+
+@pytest.mark.parametrize("n", [1, 4, 30])
+@BY_TYPE
+def test_infinities_beside_zeros_next_to_a_code(awq, n, t, group):
+    """An infinity times q - z is one of q - z's sign, however near z lies to q, and NaN for q = z alone."""
+    _say(f"infinities next to codes {n} {t} g{group}")
+    k, o = 256, 96
+    q, s, z = P.make_layer(o, k, group, 16, "cuda")
+    off = torch.tensor([2.0 ** -7, -2.0 ** -7, 2.0 ** -9, -2.0 ** -9, 0], device="cuda")
+    z.copy_((z.float() + off[torch.arange(o, device="cuda") % 5][:, None]).to(F16))
+    x = torch.randn(n, k, generator=torch.Generator().manual_seed(n)).to(t).cuda()
+    x[0, 7], x[n // 2, 130], x[n - 1, 255] = float("inf"), float("-inf"), float("inf")
+    want = x.to(P.F64) @ E.weights(q, s, z).T
+    got = awq.awq_w4a16_linear(x, q, s, z, out_dtype=F32).to(P.F64)
+    assert torch.equal(got.isnan(), want.isnan())
+    inf = want.isinf()
+    assert torch.equal(got.isinf(), inf) and torch.equal(got[inf], want[inf])
+
+
+def test_large_finite_rows_keep_their_remainders(awq):
+    """Sums of a group past binary32's end, within it in the operators' unit of 512 steps: so are the token sums that a
+    zero's remainder multiplies."""
+    _say("large finite rows")
+    k, o = 256, 64
+    q, s, z = P.make_layer(o, k, 128, 18, "cuda", "any")
+    s.fill_(2.0 ** -24)
+    for n in (1, 20):
+        x = torch.full((n, k), 6.0e37, dtype=BF16, device="cuda")
+        x[:, 1::2] = 4.0e37
+        w = E.weights(q, s, z)
+        xd = x.to(P.F64)
+        e = 2 * (k + 128) * P.U32 * (xd @ (size(E.differences(q, z), z, k) * P.spread(s, k)).T)
+        close(awq.awq_w4a16_linear(x, q, s, z, out_dtype=F32), xd @ w.T, e, n)
+
+
 @pytest.mark.parametrize("n,k,o", [(1, 256, 300), (3, 640, 17), (33, 512, 130), (129, 384, 193), (600, 1024, 260)])
 @BY_TYPE
 def test_param_grad_with_any_zero(awq, n, k, o, t, group):

@@ -75,8 +75,11 @@ def a_chain(n, k, f, group, t, act, seed, dev="cpu"):
 ALL = (128, 64, 32)
 ROUNDED_PARAM_GRAD = {(1, 128, 1): (64,), (1, 512, 512): ALL, (1, 1152, 333): ALL, (3, 640, 17): ALL, (5, 384, 96): ALL,
                       (17, 256, 65): ALL, (33, 640, 130): ALL, (65, 128, 257): (64, 32), (129, 1280, 193): (64, 32)}
+ROUNDED_LINEAR_ZEROS = (7, 40)
 
 
 def holds_rounded_zeros(test, p):
     """Whether the case `p` (its parameters) of a test is one of them."""
+    if test == "test_linear_zeros":
+        return p["zeros"] == "any" and p["n"] in ROUNDED_LINEAR_ZEROS
     return test == "test_param_grad" and p["group"] in ROUNDED_PARAM_GRAD.get((p["n"], p["k"], p["o"]), ())
