@@ -269,10 +269,9 @@ int awq_w4a16_matmul(const void* X, int64_t n_tokens, int64_t in_features, int64
  *   group_size: 32, 64 or 128
  *   qweight:    [rows, in_features / 8] int32, nibble j of word w = column 8w + j
  *   step16, zero16: [rows, in_features / group_size] fp16, finite; zero may
- *               have any value (awq_pack writes integers).  q - zero is held in
- *               fp16 in units of 2^-9: exact for integer zeros of magnitude up
- *               to 2032, else rounded once to 11 bits or, below 2^-5, to a
- *               multiple of 2^-15 (a zero below 2^-5 is rounded so first)
+ *               have any value (awq_pack writes integers).  The products and
+ *               dstep take q - zero without rounding it; awq_w4a16_input_grad
+ *               says what the gradients for the input do
  *   workspace:  scratch of at least the matching *_workspace_size bytes; its
  *               contents on entry do not matter.  A size of 0 means that none
  *               is used and workspace may be NULL; (size_t)-1 means that the
@@ -327,7 +326,9 @@ int awq_w4a16_gated(const void* X, int dtype, int64_t n_tokens, int64_t in_featu
 
 /* dX[t, k] = sum_o dY[t, o] W[o, k], the packed codes frozen.  Each W[o, k]
  * is rounded to fp16 (the step varies along the sum, so it cannot be applied
- * to sums of exact products).
+ * to sums of exact products), after q - zero was, which is exact for integer
+ * zeros of magnitude up to 2032, else off by 2^-12 of itself or, from a zero
+ * below 2^-5, by 2^-16 more.
  *   dY: [n_tokens, out_features] dtype; dX: [n_tokens, in_features] dtype */
 size_t awq_w4a16_input_grad_workspace_size(int64_t n_tokens, int64_t in_features,
                                            int64_t out_features, int group_size, int dtype);

@@ -21,6 +21,11 @@
 //     Ratios are rounded to nearest: 1 between equal steps, so that a row of
 //     them keeps its first sums (a reciprocal's rounding, always to one side,
 //     took 5e-5 of them in 432 groups).
+//   * A zero is taken as a high part, which the differences hold exactly, and a
+//     low one, 0 for the zeros that packing writes: where there are others, fp32
+//     MFMAs behind the loop add the low parts times the tokens' group sums (333
+//     tokens, 4096 -> 11008 in groups of 64: 70 and 84 us; 4096 tokens, gated
+//     5120 -> 2 x 13824: 1.10 and 1.25 ms on one card).
 //   * A group whose step is 0 leaves the unit as it is and takes codes and
 //     zero as 0.
 // bf16 activations are first brought to fp16 by a power of two per row
@@ -140,10 +145,58 @@ struct GemmLds {
   static_assert(kBytes <= 160 * 1024);
 };
 
+// The zeros' low parts: they multiply the tokens' sums over each group, as fp32
+// matrix products over the groups g0 .. g1 - 1, from what the preparing launch
+// left of the sums.
+struct Lows {
+  const float* sums;  // [N, ng], and as far behind as a last lane's four loads reach
+  const int* parted;  // per 32 rows x 32 groups: whether `lows` holds them
+  const float* lows;  // [ng, O]
+};
+template <int MT, typename RowOf>
+__device__ __forceinline__ void add_lows(floatx4 (&acc)[MT][4], const Lows& l, RowOf row_of, int N, int O,
+                                         int ng, int g0, int g1, int t0, int lane) {
+  typedef float float4u __attribute__((ext_vector_type(4), aligned(4)));
+  const int r16 = lane & 15, q4 = lane >> 4;
+  // 16 groups' loads at a time, four neighbours per lane
+#pragma unroll 1
+  for (int gb = g0; gb < g1; gb += 16) {
+    const int g = gb + 4 * q4;
+    float c[4][4];
+    float4u s[MT];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const int row = row_of(16 * n + r16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // loaded in any case, so that no load waits for the other
+        const int at = min(g + i, ng - 1);
+        const float v = l.lows[(size_t)at * O + row];
+        const int there = l.parted[(at >> 5) * ((O + 31) >> 5) + (row >> 5)];
+        c[i][n] = g + i < g1 && there ? v : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      s[m] = *(const float4u*)(l.sums + (size_t)min(t0 + 16 * m + r16, N - 1) * ng + g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[m][i] = g + i < g1 ? s[m][i] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+          acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x4f32(s[m][i], c[i][n], acc[m][n], 0, 0, 0);
+  }
+}
+
 template <int GROUP, bool GATED, int MT, bool SPLIT>
 __global__ void __launch_bounds__(512, 2)
 k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
-          const char* __restrict__ prm, float* __restrict__ parts, TileSplit sp, Epilogue ep) {
+          const char* __restrict__ prm, Lows lows, float* __restrict__ parts, TileSplit sp,
+          Epilogue ep) {
   using L = GemmLds<GROUP, MT, SPLIT>;
   constexpr int BM = (SPLIT ? 16 : 32) * MT;
   constexpr int GPB = 128 / GROUP, JG = 4 / GPB;
@@ -384,7 +437,21 @@ k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
 #pragma unroll
       for (int r = 0; r < 4; ++r) acc[m][n][r] *= unit[n] * kCodeScale;
   const int ow = rb + (GATED ? 32 : 64) * wn;
+  // Does a zero of this wavefront's columns and groups have a low part?  Its 64
+  // columns begin on a multiple of 32 rows, but for the up rows' 32.
+  const int ng = K / GROUP, g0 = (SPLIT ? 2 : 1) * un.s0 * GPB;
+  const int g1 = min((SPLIT ? 2 : 1) * un.s1 * GPB, ng);
+  int low = 0;
+  for (int e = 4 * (g0 >> 5) + lane; e < 4 * ((g1 + 31) >> 5); e += 64) {
+    const int j = e & 3;
+    const int row = GATED ? min(ow, F - 1) + (j & 1 ? F : 0) : ow + 32 * (j & 1);
+    const int last = GATED && j == 3 ? 31 : 0;
+    low |= lows.parted[(e >> 2) * ((O + 31) >> 5) + (min(row + last, O - 1) >> 5)];
+  }
+  low = __any(low);
+  auto row_of = [&](int i) { return packed_row(64 * wn + i); };
   if constexpr (!SPLIT) {
+    if (low) add_lows(acc, lows, row_of, N, O, ng, g0, g1, t0 + wm * MT * 16, lane);
     leave<GATED, MT>(acc, parts, un, wave, (float*)smem + wave * kEpWave, ep, t0 + wm * MT * 16, ow,
                      lane);
   } else {
@@ -406,6 +473,7 @@ k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
     for (int m = 0; m < H; ++m)
 #pragma unroll
       for (int n = 0; n < 4; ++n) keep[m][n] += other[(m * 4 + n) * 64];
+    if (low) add_lows(keep, lows, row_of, N, O, ng, g0, g1, t0 + wm * H * 16, lane);
     leave<GATED, H>(keep, parts, un, wave, (float*)smem + wave * kEpWave, ep, t0 + wm * H * 16, ow,
                     lane);
   }
@@ -429,7 +497,7 @@ k_gemm_join(const float* __restrict__ parts, TileSplit sp, Epilogue ep, int mt) 
 struct GemmPlan {
   int mt;
   TileSplit sp;
-  size_t off_prm, off_a, off_back, off_parts, bytes;
+  size_t off_prm, off_parted, off_lows, off_sums, off_a, off_back, off_parts, bytes;
 };
 static GemmPlan gemm_plan(W4Op op, const W4Args& a) {
   GemmPlan p;
@@ -442,6 +510,12 @@ static GemmPlan gemm_plan(W4Op op, const W4Args& a) {
   size_t at = 0;
   p.off_prm = at;
   at += align256((size_t)a.O * (a.K / a.group) * 4);
+  p.off_parted = at;
+  at += align256((size_t)((a.O + 31) / 32) * ((a.K / a.group + 31) / 32) * 4);
+  p.off_lows = at;
+  at += align256((size_t)a.O * (a.K / a.group) * 4);
+  p.off_sums = at;
+  at += align256((size_t)a.N * (a.K / a.group) * 4 + 64);
   p.off_a = p.off_back = at;
   if (a.type == kBF16) {
     at += align256((size_t)a.N * a.K * 2);
@@ -469,10 +543,12 @@ static hipError_t launch(const W4Args& a, const GemmPlan& p, hipStream_t stream)
   const bool bf = a.type == kBF16;
   const Epilogue ep{bf ? (const int*)(ws + p.off_back) : nullptr,
                     a.out0, a.out1, (int)a.N, (int)a.O, a.y_type, a.type, a.act};
+  const Lows lows{(const float*)(ws + p.off_sums), (const int*)(ws + p.off_parted),
+                  (const float*)(ws + p.off_lows)};
   float* parts = (float*)(ws + p.off_parts);
   hipLaunchKernelGGL(kernel, dim3((unsigned)(p.sp.full + p.sp.left * p.sp.parts)), dim3(512), lds,
                      stream, bf ? (const _Float16*)(ws + p.off_a) : (const _Float16*)a.in0, (int)a.K,
-                     (const char*)a.qweight, ws + p.off_prm, parts, p.sp, ep);
+                     (const char*)a.qweight, ws + p.off_prm, lows, parts, p.sp, ep);
   if (p.sp.parts > 1)
     hipLaunchKernelGGL(k_gemm_join<GATED>, dim3((unsigned)(p.sp.left * 4 * MT)), dim3(64), 0, stream,
                        parts, p.sp, ep, MT);
@@ -503,11 +579,14 @@ hipError_t launch_w4_gemm(W4Op op, const W4Args& a, hipStream_t stream) {
   q.O = (int)a.O;
   q.ng = (int)(a.K / a.group);
   q.prm = ws + p.off_prm;
+  q.parted = (int*)(ws + p.off_parted);
+  q.lows = (float*)(ws + p.off_lows);
+  q.sums = (float*)(ws + p.off_sums);
   q.in0 = a.in0;
   q.cols = q.ld_out = (int)a.K;
   q.out = ws + p.off_a;
   q.back = (int*)(ws + p.off_back);
-  const hipError_t e = launch_w4_prepare(q, a.type, 1, false, a.type == kBF16 ? a.N : 0, stream);
+  const hipError_t e = launch_w4_prepare(q, a.type, 1, false, a.N, stream);
   if (e != hipSuccess) return e;
   return op == kOpGated ? by_group<true>(a, p, stream) : by_group<false>(a, p, stream);
 }

@@ -185,7 +185,10 @@ struct Prepare {
   const _Float16 *step16, *zero16;
   int O, ng;
   void* prm;
-  int* big;  // input gradient
+  int* big;     // input gradient
+  int* parted;  // products: one per 32 rows x 32 groups
+  float* lows;  // products: [ng, O]
+  float* sums;  // products: [rows, ng], each row's sums over the groups
   // rows: cols values of in0 (gated: cols / 2 of dH in in0 and cols of pre in
   // in1, giving dpre) to out, ld_out apart; out may be NULL with gated
   const void *in0, *in1;

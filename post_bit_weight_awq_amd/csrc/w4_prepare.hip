@@ -7,26 +7,36 @@
 
 namespace awq {
 
-// 32 rows x 32 groups as (step, -zero 2^-9) fp16 pairs by group:
-// prm[g * O + row].
+// 32 rows x 32 groups as (step, -zero 2^-9) fp16 pairs by group, of the zeros
+// their high parts: prm[g * O + row]; parted[block]: whether any has a low one,
+// and then lows[g * O + row], -low times the step.
 __device__ __forceinline__ void product_params(const Prepare& a, int block) {
   __shared__ uint32_t tile[32][33];
+  __shared__ float lows[32][33];
   const int nr = (a.O + 31) / 32, r0 = block % nr * 32, g0 = block / nr * 32;
   const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
+  int parted = 0;
 #pragma unroll
   for (int i = 0; i < 32; i += 8) {
     const int row = r0 + r + i, g = g0 + c;
     if (row < a.O && g < a.ng) {
       const size_t at = (size_t)row * a.ng + g;
-      const uint32_t nz = neg_zero_pair(a.zero16[at]);
+      const ZeroParts z = split_zero<false>((float)a.zero16[at]);
+      const uint32_t nz = neg_zero_pair((_Float16)z.high);
+      parted |= z.low != 0.0f;
+      lows[r + i][c] = -z.low * (float)a.step16[at];
       tile[r + i][c] = (uint32_t)__builtin_bit_cast(uint16_t, a.step16[at]) | (nz & 0xffff0000u);
     }
   }
-  __syncthreads();
+  parted = __syncthreads_or(parted);
+  if (threadIdx.x == 0) a.parted[block] = parted;
 #pragma unroll
   for (int i = 0; i < 32; i += 8) {
     const int row = r0 + c, g = g0 + r + i;
-    if (row < a.O && g < a.ng) ((uint32_t*)a.prm)[(size_t)g * a.O + row] = tile[c][r + i];
+    if (row < a.O && g < a.ng) {
+      ((uint32_t*)a.prm)[(size_t)g * a.O + row] = tile[c][r + i];
+      if (parted) a.lows[(size_t)g * a.O + row] = lows[c][r + i];
+    }
   }
 }
 
@@ -97,13 +107,26 @@ __device__ __forceinline__ uint32_t f32_to_bits(float v) {
   return __builtin_bit_cast(uint16_t, from_f32<T>(v));
 }
 
+// The sum over a group of a row's fp16 values, 0 where it is not finite, from
+// eight values of each of the group's lanes.
+__device__ __forceinline__ void sum_group(const Prepare& a, int row, int col, const uint32_t (&v)[8]) {
+  const int group = a.cols / a.ng;
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s += bits_to_f32<_Float16>(v[i]);
+  for (int d = 1; d < group / 8; d *= 2) s += __shfl_xor(s, d, 64);
+  if (col % group == 0)
+    a.sums[(size_t)row * a.ng + col / group] = fabsf(s) < INFINITY ? s : 0.0f;
+}
+
 // One row.  GATED: dG = dH U act'(G), dU = dH act(G), each rounded once, into
 // dpre; the row that follows is dpre's.  Then, where `out` is given, the row as
 // fp16 with zeros behind it up to ld_out: fp16 as it is; bf16 times 2^e, e
 // from the row's largest finite magnitude (which lands in [2^14, 2^15)) and
 // back[row] = -e.  Values down to 2^-31 of the largest stay exact,
 // smaller ones may be off by 2^-39 of it (half of fp16's last place, 2^-25).
-template <typename T, bool GATED, int N>
+// SUMS: also sums[row, g] of what `out` gets, or of an fp16 row left in place.
+template <typename T, bool GATED, int N, bool SUMS>
 __device__ __forceinline__ void prepare_row(const Prepare& a, int row) {
   constexpr bool SCALE = !__is_same(T, _Float16);
   __shared__ uint32_t red[4];
@@ -164,6 +187,14 @@ __device__ __forceinline__ void prepare_row(const Prepare& a, int row) {
     e = top ? 15 - x : 0;
     if (threadIdx.x == 0) a.back[row] = -e;
   }
+  if constexpr (SUMS && !SCALE) {
+    for (int c = threadIdx.x * N; c < cols; c += 256 * N) {
+      uint32_t v[8];
+      load_bits<N>(src + c, v);
+      sum_group(a, row, c, v);
+    }
+    return;
+  }
   uint16_t* dst = (uint16_t*)a.out + (size_t)row * a.ld_out;
   auto copy = [&](int from, int to) {
     for (int c = from + threadIdx.x * N; c < to; c += 256 * N) {
@@ -173,6 +204,7 @@ __device__ __forceinline__ void prepare_row(const Prepare& a, int row) {
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = f32_to_bits<_Float16>(ldexpf(bits_to_f32<T>(v[i]), e));
       store_bits<N>(dst + c, v);
+      if constexpr (SUMS) sum_group(a, row, c, v);
     }
   };
   if constexpr (GATED) {
@@ -197,11 +229,14 @@ __global__ void __launch_bounds__(256) k_w4_prepare(Prepare a) {
     return;
   }
   const int row = block - (PARAMS ? a.param_blocks : 0);
-  // whole 16-byte pieces where both halves of a row begin on a boundary
-  if ((a.cols & (GATED ? 15 : 7)) == 0)
-    prepare_row<T, GATED, 8>(a, row);
+  // whole 16-byte pieces where both halves of a row begin on a boundary, as the
+  // products' rows always do
+  if constexpr (PARAMS == 1)
+    prepare_row<T, GATED, 8, true>(a, row);
+  else if ((a.cols & (GATED ? 15 : 7)) == 0)
+    prepare_row<T, GATED, 8, false>(a, row);
   else
-    prepare_row<T, GATED, 1>(a, row);
+    prepare_row<T, GATED, 1, false>(a, row);
 }
 
 hipError_t launch_w4_prepare(const Prepare& p, int type, int params, bool gated, int64_t rows,

@@ -113,7 +113,7 @@ BY_TYPE = pytest.mark.parametrize("t,group", [(F16, 128), (F16, 64), (F16, 32), 
                                   ids=lambda v: str(v).replace("torch.", ""))
 
 
-@pytest.mark.parametrize("n", [1, 4, 12, 30, 48])
+@pytest.mark.parametrize("n", [1, 4, 12, 30, 48, 64, 100, 200, 600])
 @BY_TYPE
 def test_each_weight_alone(awq, n, t, group):
     """One column per token, all others 0: the output is one weight times a power of two, the fp32 output off by the
@@ -130,7 +130,8 @@ def test_each_weight_alone(awq, n, t, group):
           8 * P.U32 * (xd.abs() @ (size(d, layer[2], k) * s).T), "Y")
 
 
-@pytest.mark.parametrize("n,k,o", [(1, 512, 200), (3, 1152, 40), (16, 640, 333), (40, 512, 200), (64, 256, 20481)])
+@pytest.mark.parametrize("n,k,o", [(1, 512, 200), (3, 1152, 40), (16, 640, 333), (40, 512, 200), (64, 256, 20481), (64, 384, 520),
+                                   (70, 512, 640), (200, 1152, 250), (600, 640, 700), (1100, 512, 4100)])
 @BY_TYPE
 def test_products_with_any_zero(awq, n, k, o, t, group):
     _say(f"any zero {n}x{k}->{o} {t} g{group}")
@@ -151,7 +152,7 @@ def test_products_with_any_zero(awq, n, k, o, t, group):
     close(h, a * u, P.rounded(a * u, (a.abs() + ea) * eu + ea * u.abs() + 2 * P.U32 * (a * u).abs(), t), "H")
 
 
-@pytest.mark.parametrize("n", [1, 4, 30])
+@pytest.mark.parametrize("n", [1, 4, 30, 64, 100, 300])
 @BY_TYPE
 def test_infinities_beside_zeros_next_to_a_code(awq, n, t, group):
     """An infinity times q - z is one of q - z's sign, however near z lies to q, and NaN for q = z alone."""
@@ -176,7 +177,7 @@ def test_large_finite_rows_keep_their_remainders(awq):
     k, o = 256, 64
     q, s, z = P.make_layer(o, k, 128, 18, "cuda", "any")
     s.fill_(2.0 ** -24)
-    for n in (1, 20):
+    for n in (1, 20, 100):
         x = torch.full((n, k), 6.0e37, dtype=BF16, device="cuda")
         x[:, 1::2] = 4.0e37
         w = E.weights(q, s, z)

@@ -75,7 +75,7 @@ def a_chain(n, k, f, group, t, act, seed, dev="cpu"):
 ALL = (128, 64, 32)
 ROUNDED_PARAM_GRAD = {(1, 128, 1): (64,), (1, 512, 512): ALL, (1, 1152, 333): ALL, (3, 640, 17): ALL, (5, 384, 96): ALL,
                       (17, 256, 65): ALL, (33, 640, 130): ALL, (65, 128, 257): (64, 32), (129, 1280, 193): (64, 32)}
-ROUNDED_LINEAR_ZEROS = (7, 40)
+ROUNDED_LINEAR_ZEROS = (7, 40, 200, 600)
 
 
 def holds_rounded_zeros(test, p):
