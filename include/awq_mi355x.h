@@ -328,7 +328,9 @@ int awq_w4a16_gated(const void* X, int dtype, int64_t n_tokens, int64_t in_featu
  * is rounded to fp16 (the step varies along the sum, so it cannot be applied
  * to sums of exact products), after q - zero was, which is exact for integer
  * zeros of magnitude up to 2032, else off by 2^-12 of itself or, from a zero
- * below 2^-5, by 2^-16 more.
+ * below 2^-5, by 2^-16 more.  Column blocks of 256 with a W that may leave
+ * fp16 (a step of 128, or |step| (|zero| + 15) of 65504, or more) are summed in
+ * binary32 without the matrix units, about fifteen times as slowly.
  *   dY: [n_tokens, out_features] dtype; dX: [n_tokens, in_features] dtype */
 size_t awq_w4a16_input_grad_workspace_size(int64_t n_tokens, int64_t in_features,
                                            int64_t out_features, int group_size, int dtype);

@@ -18,7 +18,10 @@
 //     j = 0..15, h the wavefront's half of the words.  No transpose, and a
 //     lane's four tiles are four neighbouring columns of dX.
 //   * The step changes along the sum, so it has to enter the operand: weights
-//     are formed as fp16((q - z) step), one rounding, 14 operations per eight.
+//     are formed as fp16((q - z) step), 15 operations per eight.  A block with
+//     weights that fp16 may not hold sums in fp32 without the matrix units (512
+//     x 4096 <- 4096, all blocks: 0.4 ms against 40 us): no layer that is packed
+//     from ordinary weights has one.
 //   * The LDS rows of the codes are ordered (row % 8, row / 8) and every
 //     second pair swaps its 64-byte halves: the 64 words of a read then lie
 //     in 64 banks.
@@ -28,8 +31,6 @@
 // Bound by the issue of MFMAs and conversions: 4096 x 5120 <- 27648 takes
 // 0.95 ms (1.2 PFLOP/s) of 1.12 with its row scaling, 2048 x 4096 <- 12288 200 us
 // of which 27 are the scaling.
-#include <type_traits>
-
 #include "w4_internal.h"
 
 namespace awq {
@@ -180,17 +181,32 @@ k_w4_dx(const _Float16* __restrict__ A, int lda, const int* __restrict__ back, i
     load_a(un.s0 + 1);
   }
   if (L::kNC == 4 && un.s0 + 2 < send) load_c(un.s0 + 2);
-  // steps of 128 and more among the block's: 512 step leaves fp16's range, so
-  // the factor goes to the differences, one operation more
+  // weights that fp16 may not hold among the block's: it takes them in fp32
   int over = 0;
   const int gb = (ng + 31) / 32, gb0 = k0 / GROUP / 32, gb1 = min(k0 + 255, K - 1) / GROUP / 32;
   for (int s = CL * un.s0 + tid; s < min(CL * un.s1, steps); s += 512)
     over |= big[s * gb + gb0] | big[s * gb + gb1];
   over = __syncthreads_or(over);
+  // the iteration's dY and the next one's codes have landed (what was
+  // requested after them may be in flight), and no wavefront still reads the
+  // stages that are requested next
+  auto landed = [&](int s) {
+    if (L::kNC == 4 && s + 2 < send && s > un.s0)
+      wait_vm<AL + CL + PL>();
+    else if (L::kNC == 3 && s + 1 < send && s > un.s0)
+      wait_vm<AL>();
+    else
+      wait_vm<0>();
+    __syncthreads();
+  };
+  auto request = [&](int s) {
+    if (s + L::kNC - 1 < send) load_c(s + L::kNC - 1);
+    if (s + 2 < send) load_a(s + 2);
+  };
   // Half a step (32 packed rows) at a time; while one half multiplies, the
   // next one's codes are read and converted a row pair after each few
   // fragments, so that the conversion fills the gaps between MFMAs.
-  auto sum = [&](auto plain) {
+  auto sum = [&]() {
     uint32_t w[8];
     uint4 zv, sv, b[4];
     uint32_t bn[4][4];
@@ -219,7 +235,7 @@ k_w4_dx(const _Float16* __restrict__ A, int lda, const int* __restrict__ back, i
       for (int c = 0; c < 4; ++c) {
         const half2v d =
             __builtin_elementwise_fma(__builtin_bit_cast(half2v, n[c]), c & 1 ? m1 : m0, z);
-        bn[c][p] = __builtin_bit_cast(uint32_t, plain ? d * s5 : (d * k512) * s1);
+        bn[c][p] = __builtin_bit_cast(uint32_t, d * s5);
       }
     };
     auto take = [&]() {
@@ -233,16 +249,7 @@ k_w4_dx(const _Float16* __restrict__ A, int lda, const int* __restrict__ back, i
     for (int p = 0; p < 4; ++p) convert(p);
     take();
     for (int s = un.s0; s < send; ++s) {
-      // the iteration's dY and the next one's codes have landed (what was
-      // requested after them may be in flight), and no wavefront still reads
-      // the stages that are requested next
-      if (L::kNC == 4 && s + 2 < send && s > un.s0)
-        wait_vm<AL + CL + PL>();
-      else if (L::kNC == 3 && s + 1 < send && s > un.s0)
-        wait_vm<AL>();
-      else
-        wait_vm<0>();
-      __syncthreads();
+      landed(s);
       // the odd step past the last one
       const bool live = !SPLIT || 2 * s + wm < steps;
 #pragma unroll
@@ -264,17 +271,48 @@ k_w4_dx(const _Float16* __restrict__ A, int lda, const int* __restrict__ back, i
           take();
         }
         // between the halves the requests delay the MFMAs least
-        if (ch == 0) {
-          if (s + L::kNC - 1 < send) load_c(s + L::kNC - 1);
-          if (s + 2 < send) load_a(s + 2);
-        }
+        if (ch == 0) request(s);
       }
     }
   };
+  // The same sums a packed row at a time, one product per weight and token: a
+  // register of a lane is token 4 (l / 16) + r of its tile.
+  auto sum_fp32 = [&]() {
+    for (int s = un.s0; s < send; ++s) {
+      landed(s);
+      if (!SPLIT || 2 * s + wm < steps) {
+        const char* pc = smem + L::kOffC + (s % L::kNC) * L::kC + (SPLIT ? wm * 8192 : 0) + 4 * r16;
+        const char* pp = smem + L::kOffP + (s % L::kNC) * L::kP + (SPLIT ? wm * 2048 : 0) + gl * 256;
+        const char* ta = smem + (s % 3) * L::kA + (wm * MT * 16 + 4 * q4) * 128;
+#pragma unroll 1
+        for (int row = 0; row < 64; ++row) {
+          const int q = (row >> 3) & 3;
+          const uint32_t w = *(const uint32_t*)(pc + (32 * (row >> 5) + 4 * (row & 7) + q) * 128 +
+                                                ((wb ^ (q >> 1)) * 64)) >> (16 * half);
+          const float nz = (float)*(const _Float16*)(pp + 2 * row) * kCodeScale;
+          const float st = (float)*(const _Float16*)(pp + 128 + 2 * row);
+          float v[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) v[c] = ((float)((w >> (4 * c)) & 15u) + nz) * st;
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int t = 4 * q4 + r;  // of the tile; its rows are multiples of 8
+              const float a = (float)*(const _Float16*)(ta + (16 * m + r) * 128 +
+                                                        16 * ((row >> 3) ^ (t & 7)) + 2 * (row & 7));
+#pragma unroll
+              for (int c = 0; c < 4; ++c) acc[m][c][r] = fmaf(a, v[c], acc[m][c][r]);
+            }
+        }
+      }
+      request(s);
+    }
+  };
   if (over)
-    sum(std::false_type{});
+    sum_fp32();
   else
-    sum(std::true_type{});
+    sum();
   const int col = k0 + 128 * wb + 8 * r16 + 4 * half;
   if constexpr (!SPLIT) {
     leave<T, MT>(acc, parts, un, wave, back, N, K, t0 + wm * MT * 16, col, lane, dX);

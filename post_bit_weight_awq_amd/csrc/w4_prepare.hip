@@ -43,7 +43,7 @@ __device__ __forceinline__ void product_params(const Prepare& a, int block) {
 // 64 packed rows (a step of the input gradient) x 32 groups:
 // prm[(s * ng + g) * 128 + ..] as 64 halfs -zero 2^-9 and 64 halfs of the step,
 // 0 for rows past the end; big[s * blocks of 32 groups + block]: whether a step
-// is 128 or more.
+// is 128 or more (512 of them leave fp16) or a weight may leave it.
 __device__ __forceinline__ void gradient_params(const Prepare& a, int block) {
   __shared__ uint32_t tile[64][33];
   const int gb = (a.ng + 31) / 32, s = block / gb, o0 = s * 64, g0 = block % gb * 32;
@@ -57,7 +57,8 @@ __device__ __forceinline__ void gradient_params(const Prepare& a, int block) {
       const size_t at = (size_t)(o0 + r) * a.ng + g0 + c;
       v = (neg_zero_pair(a.zero16[at]) & 0xffffu) |
           ((uint32_t)__builtin_bit_cast(uint16_t, a.step16[at]) << 16);
-      over |= (v & 0x7fff0000u) >= 0x58000000u;  // 128
+      const float st = fabsf((float)a.step16[at]), z = fabsf((float)a.zero16[at]);
+      over |= !(st < 128.0f && st * (z + 15.0f) < 65504.0f);
     }
     tile[r][c] = v;
   }

@@ -201,3 +201,27 @@ def test_param_grad_with_any_zero(awq, n, k, o, t, group):
     close(ds, (d * q).sum(-1), e * (da * q.abs()).sum(-1) + 2.0 ** -149, "dstep")
     s = layer[1].to(P.F64)
     close(dz, -s * d.sum(-1), e * s * da.sum(-1) + 2.0 ** -149, "dzero")
+
+
+# ----------------------------------------------------------------- large weights
+@pytest.mark.parametrize("n,o", [(1, 72), (40, 72), (130, 200), (300, 1000), (600, 72)])
+@BY_TYPE
+def test_input_grad_of_weights_past_fp16(awq, n, o, t, group):
+    """Weights beyond 65504, by their step or by their zero, beside ordinary ones: dX is finite where the sum is."""
+    _say(f"large weights {n} {o} {t} g{group}")
+    k = 640
+    q, s, z = P.make_layer(o, k, group, 9, "cuda", "any")
+    s[3, 0], s[7, -1], s[11] = 60000.0, -9000.0, 130.0
+    z[13], z[17, 0], s[17, 0] = 60000.0, -65504.0, 100.0
+    z[19, 1], s[19, 1] = 2000.0, 127.0
+    g = torch.Generator().manual_seed(n)
+    dy = (2.0 ** -14 * torch.randn(n, o, generator=g)).to(t).cuda()
+    dy[:, 17] = 2.0 ** -24
+    got = awq.awq_w4a16_input_grad(dy, q, s, z)
+    # each weight off by two roundings to 11 bits, its zero by 2^-16 and a half of its last place
+    w, a = E.weights(q, s, z), dy.to(P.F64).abs()
+    y = dy.to(P.F64) @ w
+    sl = P.spread(s, k).abs()
+    b = 2 * (o + 64) * P.U32 * (a @ w.abs()) + a @ (2.0 ** -10 * w.abs() + 2.0 ** -15 * sl + 2.0 ** -24)
+    assert bool(got.isfinite().all())
+    close(got, y, P.rounded(y, b, t), "dX")
