@@ -157,7 +157,12 @@ __device__ __forceinline__ void prepare_row(const Prepare& a, int row) {
         float slope;
         const float y = a.act == kActSilu ? act_value<kActSilu>(x, &slope)
                                           : act_value<kActGelu>(x, &slope);
-        dg[i] = f32_to_bits<T>(e * bits_to_f32<T>(u[i]) * slope);
+        const float w = bits_to_f32<T>(u[i]);
+        float z = e * w * slope;
+        // dH U may leave binary32 where the slope, below 1 then, brings it back
+        if (SCALE && !(fabsf(e * w) < INFINITY) && fabsf(e) < INFINITY && fabsf(w) < INFINITY)
+          z = e * slope * w;
+        dg[i] = f32_to_bits<T>(z);
         du[i] = f32_to_bits<T>(e * y);
       }
       store_bits<N>(dpre + c, dg);

@@ -225,3 +225,20 @@ def test_input_grad_of_weights_past_fp16(awq, n, o, t, group):
     b = 2 * (o + 64) * P.U32 * (a @ w.abs()) + a @ (2.0 ** -10 * w.abs() + 2.0 ** -15 * sl + 2.0 ** -24)
     assert bool(got.isfinite().all())
     close(got, y, P.rounded(y, b, t), "dX")
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_gate_gradient_of_large_factors(awq, act):
+    """dH U leaves binary32's range and the slope brings it back."""
+    _say("large factors", act)
+    g = torch.tensor([-60.0, -30.0, -8.0, -3.0], device="cuda").to(BF16)
+    f = 64
+    gate = g.repeat(f // 4)
+    pre = torch.stack([torch.cat([gate, torch.full_like(gate, u)]) for u in (1e20, -1e25, 3.0)])
+    dh = torch.full((3, f), 1e18, dtype=BF16, device="cuda")
+    dh[0, ::3] = 1e19
+    layer = P.make_layer(2 * f, 128, 128, 7, "cuda")
+    _, dpre = awq.awq_w4a16_gated_backward(dh, pre, *layer, act=act)
+    want, e = P.gated_grad(dh, pre, act)
+    finite = want.abs() < 3.38e38
+    close(torch.where(finite, dpre.to(P.F64), 0), torch.where(finite, want, 0), P.rounded(want, e, BF16), "dpre")
