@@ -252,14 +252,23 @@ _ACTS = {"silu": _lib.ACT_SILU, "gelu": _lib.ACT_GELU_TANH}
 _REFUSED = ctypes.c_size_t(-1).value
 
 
+def _w4_tracked(name: str):
+    raise RuntimeError(
+        f"{name} requires a gradient, and these calls record none: a result would silently be cut "
+        "off from it. Call them under torch.no_grad() or inside a torch.autograd.Function, whose "
+        "backward calls awq_w4a16_input_grad, awq_w4a16_gated_backward and awq_w4a16_param_grad")
+
+
 def _w4_ptr(t, name: str, dtype: torch.dtype, shape, dev: int) -> int:
-    """_dev's checks, and that the tensor is on GPU ``dev``."""
+    """_dev's checks, and that the tensor is on GPU ``dev`` and needs no gradient recorded."""
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.shape == shape
             and t.is_contiguous()):
         _dev(t, name, dtype, shape)
     if t.get_device() != dev:
         raise ValueError(f"{name} is on cuda:{t.get_device()}: all tensors must be on one device, "
                          f"the current one (cuda:{dev})")
+    if t.requires_grad and torch.is_grad_enabled():
+        _w4_tracked(name)
     return t.data_ptr()
 
 
@@ -272,6 +281,8 @@ def _w4_layer(lead: torch.Tensor, name: str, qweight, step, zero):
     dt = _DTYPES.get(lead.dtype)
     if dt is None:
         raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {lead.dtype}")
+    if lead.requires_grad and torch.is_grad_enabled():
+        _w4_tracked(name)
     if lead.dim() != 2 or qweight.dim() != 2 or step.dim() != 2:
         raise ValueError(f"{name}, qweight and step must be 2-D")
     o, words = qweight.shape

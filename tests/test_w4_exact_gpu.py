@@ -242,3 +242,38 @@ def test_gate_gradient_of_large_factors(awq, act):
     want, e = P.gated_grad(dh, pre, act)
     finite = want.abs() < 3.38e38
     close(torch.where(finite, dpre.to(P.F64), 0), torch.where(finite, want, 0), P.rounded(want, e, BF16), "dpre")
+
+
+# ------------------------------------------------------------------ the binding
+def test_tracked_tensors_are_refused(awq):
+    """Any tensor of a call, outputs too; a Function joins the calls to autograd."""
+    _say("tracked tensors")
+    n, k, o = 5, 256, 96
+    q, s, z = P.make_layer(o, k, 64, 3, "cuda")
+    x = torch.randn(n, k, device="cuda").to(F16)
+    dy = torch.randn(n, o, device="cuda").to(F16)
+    y = torch.zeros(n, o, dtype=F16, device="cuda", requires_grad=True)
+    for a, kw in (((x, q, s.clone().requires_grad_(), z), {}), ((x, q, s, z.clone().requires_grad_()), {}),
+                  ((x, q, s, z), {"out": y})):
+        with pytest.raises(RuntimeError, match="requires a gradient"):
+            awq.awq_w4a16_linear(*a, **kw)
+    with pytest.raises(RuntimeError, match="X requires a gradient"):
+        awq.awq_w4a16_param_grad(dy, x.clone().requires_grad_(), q, s, z)
+
+    class Linear(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, s, z):
+            ctx.save_for_backward(x, s, z)
+            return awq.awq_w4a16_linear(x, q, s, z)
+
+        @staticmethod
+        def backward(ctx, dy):
+            x, s, z = ctx.saved_tensors
+            ds, dz = awq.awq_w4a16_param_grad(dy, x, q, s, z)
+            return awq.awq_w4a16_input_grad(dy, q, s, z), ds.to(F16), dz.to(F16)
+
+    args = [t.clone().requires_grad_() for t in (x, s, z)]
+    Linear.apply(*args).backward(dy)
+    ds, dz = awq.awq_w4a16_param_grad(dy, x, q, s, z)
+    for got, want in zip(args, (awq.awq_w4a16_input_grad(dy, q, s, z), ds.to(F16), dz.to(F16))):
+        assert torch.equal(got.grad, want)
