@@ -248,7 +248,9 @@ def awq_w4a16_matmul(X: torch.Tensor, qweight: torch.Tensor, step: torch.Tensor,
 # cheap checks: an argument that is as expected costs a few attribute reads,
 # and only one that is not goes through _dev, which says what is wrong.
 _DTYPES = {torch.float16: _lib.DTYPE_F16, torch.bfloat16: _lib.DTYPE_BF16}
-_ACTS = {"silu": _lib.ACT_SILU, "gelu": _lib.ACT_GELU_TANH}
+#: "gelu" is the tanh form here, another name of "gelu_tanh"; the erf form, which torch calls
+#: "gelu" (its tanh form is approximate="tanh"), is up to 5e-4 away and not offered
+_ACTS = {"silu": _lib.ACT_SILU, "gelu": _lib.ACT_GELU_TANH, "gelu_tanh": _lib.ACT_GELU_TANH}
 _REFUSED = ctypes.c_size_t(-1).value
 
 
@@ -369,8 +371,11 @@ def awq_w4a16_gated(X: torch.Tensor, qweight: torch.Tensor, step: torch.Tensor,
                     out: Optional[torch.Tensor] = None, pre: Optional[torch.Tensor] = None,
                     workspace: Optional[torch.Tensor] = None, stream=None):
     """H = act(X Wg^T) * (X Wu^T) in one kernel; the packed layer holds the
-    gate's rows and then the up rows.  With keep_pre (or a pre buffer) returns
-    (H, pre), pre = [G | U] in X's type, which the backward pass reads."""
+    gate's rows and then the up rows.  act is "silu" or "gelu_tanh",
+    g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))), torch's gelu with
+    approximate="tanh"; "gelu" is another name of that form, not the erf one.
+    With keep_pre (or a pre buffer) returns (H, pre), pre = [G | U] in X's
+    type, which the backward pass reads."""
     lib = load()
     dt, n, k, o, group, layer, dev = _w4_layer(X, "X", qweight, step, zero)
     f, code = _w4_half(o), _w4_act(act)
@@ -412,7 +417,7 @@ def awq_w4a16_gated_backward(dH: torch.Tensor, pre: torch.Tensor, qweight: torch
                              out: Optional[torch.Tensor] = None,
                              dpre: Optional[torch.Tensor] = None,
                              workspace: Optional[torch.Tensor] = None, stream=None):
-    """(dX, dpre) of awq_w4a16_gated from the gradient of H and the kept pre;
+    """(dX, dpre) of awq_w4a16_gated (act as there) from the gradient of H and the kept pre;
     dpre = [dG | dU] is what awq_w4a16_param_grad takes as dY."""
     lib = load()
     dt, n, k, o, group, layer, dev = _w4_layer(dH, "dH", qweight, step, zero)

@@ -23,3 +23,14 @@ def test_a_tensor_that_requires_a_gradient(name):
         CALLS[name](x, layer)
     with torch.no_grad(), pytest.raises(ValueError, match="GPU"):
         CALLS[name](x, layer)
+
+
+def test_gelu_is_the_tanh_form_by_either_name():
+    assert awq._w4_act("gelu") == awq._w4_act("gelu_tanh") != awq._w4_act("silu")
+    for name in ("gelu_erf", "tanh", "relu", ""):
+        with pytest.raises(ValueError, match="act must be one of"):
+            awq._w4_act(name)
+    assert "not the erf one" in awq.awq_w4a16_gated.__doc__
+    # the plain form the tests hold the kernels to is torch's tanh form
+    g = torch.linspace(-6, 6, 201, dtype=torch.float64)
+    assert torch.allclose(P.act(g, "gelu")[0], torch.nn.functional.gelu(g, approximate="tanh"), rtol=0, atol=1e-14)
