@@ -325,7 +325,11 @@ def _w4_workspace(query, sizes, lead, workspace):
 
 
 def _w4_stream(stream, dev: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors on cuda:{dev}")
+    return stream.cuda_stream
 
 
 def awq_w4a16_linear(X: torch.Tensor, qweight: torch.Tensor, step: torch.Tensor,

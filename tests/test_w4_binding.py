@@ -34,3 +34,15 @@ def test_gelu_is_the_tanh_form_by_either_name():
     # the plain form the tests hold the kernels to is torch's tanh form
     g = torch.linspace(-6, 6, 201, dtype=torch.float64)
     assert torch.allclose(P.act(g, "gelu")[0], torch.nn.functional.gelu(g, approximate="tanh"), rtol=0, atol=1e-14)
+
+
+def test_a_stream_of_another_device_is_refused():
+    class Stream:
+        cuda_stream = 5
+
+        def __init__(self, device_index):
+            self.device_index = device_index
+
+    assert awq._w4_stream(Stream(0), 0) == 5
+    with pytest.raises(ValueError, match="stream is on cuda:1, the tensors on cuda:0"):
+        awq._w4_stream(Stream(1), 0)
