@@ -136,18 +136,13 @@ struct Epilogue {
 };
 
 // Direct loads to LDS: 16 (or 4) bytes per lane from base + off to l + 16 (4)
-// times the lane.  A load to LDS needs a wait state after its M0 is written.
+// times the lane.  l goes to M0 as an operand, so that the compiler writes the
+// register and knows it; the load needs a wait state behind that.
 __device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t l) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-               :
-               : "v"(off), "s"(base), "s"(l)
-               : "memory", "m0");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "{m0}"(l) : "memory");
 }
 __device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t l) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
-               :
-               : "v"(off), "s"(base), "s"(l)
-               : "memory", "m0");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, %1" : : "v"(off), "s"(base), "{m0}"(l) : "memory");
 }
 // All but the wavefront's last N vector memory operations have ended.
 template <int N>
