@@ -78,7 +78,7 @@ hipError_t launch_w4a16(const void* X, int64_t M, int64_t K, int64_t OUT, const 
 // largest token count of one W4A16 launch (16 tokens per block row of the grid)
 constexpr int64_t kMaxW4Tokens = (int64_t)65535 * 16;
 
-// Packed-weight operators (w4_linear.hip).  The layer is [O, K] with groups
+// Packed-weight operators (w4_ops.hip).  The layer is [O, K] with groups
 // of `group` columns; a gated block's O counts the gate's and the up rows.
 enum W4Op { kOpLinear, kOpGated, kOpInputGrad, kOpGatedBackward, kOpParamGrad };
 enum ElemType { kF16 = 0, kBF16 = 1, kF32 = 2 };

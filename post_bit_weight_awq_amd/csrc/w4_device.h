@@ -1,5 +1,5 @@
-// Device-side helpers of the packed-weight operators (w4_linear.hip,
-// w4_grad.hip): element types, activation functions, codes as fp16.
+// Device-side helpers of the packed-weight operators (w4_*.hip): element types,
+// activation functions, zeros in two parts, codes as fp16.
 #pragma once
 
 #include "awq_device.h"
@@ -45,7 +45,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 // Differences are held in units of 2^-9 between the codes and the step, which
 // takes the factor back: a nibble in bits 0-3 of a half is the fp16 subnormal
 // q 2^-24 and in bits 4-7 q 2^-20, so one packed fma by (2^15, 2^11) gives
-// (q - z) 2^-9 with one rounding, for any fp16 zero.
+// (q - z) 2^-9 with one rounding; none for the high part of a zero.
 constexpr float kCodeScale = 512.0f;
 __device__ __forceinline__ uint32_t neg_zero_pair(_Float16 z) {
   const _Float16 n = (_Float16)(-0.001953125f) * z;
@@ -77,8 +77,9 @@ __device__ __forceinline__ ZeroParts split_zero(float z) {
 constexpr uint32_t kNibbleFactors = 0x68007800u;
 
 // The eight codes of a word, in column order, as (q - z) 2^-9: ten operations.
-// With factors and zero 0 they all become 0.  The first or last four alone:
-__device__ __forceinline__ uint2 dequant_half(uint32_t w, uint32_t nz, uint32_t factors, int half) {
+// With factors and zero 0 they all become 0.
+__device__ __forceinline__ uint4 dequant_word(uint32_t w, uint32_t nz,
+                                              uint32_t factors = kNibbleFactors) {
   const uint32_t lo = w & 0x0F0F0F0Fu, hi = w & 0xF0F0F0F0u;
   const half2v m = __builtin_bit_cast(half2v, factors);
   const half2v z = __builtin_bit_cast(half2v, nz);
@@ -86,25 +87,7 @@ __device__ __forceinline__ uint2 dequant_half(uint32_t w, uint32_t nz, uint32_t 
     const half2v c = __builtin_bit_cast(half2v, __builtin_amdgcn_perm(hi, lo, sel));
     return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(c, m, z));
   };
-  return half ? make_uint2(pair(0x0c060c02u), pair(0x0c070c03u))
-              : make_uint2(pair(0x0c040c00u), pair(0x0c050c01u));
-}
-__device__ __forceinline__ uint4 dequant_word(uint32_t w, uint32_t nz,
-                                              uint32_t factors = kNibbleFactors) {
-  const uint2 a = dequant_half(w, nz, factors, 0), b = dequant_half(w, nz, factors, 1);
-  return make_uint4(a.x, a.y, b.x, b.y);
-}
-
-// Words of four lane groups of 16: word j of group q becomes word q of group
-// j.  A group that loaded words 4q .. 4q+3 of a row's 16 (one 16-byte load)
-// then holds words q, 4 + q, 8 + q, 12 + q: word j of every group lies in the
-// j-th 32 of the 128 columns.
-__device__ __forceinline__ void transpose_words(uint4& w) {
-  const auto a = __builtin_amdgcn_permlane32_swap(w.x, w.z, false, false);
-  const auto b = __builtin_amdgcn_permlane32_swap(w.y, w.w, false, false);
-  const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
-  const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-  w = make_uint4(c[0], c[1], d[0], d[1]);
+  return make_uint4(pair(0x0c040c00u), pair(0x0c050c01u), pair(0x0c060c02u), pair(0x0c070c03u));
 }
 
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int j) {
