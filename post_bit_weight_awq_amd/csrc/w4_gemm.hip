@@ -24,16 +24,16 @@
 //   * A zero is taken as a high part, which the differences hold exactly, and a
 //     low one, 0 for the zeros that packing writes: where there are others, fp32
 //     MFMAs behind the loop add the low parts times the tokens' group sums (333
-//     tokens, 4096 -> 11008 in groups of 64: 70 and 84 us; 4096 tokens, gated
-//     5120 -> 2 x 13824: 1.10 and 1.25 ms on one card).
+//     tokens, 4096 -> 11008 in groups of 64: 69 and 80 us; 4096 tokens, gated
+//     5120 -> 2 x 13824: 1.03 and 1.18 ms).
 //   * A group whose step is 0 leaves the unit as it is and takes codes and
 //     zero as 0.
 // bf16 activations are first brought to fp16 by a power of two per row
 // (w4_prepare.hip), which the epilogue takes back.
 // Bound by the issue of MFMAs and of the conversions beside them: 4096 tokens,
-// gated 5120 -> 2 x 13824 with [G | U] kept, 1.00 ms (1.16 PFLOP/s; 1.04 ms
-// with the codes converted where they are used); 333 tokens, 4096 -> 11008 in
-// groups of 64, 64 us.
+// gated 5120 -> 2 x 13824 with [G | U] kept, 1.02-1.11 ms over the cards
+// measured (up to 1.13 PFLOP/s; with the codes converted where they are used 4 %
+// more); 333 tokens, 4096 -> 11008 in groups of 64, 68-70 us.
 #include "w4_internal.h"
 
 namespace awq {
@@ -324,6 +324,20 @@ k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
     next_ratio[n] = fmaf(fmaf(-q, st, unit[n]), inv, q);
     unit[n] = st;
   };
+  // Does a zero of this wavefront's columns and groups have a low part?  Its 64
+  // columns begin on a multiple of 32 rows, but for the up rows' 32.  The first
+  // answers are requested here and looked at behind the loop.
+  const int ow = rb + (GATED ? 32 : 64) * wn;
+  const int ng = K / GROUP, g0 = (SPLIT ? 2 : 1) * un.s0 * GPB;
+  const int g1 = min((SPLIT ? 2 : 1) * un.s1 * GPB, ng);
+  const int first = 4 * (g0 >> 5) + lane, last = 4 * ((g1 + 31) >> 5);
+  auto flag = [&](int e) {
+    const int j = e & 3;
+    const int row = GATED ? min(ow, F - 1) + (j & 1 ? F : 0) : ow + 32 * (j & 1);
+    const int off = GATED && j == 3 ? 31 : 0;
+    return lows.parted[(e >> 2) * ((O + 31) >> 5) + (min(row + off, O - 1) >> 5)];
+  };
+  int low = flag(min(first, last - 1));
   const int end = un.s1, send = 2 * end;
   if constexpr (SPLIT) {
     load_p(un.s0);
@@ -436,18 +450,7 @@ k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
     for (int n = 0; n < 4; ++n)
 #pragma unroll
       for (int r = 0; r < 4; ++r) acc[m][n][r] *= unit[n] * kCodeScale;
-  const int ow = rb + (GATED ? 32 : 64) * wn;
-  // Does a zero of this wavefront's columns and groups have a low part?  Its 64
-  // columns begin on a multiple of 32 rows, but for the up rows' 32.
-  const int ng = K / GROUP, g0 = (SPLIT ? 2 : 1) * un.s0 * GPB;
-  const int g1 = min((SPLIT ? 2 : 1) * un.s1 * GPB, ng);
-  int low = 0;
-  for (int e = 4 * (g0 >> 5) + lane; e < 4 * ((g1 + 31) >> 5); e += 64) {
-    const int j = e & 3;
-    const int row = GATED ? min(ow, F - 1) + (j & 1 ? F : 0) : ow + 32 * (j & 1);
-    const int last = GATED && j == 3 ? 31 : 0;
-    low |= lows.parted[(e >> 2) * ((O + 31) >> 5) + (min(row + last, O - 1) >> 5)];
-  }
+  for (int e = first + 64; e < last; e += 64) low |= flag(e);
   low = __any(low);
   auto row_of = [&](int i) { return packed_row(64 * wn + i); };
   if constexpr (!SPLIT) {
@@ -582,6 +585,7 @@ hipError_t launch_w4_gemm(W4Op op, const W4Args& a, hipStream_t stream) {
   q.parted = (int*)(ws + p.off_parted);
   q.lows = (float*)(ws + p.off_lows);
   q.sums = (float*)(ws + p.off_sums);
+  q.shift = __builtin_ctz((unsigned)a.group);
   q.in0 = a.in0;
   q.cols = q.ld_out = (int)a.K;
   q.out = ws + p.off_a;

@@ -183,7 +183,8 @@ struct Prepare {
   int* big;     // input gradient
   int* parted;  // products: one per 32 rows x 32 groups
   float* lows;  // products: [ng, O]
-  float* sums;  // products: [rows, ng], each row's sums over the groups
+  float* sums;  // products: [rows, ng], each row's sums over groups of 2^shift
+  int shift;
   // rows: cols values of in0 (gated: cols / 2 of dH in in0 and cols of pre in
   // in1, giving dpre) to out, ld_out apart; out may be NULL with gated
   const void *in0, *in1;

@@ -111,13 +111,12 @@ __device__ __forceinline__ uint32_t f32_to_bits(float v) {
 // The sum over a group of a row's fp16 values, 0 where it is not finite, from
 // eight values of each of the group's lanes.
 __device__ __forceinline__ void sum_group(const Prepare& a, int row, int col, const uint32_t (&v)[8]) {
-  const int group = a.cols / a.ng;
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) s += bits_to_f32<_Float16>(v[i]);
-  for (int d = 1; d < group / 8; d *= 2) s += __shfl_xor(s, d, 64);
-  if (col % group == 0)
-    a.sums[(size_t)row * a.ng + col / group] = fabsf(s) < INFINITY ? s : 0.0f;
+  for (int d = 1; d < (1 << a.shift) / 8; d *= 2) s += __shfl_xor(s, d, 64);
+  if ((col & ((1 << a.shift) - 1)) == 0)
+    a.sums[(size_t)row * a.ng + (col >> a.shift)] = fabsf(s) < INFINITY ? s : 0.0f;
 }
 
 // One row.  GATED: dG = dH U act'(G), dU = dH act(G), each rounded once, into
@@ -194,10 +193,18 @@ __device__ __forceinline__ void prepare_row(const Prepare& a, int row) {
     if (threadIdx.x == 0) a.back[row] = -e;
   }
   if constexpr (SUMS && !SCALE) {
-    for (int c = threadIdx.x * N; c < cols; c += 256 * N) {
-      uint32_t v[8];
-      load_bits<N>(src + c, v);
-      sum_group(a, row, c, v);
+    // four pieces' loads in flight
+    for (int c = threadIdx.x * N; c < cols; c += 4 * 256 * N) {
+      uint4 w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = *(const uint4*)(src + min(c + j * 256 * N, cols - N));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (c + j * 256 * N >= cols) break;
+        uint32_t v[8];
+        load_bits<N>((const uint16_t*)&w[j], v);
+        sum_group(a, row, c + j * 256 * N, v);
+      }
     }
     return;
   }
