@@ -277,3 +277,66 @@ def test_tracked_tensors_are_refused(awq):
     ds, dz = awq.awq_w4a16_param_grad(dy, x, q, s, z)
     for got, want in zip(args, (awq.awq_w4a16_input_grad(dy, q, s, z), ds.to(F16), dz.to(F16))):
         assert torch.equal(got.grad, want)
+
+
+# ------------------------------------------------------------ how calls are made
+def poisoned(awq, op, n, k, o, group, t):
+    """A workspace of exactly the stated size, full of NaN bytes."""
+    size = getattr(awq.load(), f"awq_w4a16_{op}_workspace_size")(n, k, o, group, 0 if t == F16 else 1)
+    return torch.full((max(size, 16),), 255, dtype=torch.uint8, device="cuda")
+
+
+@pytest.mark.parametrize("n,k,o", [(65, 128, 33), (70, 512, 640), (200, 1152, 250), (600, 640, 700), (2, 131072, 40), (90, 4224, 4160)])
+@BY_TYPE
+def test_any_zero_in_a_used_workspace(awq, n, k, o, t, group):
+    """What a call has not written itself stays out of its result: NaN all over the workspace, zeros with remainders in
+    some blocks of 32 rows and groups alone."""
+    _say(f"poisoned {n}x{k}->{o} {t} g{group}")
+    q, s, z = P.make_layer(2 * o, k, group, n, "cuda")
+    z[-1, -1], z[o // 2, 0] = 3.3, 0.4
+    g = torch.Generator().manual_seed(n)
+    x = torch.randn(n, k, generator=g).to(t).cuda()
+    got = awq.awq_w4a16_linear(x, q, s, z, out_dtype=F32, workspace=poisoned(awq, "linear", n, k, 2 * o, group, t))
+    xd, d = x.to(P.F64), E.differences(q, z)
+    e = 2 * (k + 128) * P.U32 * (xd.abs() @ (size(d, z, k) * P.spread(s, k)).T)
+    want = xd @ E.weights(q, s, z).T
+    close(got, want, e, "Y")
+    _, pre = awq.awq_w4a16_gated(x, q, s, z, keep_pre=True, workspace=poisoned(awq, "gated", n, k, o, group, t))
+    close(pre, want, P.rounded(want, e, t), "pre")
+
+
+@pytest.mark.parametrize("n", [1, 20, 64, 100, 600])
+@pytest.mark.parametrize("t", [F16, BF16], ids=str)
+def test_zeros_and_steps_change_between_replays(awq, n, t):
+    """A captured call looks at the layer as it then is: whole zeros, fractions, steps beyond fp16's weights, back."""
+    _say(f"replays {n} {t}")
+    k, o, group = 512, 200, 64
+    q, s, z = P.make_layer(o, k, group, 4, "cuda")
+    g = torch.Generator().manual_seed(n)
+    x = torch.randn(n, k, generator=g).to(t).cuda()
+    dy = (0.001 * torch.randn(n, o, generator=g)).to(t).cuda()
+    whole, step = z.clone(), s.clone()
+
+    def go():
+        y = awq.awq_w4a16_linear(x, q, s, z, out_dtype=F32)
+        return [y, awq.awq_w4a16_input_grad(dy, q, s, z), *awq.awq_w4a16_param_grad(dy, x, q, s, z)]
+
+    go()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = go()
+    seen = []
+    for part, large in ((0.0, False), (0.37, False), (0.37, True), (0.0, False)):
+        z.copy_((whole.float() + part).to(F16))
+        s.copy_(step)
+        if large:
+            s[3, 1] = 400.0
+        eager = go()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(eager, out):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+        seen.append([v.clone() for v in out])
+    assert not torch.equal(seen[0][0], seen[1][0])
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(seen[0], seen[3]))
