@@ -29,8 +29,8 @@
 //     rows of a padded width first (w4_prepare.hip; zeros behind the row's end
 //     meet weights of 0).
 // Bound by the issue of MFMAs and conversions: 4096 x 5120 <- 27648 takes
-// 0.95 ms (1.2 PFLOP/s) of 1.12 with its row scaling, 2048 x 4096 <- 12288 200 us
-// of which 27 are the scaling.
+// 0.95-1.03 ms (1.13-1.22 PFLOP/s over the cards measured) of 1.13-1.18 with its
+// row scaling, 2048 x 4096 <- 12288 203-222 us of which 27 are the scaling.
 #include "w4_internal.h"
 
 namespace awq {

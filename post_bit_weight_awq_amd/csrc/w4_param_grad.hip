@@ -16,8 +16,9 @@
 // fp32, for any fp16 zero.
 // The result is linear in D, so a split tile's parts are split over tokens and
 // write their group sums, 256 x groups pairs, which a second launch adds.
-// Bound by MFMA issue: 4096 tokens, 13824 -> 5120, 0.49 ms (1.17 PFLOP/s);
-// 512 tokens, 4096 x 4096, 21 us, eight steps between prologue and epilogue.
+// Bound by MFMA issue: 4096 tokens, 13824 -> 5120, 0.49-0.52 ms over the cards
+// measured (1.12-1.18 PFLOP/s); 512 tokens, 4096 x 4096, 22-24 us, eight steps
+// between prologue and epilogue.
 #include "w4_internal.h"
 
 namespace awq {

@@ -1,6 +1,8 @@
 // Y = X W^T and H = act(X Wg^T) * (X Wu^T) on packed weights for up to 64
-// tokens: the weights stream from HBM once and bound the call (one token,
-// 5120 -> 15360: 9.4 us, 4.2 TB/s; 48 tokens, gated 5120 -> 2 x 13824: 37 us).
+// tokens: the weights are read once (one token, 5120 -> 15360 in fp16: 42 MB,
+// 10.6 us a call from the 256 MB cache, 11.8 us or 3.5 TB/s from HBM; 48 tokens,
+// gated 5120 -> 2 x 13824 in bf16: 34 and 38 us).  Beside that stream VALU
+// issue bounds it: 0.6 of the busy units' cycles.
 //
 // A block of eight wavefronts owns 32 WR packed rows (gated: 16 WR of the gate
 // and the same features' 16 WR up rows) and all tokens.  The wavefronts are KS
