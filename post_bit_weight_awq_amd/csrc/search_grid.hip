@@ -458,10 +458,11 @@ k_grid_pp(const _Float16* __restrict__ X, const _Float16* __restrict__ W,
   // global address = uniform base + per-lane 32-bit byte offset
   auto dma = [&](const void* base, uint32_t off, const void* l) {
     const uint32_t la = (uint32_t)(uintptr_t)l;
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
+    // a load to LDS needs a wait state behind the write of M0
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                  :
-                 : "v"(off), "s"(base), "s"(la)
-                 : "memory", "m0");
+                 : "v"(off), "s"(base), "{m0}"(la)
+                 : "memory");
   };
   // Loads past the last chunk or group re-read the last one (never used)
   // into the slot the unclamped index selects, so the load counts never vary.

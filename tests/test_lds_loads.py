@@ -11,7 +11,7 @@ ASM = re.compile(r"asm volatile\((.*?)\);", re.S)
 
 
 def loads():
-    for path in sorted(glob.glob(os.path.join(CSRC, "w4_*"))):
+    for path in sorted(glob.glob(os.path.join(CSRC, "*"))):
         with open(path) as f:
             for m in ASM.finditer(f.read()):
                 if "global_load_lds" in m.group(1):
