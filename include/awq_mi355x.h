@@ -368,6 +368,95 @@ int awq_w4a16_param_grad(const void* dY, const void* X, int dtype, int64_t n_tok
                          void* stream);
 
 /* ------------------------------------------------------------------------
+ * A key/value cache held in 4 bits: the groups of the packed weights, along
+ * the columns of a token's head, in pages.  For each token, head and group of
+ * G columns
+ *   step = fp16((hi - lo) / 15), offset = fp16(lo)       lo, hi: least, largest
+ *   code = clamp(rint((x - offset) / step), 0, 15), 0 where step = 0
+ *   value = step * code + offset
+ * in binary32 with IEEE division.  Finite x beyond +-65504 count as that; a
+ * group with an infinity or a NaN reads as NaN.  Place p * page_size + i is
+ * token i of page p.
+ *   k_codes:  [n_pages, n_heads, page_size, head_dim / 8] uint32.  Word J q + j,
+ *             J = head_dim / 32, q = 0..3, holds columns c = 8 (4 j + q) ..
+ *             c + 7, column c + i in bits 4i .. 4i + 3
+ *   v_codes:  [n_pages, n_heads, page_size / 16, head_dim / 8, 16] uint32: word
+ *             [T, b, u] holds columns 8 b .. 8 b + 7 of token 16 T + u
+ *   k_params, v_params: [n_pages, n_heads, page_size, head_dim / group_size, 2]
+ *             fp16: step, offset
+ *   n_heads: 1..1024; page_size: 16, 32, 64 or 128; head_dim: 64 or 128;
+ *   group_size: 32, 64 or 128, at most head_dim; n_pages * page_size < 2^31
+ * The arrays are dense and 16-byte aligned and belong to the caller, who hands
+ * out the pages.  What they hold where nothing was written has no effect.
+ * Source: dev.to page, "What do you actually deploy" (4-bit groups with 16-bit
+ * activations); mbrenndoerfer.com "AWQ > Salient Weight Preservation" (the step
+ * of a group).
+ * ---------------------------------------------------------------------- */
+typedef struct awq_kv4_cache {
+  void *k_codes, *v_codes, *k_params, *v_params;
+  int64_t n_pages;
+  int32_t n_heads, page_size, head_dim, group_size;
+} awq_kv4_cache;
+
+/* Writes the keys and values of n_tokens tokens to their places.
+ *   k, v:  dtype (AWQ_F16 or AWQ_BF16); token t, head h begins t * token_stride +
+ *          h * head_stride values behind, its head_dim values are dense.
+ *          Strides are multiples of 8 from 0 on, pointers 16-byte aligned
+ *   slots: [n_tokens] int32; a token whose slot is negative or past the last
+ *          page is left out.  Two tokens of one call must not have the same
+ *          slot: which of them (or of which a part) it then holds is open
+ *   1 <= n_tokens <= 2^20
+ * Errors: AWQ_ERR_INVALID_ARG for NULL, misaligned or overlapping pointers and
+ * sizes out of range; AWQ_ERR_UNSUPPORTED for another dtype, page_size,
+ * head_dim or group_size (nothing is enqueued); AWQ_ERR_HIP. */
+int awq_kv4_append(const awq_kv4_cache* cache, const void* k, const void* v, int dtype,
+                   int64_t n_tokens, int64_t k_token_stride, int64_t k_head_stride,
+                   int64_t v_token_stride, int64_t v_head_stride, const int32_t* slots,
+                   void* stream);
+
+/* The values at n_tokens places (any, also one place many times), rounded once:
+ *   k, v: [n_tokens, n_heads, head_dim] dtype, dense; zeros where a slot is
+ *         negative or past the last page
+ * Errors: as awq_kv4_append. */
+int awq_kv4_gather(const awq_kv4_cache* cache, const int32_t* slots, int64_t n_tokens, void* k,
+                   void* v, int dtype, void* stream);
+
+/* O[t, h] = sum_j p_j V[j], p = softmax over j of scale * Q[t, h] . K[j], K and V
+ * the values of kv head h / (n_heads / cache->n_heads).
+ * Sequence s has lens[s] keys (those of its query tokens among them): key j lies
+ * at place table[s, j / page_size] * page_size + j % page_size.  Its query tokens
+ * are rows starts[s] .. starts[s + 1] - 1 of Q, the last of which is the last
+ * key: row starts[s + 1] - 1 - i sees the keys below lens[s] - i.  A row that
+ * sees no key gets zeros; rows of no sequence are left as they are.
+ *   q:      dtype (AWQ_F16 or AWQ_BF16), [n_tokens, n_heads, head_dim], strides as
+ *           awq_kv4_append takes them
+ *   starts: [n_seqs + 1] int32, not falling, from 0 to n_tokens; or NULL: one
+ *           token for each sequence, n_tokens = n_seqs
+ *   table:  [n_seqs, max_pages] int32; the keys of a page outside 0..n_pages - 1
+ *           are not seen.  Pages may be shared
+ *   lens:   [n_seqs] int32; taken as at least 0 and at most max_pages * page_size
+ *   scale:  finite
+ *   out:    [n_tokens, n_heads, head_dim] dtype, dense
+ *   n_heads: a multiple of cache->n_heads, up to 1024 times; n_tokens, n_seqs:
+ *           1..2^20, n_tokens * n_heads < 2^31; max_pages * page_size: up to 2^30
+ *   workspace: as the packed-weight operators'; its size depends on the sizes
+ *           alone, not on lens
+ * Codes meet Q without rounding, scores and sums are binary32, the weight of a
+ * key times the step of its values is held in 16 bits (two bf16 parts), the
+ * output rounds once.  Sums have a fixed order for given sizes.  NaN and
+ * infinities at keys that a row does not see do not reach it; a query with an
+ * infinity or a NaN gets NaN.
+ * Errors: as awq_kv4_append; AWQ_ERR_WORKSPACE for a short workspace. */
+size_t awq_kv4_attention_workspace_size(const awq_kv4_cache* cache, int64_t n_tokens,
+                                        int64_t n_heads, int64_t n_seqs, int64_t max_pages,
+                                        int has_starts);
+int awq_kv4_attention(const awq_kv4_cache* cache, const void* q, int dtype, int64_t n_tokens,
+                      int64_t n_heads, int64_t q_token_stride, int64_t q_head_stride,
+                      int64_t n_seqs, const int32_t* starts, const int32_t* table,
+                      int64_t max_pages, const int32_t* lens, float scale, void* out,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Folding 1/s into whatever produces the layer's input channels:
  *   dst[j, c] = fp16( fp32(src[j, c]) / s[j] )   (IEEE binary32 division)
  * for a [rows, cols] fp16 array whose row j feeds input channel j: a norm's

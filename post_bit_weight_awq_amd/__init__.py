@@ -20,14 +20,15 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._lib import AwqConfig, AwqError, AwqSearchPlan, check, load  # noqa: F401
+from ._lib import AwqConfig, AwqError, AwqKv4Cache, AwqSearchPlan, check, load  # noqa: F401
 from ._lib import STAGE_ALL, STAGE_GRID, STAGE_PREPARE, STAGE_SELECT  # noqa: F401
 
 __all__ = ["AwqConfig", "AwqError", "default_config", "awq_act_stats", "awq_act_stats_noalloc",
            "awq_act_stats_workspace_size", "awq_search_plan", "awq_search_workspace_size",
            "awq_search_layer", "awq_pack", "awq_w4a16_matmul", "awq_fold_inverse_scale", "awq_select_top_channels", "awq_weight_saliency",
            "awq_w4a16_linear", "awq_w4a16_gated", "awq_w4a16_input_grad", "awq_w4a16_gated_backward",
-           "awq_w4a16_param_grad", "SearchResult", "load"]
+           "awq_w4a16_param_grad", "Kv4Cache", "awq_kv4_cache", "awq_kv4_append", "awq_kv4_gather",
+           "awq_kv4_attention", "SearchResult", "load"]
 
 
 def default_config(n_grid: int = 20, sal_floor: float = 1e-4, *, group_size: int = 128,
@@ -463,6 +464,181 @@ def awq_w4a16_param_grad(dY: torch.Tensor, X: torch.Tensor, qweight: torch.Tenso
     if rc:
         check(rc)
     return dstep, dzero
+
+
+# ------------------------------------------------- key/value cache in 4 bits
+@dataclass(frozen=True)
+class Kv4Cache:
+    """The arrays of a 4-bit key/value cache (include/awq_mi355x.h has their
+    order); awq_kv4_cache makes one, and a program may bring its own memory.
+    Place p * page_size + i is token i of page p."""
+    k_codes: torch.Tensor   # [n_pages, n_heads, page_size, head_dim / 8] int32
+    v_codes: torch.Tensor   # [n_pages, n_heads, page_size / 16, head_dim / 8, 16] int32
+    k_params: torch.Tensor  # [n_pages, n_heads, page_size, head_dim / group_size, 2] fp16
+    v_params: torch.Tensor  # the same
+
+    @property
+    def n_pages(self) -> int:
+        return self.k_codes.shape[0]
+
+    @property
+    def n_heads(self) -> int:
+        return self.k_codes.shape[1]
+
+    @property
+    def page_size(self) -> int:
+        return self.k_codes.shape[2]
+
+    @property
+    def head_dim(self) -> int:
+        return 8 * self.k_codes.shape[3]
+
+    @property
+    def group_size(self) -> int:
+        return self.head_dim // self.k_params.shape[3]
+
+
+def awq_kv4_cache(n_pages: int, n_heads: int, page_size: int, head_dim: int, group_size: int = 64,
+                  *, device="cuda") -> Kv4Cache:
+    """An empty cache: page_size 16, 32, 64 or 128; head_dim 64 or 128; groups of
+    32, 64 or 128 columns.  0.5 + 4 / group_size bytes for each key and value."""
+    if page_size not in (16, 32, 64, 128) or head_dim not in (64, 128) \
+            or group_size not in (32, 64, 128) or group_size > head_dim:
+        raise AwqError(_lib.AWQ_ERR_UNSUPPORTED, f"page_size={page_size} (16, 32, 64, 128), head_dim="
+                       f"{head_dim} (64, 128), group_size={group_size} (32, 64, 128, at most head_dim)")
+    if n_pages < 1 or n_heads < 1 or n_heads > 1024 or n_pages * page_size >= 2 ** 31:
+        raise AwqError(_lib.AWQ_ERR_INVALID_ARG, f"n_pages={n_pages}, n_heads={n_heads}")
+    w, g = head_dim // 8, head_dim // group_size
+    return Kv4Cache(
+        torch.zeros((n_pages, n_heads, page_size, w), dtype=torch.int32, device=device),
+        torch.zeros((n_pages, n_heads, page_size // 16, w, 16), dtype=torch.int32, device=device),
+        torch.zeros((n_pages, n_heads, page_size, g, 2), dtype=torch.float16, device=device),
+        torch.zeros((n_pages, n_heads, page_size, g, 2), dtype=torch.float16, device=device))
+
+
+def _kv4(cache: Kv4Cache, dev: int) -> AwqKv4Cache:
+    """The C struct of a cache, its arrays checked against each other."""
+    if not isinstance(cache, Kv4Cache):
+        raise TypeError("cache must be a Kv4Cache")
+    kc, kp = cache.k_codes, cache.k_params
+    if kc.dim() != 4 or kp.dim() != 5 or kp.shape[3] == 0:
+        raise ValueError("k_codes must be 4-D and k_params 5-D, with a group")
+    p, h, s, w = kc.shape
+    g = kp.shape[3]
+    if (8 * w) % g:
+        raise ValueError(f"k_params has {g} groups for head_dim={8 * w}")
+    c = AwqKv4Cache()
+    c.k_codes = _w4_ptr(kc, "k_codes", torch.int32, (p, h, s, w), dev)
+    c.v_codes = _w4_ptr(cache.v_codes, "v_codes", torch.int32, (p, h, s // 16, w, 16), dev)
+    c.k_params = _w4_ptr(kp, "k_params", torch.float16, (p, h, s, g, 2), dev)
+    c.v_params = _w4_ptr(cache.v_params, "v_params", torch.float16, (p, h, s, g, 2), dev)
+    c.n_pages, c.n_heads, c.page_size, c.head_dim, c.group_size = p, h, s, 8 * w, 8 * w // g
+    return c
+
+
+def _kv4_rows(t, name: str, heads, dim: int, dtype, dev: int):
+    """(pointer, token stride, head stride) of [tokens, heads, dim] rows, whose
+    strides may be a slice's; heads None: any number."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _DTYPES or (dtype is not None and t.dtype is not dtype):
+        raise TypeError(f"{name} must be {dtype or 'torch.float16 or torch.bfloat16'}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {dim}], got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    if t.requires_grad and torch.is_grad_enabled():
+        _w4_tracked(name)
+    if t.stride(2) != 1:
+        raise ValueError(f"{name}'s last dimension must be dense")
+    # a dimension of one row has no stride of its own
+    return (t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def _kv4_device(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+    return torch._C._cuda_getDevice()
+
+
+def awq_kv4_append(k: torch.Tensor, v: torch.Tensor, cache: Kv4Cache, slots: torch.Tensor, *,
+                   stream=None) -> None:
+    """Quantizes the keys and values of some tokens ([tokens, n_heads, head_dim]
+    fp16 or bf16, slices of a fused projection's output too) into their places,
+    slots [tokens] int32.  A token with a negative slot is left out; no two may
+    have the same slot."""
+    lib, dev = load(), _kv4_device(k, "k")
+    c = _kv4(cache, dev)
+    kp, kt, kh = _kv4_rows(k, "k", c.n_heads, c.head_dim, None, dev)
+    vp, vt, vh = _kv4_rows(v, "v", c.n_heads, c.head_dim, k.dtype, dev)
+    n = k.shape[0]
+    if v.shape[0] != n:
+        raise ValueError(f"k has {n} tokens, v {v.shape[0]}")
+    sp = _w4_ptr(slots, "slots", torch.int32, (n,), dev)
+    rc = lib.awq_kv4_append(ctypes.byref(c), kp, vp, _DTYPES[k.dtype], n, kt, kh, vt, vh, sp,
+                            _w4_stream(stream, dev))
+    if rc:
+        check(rc)
+
+
+def awq_kv4_gather(cache: Kv4Cache, slots: torch.Tensor, *, dtype: torch.dtype = torch.float16,
+                   k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None, stream=None):
+    """(k, v), [tokens, n_heads, head_dim] in dtype: the values that the places
+    slots [tokens] int32 hold, zeros for a negative slot."""
+    lib, dev = load(), _kv4_device(slots, "slots")
+    c = _kv4(cache, dev)
+    if dtype not in _DTYPES:
+        raise TypeError(f"dtype must be torch.float16 or torch.bfloat16, got {dtype}")
+    n = slots.numel()
+    sp = _w4_ptr(slots, "slots", torch.int32, (n,), dev)
+    shape = (n, c.n_heads, c.head_dim)
+    with _on(stream):
+        k, kp = _w4_out(k, "k", dtype, shape, slots, dev)
+        v, vp = _w4_out(v, "v", dtype, shape, slots, dev)
+    rc = lib.awq_kv4_gather(ctypes.byref(c), sp, n, kp, vp, _DTYPES[dtype], _w4_stream(stream, dev))
+    if rc:
+        check(rc)
+    return k, v
+
+
+def awq_kv4_attention(q: torch.Tensor, cache: Kv4Cache, table: torch.Tensor, lens: torch.Tensor, *,
+                      starts: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                      out: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """softmax(scale Q K^T) V over the 4-bit cache, [tokens, heads, head_dim] in
+    q's type.  q [tokens, heads, head_dim] fp16 or bf16 may be a slice; heads is a
+    multiple of the cache's, neighbours share a kv head.  table [seqs, max_pages]
+    int32 has each sequence's pages, lens [seqs] int32 its keys, its newest tokens
+    among them (append them first).  Without starts every sequence has one query
+    token; with it, [seqs + 1] int32, sequence s has rows starts[s] ..
+    starts[s + 1] - 1 of q, its last tokens, each of which sees the keys up to its
+    own.  scale is 1 / sqrt(head_dim) by default.  A row without keys gets zeros,
+    rows behind the last sequence are left as they are."""
+    lib, dev = load(), _kv4_device(q, "q")
+    c = _kv4(cache, dev)
+    qp, qt, qh = _kv4_rows(q, "q", None, c.head_dim, None, dev)
+    n, h, d = q.shape
+    if table.dim() != 2:
+        raise ValueError("table must be [seqs, max_pages]")
+    b, pages = table.shape
+    tp = _w4_ptr(table, "table", torch.int32, (b, pages), dev)
+    lp = _w4_ptr(lens, "lens", torch.int32, (b,), dev)
+    sp = None if starts is None else _w4_ptr(starts, "starts", torch.int32, (b + 1,), dev)
+    with _on(stream):
+        out, op = _w4_out(out, "out", q.dtype, (n, h, d), q, dev)
+        workspace, ws, size = _w4_workspace(lib.awq_kv4_attention_workspace_size,
+                                            (ctypes.byref(c), n, h, b, pages, starts is not None), q,
+                                            workspace)
+    rc = lib.awq_kv4_attention(ctypes.byref(c), qp, _DTYPES[q.dtype], n, h, qt, qh, b, sp, tp, pages, lp,
+                               d ** -0.5 if scale is None else scale, op, ws, size,
+                               _w4_stream(stream, dev))
+    if rc:
+        check(rc)
+    return out
 
 
 def awq_fold_inverse_scale(src: torch.Tensor, s: torch.Tensor, *,

@@ -30,6 +30,7 @@ EXPORTS = (
     "awq_w4a16_input_grad_workspace_size", "awq_w4a16_input_grad",
     "awq_w4a16_gated_backward_workspace_size", "awq_w4a16_gated_backward",
     "awq_w4a16_param_grad_workspace_size", "awq_w4a16_param_grad",
+    "awq_kv4_append", "awq_kv4_gather", "awq_kv4_attention_workspace_size", "awq_kv4_attention",
 )
 DTYPE_F16, DTYPE_BF16, DTYPE_F32 = 0, 1, 2
 ACT_SILU, ACT_GELU_TANH = 0, 1
@@ -46,6 +47,14 @@ class AwqSearchPlan(ctypes.Structure):
                 ("n_token_tiles", ctypes.c_int64), ("n_out_tiles", ctypes.c_int64),
                 ("partials_offset", ctypes.c_size_t), ("scales_offset", ctypes.c_size_t),
                 ("workspace_bytes", ctypes.c_size_t)]
+
+
+class AwqKv4Cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_params", ctypes.c_void_p), ("v_params", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int64), ("n_heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("group_size", ctypes.c_int32)]
 
 
 class AwqError(RuntimeError):
@@ -109,6 +118,16 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.awq_w4a16_gated_backward.argtypes = [P, P, I32, I64, I64, I64, I32, I32, P, P, P, P, P,
                                              P, SZ, P]
     lib.awq_w4a16_param_grad.argtypes = [P, P, I32, I64, I64, I64, I32, P, P, P, P, P, P, SZ, P]
+    C = ctypes.POINTER(AwqKv4Cache)
+    lib.awq_kv4_append.argtypes = [C, P, P, I32, I64, I64, I64, I64, I64, P, P]
+    lib.awq_kv4_append.restype = I32
+    lib.awq_kv4_gather.argtypes = [C, P, I64, P, P, I32, P]
+    lib.awq_kv4_gather.restype = I32
+    lib.awq_kv4_attention_workspace_size.argtypes = [C, I64, I64, I64, I64, I32]
+    lib.awq_kv4_attention_workspace_size.restype = SZ
+    lib.awq_kv4_attention.argtypes = [C, P, I32, I64, I64, I64, I64, I64, P, P, I64, P,
+                                      ctypes.c_float, P, P, SZ, P]
+    lib.awq_kv4_attention.restype = I32
     _lib = lib
     return lib
 

@@ -6,6 +6,7 @@
 
 #include "../../include/awq_mi355x.h"
 #include "awq_internal.h"
+#include "kv4_internal.h"
 
 namespace {
 
@@ -138,6 +139,22 @@ struct W4Bytes {
   int64_t in0, in1, out0, out1;
 };
 
+// A stretch of memory of an argument; NULL ones have none.
+struct Span {
+  const void* p;
+  int64_t n;
+};
+// What a call writes (the first `written`) shares no byte with anything else.
+int check_spans(const Span* r, int written, int count) {
+  for (int i = 0; i < written; ++i)
+    for (int j = i + 1; j < count; ++j) {
+      const uintptr_t x = (uintptr_t)r[i].p, y = (uintptr_t)r[j].p;
+      if (x && y && r[i].n && r[j].n && x < y + r[j].n && y < x + r[i].n)
+        return fail(AWQ_ERR_INVALID_ARG, "an output or the workspace overlaps another argument");
+    }
+  return AWQ_OK;
+}
+
 int run_w4(awq::W4Op op, awq::W4Args& a, const W4Bytes& b, void* workspace, size_t workspace_bytes,
            void* stream, const char* what) {
   const size_t need = awq::w4_workspace(op, a);
@@ -150,19 +167,102 @@ int run_w4(awq::W4Op op, awq::W4Args& a, const W4Bytes& b, void* workspace, size
   a.ws = workspace;
   // what is written (the first three) shares no byte with anything else
   const int64_t groups = 2 * a.O * (a.K / a.group);
-  const struct {
-    const void* p;
-    int64_t n;
-  } r[8] = {{a.out0, b.out0},    {a.out1, b.out1},        {a.ws, (int64_t)need},
-            {a.in0, b.in0},      {a.in1, b.in1},          {a.qweight, a.O * a.K / 2},
-            {a.step16, groups},  {a.zero16, groups}};
-  for (int i = 0; i < 3; ++i)
-    for (int j = i + 1; j < 8; ++j) {
-      const uintptr_t x = (uintptr_t)r[i].p, y = (uintptr_t)r[j].p;
-      if (x && y && r[i].n && r[j].n && x < y + r[j].n && y < x + r[i].n)
-        return fail(AWQ_ERR_INVALID_ARG, "an output or the workspace overlaps another argument");
-    }
+  const Span r[8] = {{a.out0, b.out0},   {a.out1, b.out1},       {a.ws, (int64_t)need},
+                     {a.in0, b.in0},     {a.in1, b.in1},         {a.qweight, a.O * a.K / 2},
+                     {a.step16, groups}, {a.zero16, groups}};
+  int rc;
+  if ((rc = check_spans(r, 3, 8))) return rc;
   return hip_result(awq::launch_w4(op, a, (hipStream_t)stream), what);
+}
+
+int check_16bit(int dtype) {
+  if (dtype != AWQ_F16 && dtype != AWQ_BF16)
+    return fail(AWQ_ERR_UNSUPPORTED, "dtype=%d: AWQ_F16 and AWQ_BF16 are implemented", dtype);
+  return AWQ_OK;
+}
+
+int check_count(int64_t n, int64_t most, const char* name) {
+  if (n < 1 || n > most)
+    return fail(AWQ_ERR_INVALID_ARG, "%s=%lld outside 1..%lld", name, (long long)n, (long long)most);
+  return AWQ_OK;
+}
+
+// Sizes of a 4-bit cache, without its pointers.
+int check_kv4(const awq_kv4_cache* c, awq::Kv4* out) {
+  int rc;
+  if (!c) return fail(AWQ_ERR_INVALID_ARG, "cache is NULL");
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+    return fail(AWQ_ERR_UNSUPPORTED, "page_size=%d: 16, 32, 64 and 128 are implemented", c->page_size);
+  if (c->head_dim != 64 && c->head_dim != 128)
+    return fail(AWQ_ERR_UNSUPPORTED, "head_dim=%d: 64 and 128 are implemented", c->head_dim);
+  if ((c->group_size != 32 && c->group_size != 64 && c->group_size != 128) ||
+      c->group_size > c->head_dim)
+    return fail(AWQ_ERR_UNSUPPORTED, "group_size=%d: 32, 64 and 128, at most head_dim=%d",
+                c->group_size, c->head_dim);
+  if ((rc = check_count(c->n_heads, 1024, "cache n_heads")) ||
+      (rc = check_count(c->n_pages, 0x7fffffff / c->page_size, "n_pages")))
+    return rc;
+  out->k_codes = (uint32_t*)c->k_codes;
+  out->v_codes = (uint32_t*)c->v_codes;
+  out->k_params = (uint32_t*)c->k_params;
+  out->v_params = (uint32_t*)c->v_params;
+  out->pages = c->n_pages;
+  out->heads = c->n_heads;
+  out->shift = __builtin_ctz((unsigned)c->page_size);
+  out->dim = c->head_dim;
+  out->group = c->group_size;
+  return AWQ_OK;
+}
+int check_kv4_arrays(const awq::Kv4& c) {
+  int rc;
+  if ((rc = check_ptr(c.k_codes, "k_codes")) || (rc = check_ptr(c.v_codes, "v_codes")) ||
+      (rc = check_ptr(c.k_params, "k_params")) || (rc = check_ptr(c.v_params, "v_params")))
+    return rc;
+  return AWQ_OK;
+}
+int64_t kv4_code_bytes(const awq::Kv4& c) { return (c.pages << c.shift) * c.heads * (c.dim / 2); }
+int64_t kv4_param_bytes(const awq::Kv4& c) {
+  return (c.pages << c.shift) * c.heads * (c.dim / c.group) * 4;
+}
+
+int check_stride(int64_t s, const char* name) {
+  if (s < 0 || s % 8 || s > ((int64_t)1 << 40))
+    return fail(AWQ_ERR_INVALID_ARG, "%s=%lld: a multiple of 8 from 0 to 2^40", name, (long long)s);
+  return AWQ_OK;
+}
+int64_t rows_bytes(int64_t tokens, int64_t heads, int64_t dim, int64_t ts, int64_t hs) {
+  return 2 * ((tokens - 1) * ts + (heads - 1) * hs + dim);
+}
+int check_index(const void* p, const char* name) {
+  if (!p) return fail(AWQ_ERR_INVALID_ARG, "%s is NULL", name);
+  if ((uintptr_t)p & 3u) return fail(AWQ_ERR_INVALID_ARG, "%s is not 4-byte aligned", name);
+  return AWQ_OK;
+}
+
+int kv4_attention_args(const awq_kv4_cache* cache, int64_t n_tokens, int64_t n_heads, int64_t n_seqs,
+                       int64_t max_pages, bool ragged, awq::Kv4Attention* a) {
+  int rc;
+  if ((rc = check_kv4(cache, &a->cache)) ||
+      (rc = check_count(n_tokens, awq::kMaxW4OpTokens, "n_tokens")) ||
+      (rc = check_count(n_seqs, awq::kMaxW4OpTokens, "n_seqs")) ||
+      (rc = check_count(max_pages, ((int64_t)1 << 30) >> a->cache.shift, "max_pages")))
+    return rc;
+  if (n_heads < 1 || n_heads % a->cache.heads || n_heads / a->cache.heads > 1024 ||
+      n_tokens * n_heads > 0x7fffffff)
+    return fail(AWQ_ERR_INVALID_ARG,
+                "n_heads=%lld must be a multiple of the cache's %d, up to 1024 times, and n_tokens * "
+                "n_heads below 2^31",
+                (long long)n_heads, a->cache.heads);
+  if (!ragged && n_tokens != n_seqs)
+    return fail(AWQ_ERR_INVALID_ARG, "n_tokens=%lld and n_seqs=%lld differ and starts is NULL",
+                (long long)n_tokens, (long long)n_seqs);
+  a->heads = (int)n_heads;
+  a->tokens = n_tokens;
+  a->seqs = n_seqs;
+  a->per_seq = max_pages;
+  static const int32_t here = 0;
+  a->starts = ragged ? &here : nullptr;
+  return AWQ_OK;
 }
 
 }  // namespace
@@ -463,6 +563,110 @@ int awq_w4a16_param_grad(const void* dY, const void* X, int dtype, int64_t n_tok
   const W4Bytes b{2 * a.N * a.O, 2 * a.N * a.K, params, params};
   return run_w4(awq::kOpParamGrad, a, b, workspace, workspace_bytes, stream,
                 "awq_w4a16_param_grad launch");
+}
+
+int awq_kv4_append(const awq_kv4_cache* cache, const void* k, const void* v, int dtype,
+                   int64_t n_tokens, int64_t k_token_stride, int64_t k_head_stride,
+                   int64_t v_token_stride, int64_t v_head_stride, const int32_t* slots,
+                   void* stream) {
+  int rc;
+  awq::Kv4 c;
+  if ((rc = check_kv4(cache, &c)) || (rc = check_16bit(dtype)) ||
+      (rc = check_count(n_tokens, awq::kMaxW4OpTokens, "n_tokens")) || (rc = check_kv4_arrays(c)) ||
+      (rc = check_ptr(k, "k")) || (rc = check_ptr(v, "v")) || (rc = check_index(slots, "slots")) ||
+      (rc = check_stride(k_token_stride, "k_token_stride")) ||
+      (rc = check_stride(k_head_stride, "k_head_stride")) ||
+      (rc = check_stride(v_token_stride, "v_token_stride")) ||
+      (rc = check_stride(v_head_stride, "v_head_stride")))
+    return rc;
+  const Span r[7] = {{c.k_codes, kv4_code_bytes(c)},
+                     {c.v_codes, kv4_code_bytes(c)},
+                     {c.k_params, kv4_param_bytes(c)},
+                     {c.v_params, kv4_param_bytes(c)},
+                     {k, rows_bytes(n_tokens, c.heads, c.dim, k_token_stride, k_head_stride)},
+                     {v, rows_bytes(n_tokens, c.heads, c.dim, v_token_stride, v_head_stride)},
+                     {slots, 4 * n_tokens}};
+  if ((rc = check_spans(r, 4, 7))) return rc;
+  const awq::Kv4Rows rows{k, v, k_token_stride, k_head_stride, v_token_stride, v_head_stride};
+  return hip_result(awq::launch_kv4_append(c, rows, dtype, n_tokens, slots, (hipStream_t)stream),
+                    "awq_kv4_append launch");
+}
+
+int awq_kv4_gather(const awq_kv4_cache* cache, const int32_t* slots, int64_t n_tokens, void* k,
+                   void* v, int dtype, void* stream) {
+  int rc;
+  awq::Kv4 c;
+  if ((rc = check_kv4(cache, &c)) || (rc = check_16bit(dtype)) ||
+      (rc = check_count(n_tokens, awq::kMaxW4OpTokens, "n_tokens")) || (rc = check_kv4_arrays(c)) ||
+      (rc = check_index(slots, "slots")) || (rc = check_ptr(k, "k")) || (rc = check_ptr(v, "v")))
+    return rc;
+  const int64_t bytes = 2 * n_tokens * c.heads * c.dim;
+  const Span r[7] = {{k, bytes},
+                     {v, bytes},
+                     {slots, 4 * n_tokens},
+                     {c.k_codes, kv4_code_bytes(c)},
+                     {c.v_codes, kv4_code_bytes(c)},
+                     {c.k_params, kv4_param_bytes(c)},
+                     {c.v_params, kv4_param_bytes(c)}};
+  if ((rc = check_spans(r, 2, 7))) return rc;
+  return hip_result(awq::launch_kv4_gather(c, n_tokens, slots, k, v, dtype, (hipStream_t)stream),
+                    "awq_kv4_gather launch");
+}
+
+size_t awq_kv4_attention_workspace_size(const awq_kv4_cache* cache, int64_t n_tokens,
+                                        int64_t n_heads, int64_t n_seqs, int64_t max_pages,
+                                        int has_starts) {
+  awq::Kv4Attention a{};
+  if (kv4_attention_args(cache, n_tokens, n_heads, n_seqs, max_pages, has_starts != 0, &a))
+    return (size_t)-1;
+  ok();
+  return awq::kv4_attention_workspace(a);
+}
+
+int awq_kv4_attention(const awq_kv4_cache* cache, const void* q, int dtype, int64_t n_tokens,
+                      int64_t n_heads, int64_t q_token_stride, int64_t q_head_stride,
+                      int64_t n_seqs, const int32_t* starts, const int32_t* table,
+                      int64_t max_pages, const int32_t* lens, float scale, void* out,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  int rc;
+  awq::Kv4Attention a{};
+  if ((rc = kv4_attention_args(cache, n_tokens, n_heads, n_seqs, max_pages, starts != nullptr, &a)) ||
+      (rc = check_16bit(dtype)) || (rc = check_kv4_arrays(a.cache)) || (rc = check_ptr(q, "q")) ||
+      (rc = check_ptr(out, "out")) || (rc = check_index(table, "table")) ||
+      (rc = check_index(lens, "lens")) || (starts && (rc = check_index(starts, "starts"))) ||
+      (rc = check_stride(q_token_stride, "q_token_stride")) ||
+      (rc = check_stride(q_head_stride, "q_head_stride")))
+    return rc;
+  if (!(scale - scale == 0.0f)) return fail(AWQ_ERR_INVALID_ARG, "scale must be finite");
+  const size_t need = awq::kv4_attention_workspace(a);
+  if (need) {
+    if ((rc = check_ptr(workspace, "workspace"))) return rc;
+    if (workspace_bytes < need)
+      return fail(AWQ_ERR_WORKSPACE, "workspace %zu bytes < %zu required", workspace_bytes, need);
+  }
+  a.q = q;
+  a.out = out;
+  a.type = dtype;
+  a.q_token = q_token_stride;
+  a.q_head = q_head_stride;
+  a.starts = starts;
+  a.table = table;
+  a.lens = lens;
+  a.scale = scale;
+  a.ws = workspace;
+  const awq::Kv4& c = a.cache;
+  const Span r[10] = {{out, 2 * n_tokens * n_heads * c.dim},
+                      {workspace, (int64_t)need},
+                      {q, rows_bytes(n_tokens, n_heads, c.dim, q_token_stride, q_head_stride)},
+                      {starts, 4 * (n_seqs + 1)},
+                      {table, 4 * n_seqs * max_pages},
+                      {lens, 4 * n_seqs},
+                      {c.k_codes, kv4_code_bytes(c)},
+                      {c.v_codes, kv4_code_bytes(c)},
+                      {c.k_params, kv4_param_bytes(c)},
+                      {c.v_params, kv4_param_bytes(c)}};
+  if ((rc = check_spans(r, 2, 10))) return rc;
+  return hip_result(awq::launch_kv4_attention(a, (hipStream_t)stream), "awq_kv4_attention launch");
 }
 
 int awq_fold_inverse_scale(const void* src, const float* s, int64_t rows, int64_t cols, void* dst,
