@@ -367,6 +367,54 @@ int awq_w4a16_param_grad(const void* dY, const void* X, int dtype, int64_t n_tok
                          float* dstep, float* dzero, void* workspace, size_t workspace_bytes,
                          void* stream);
 
+/* Adapters of many requests beside one packed projection: with a = adapter[t]
+ *   low[t, r] = sum_k X[t, k] A[a, r, k]
+ *   Y[t, o]   = sum_k X[t, k] W[o, k] + scale[a] sum_r low[t, r] B[a, o, r]
+ * A token whose adapter is outside 0..n_adapters - 1 has the first sum alone (and
+ * a low of zeros).
+ *   A: [n_adapters, rank, in_features], B: [n_adapters, out_features, rank], dtype,
+ *      finite; a smaller rank is padded with zeros
+ *   scale: [n_adapters] fp32, finite; adapter: [n_tokens] int32; 4-byte aligned
+ *   rank: a multiple of 8 from 8 to 128; n_adapters: 1..32768,
+ *      n_adapters * rank * in_features (out_features) at most 2^34
+ *   Y: [n_tokens, out_features] y_dtype, as awq_w4a16_linear's
+ *   low: [n_tokens, rank] fp32 or NULL: what the backward pass reads.  The
+ *      workspace's size is asked for with keep_low 1 where it is given
+ * low is held in binary32; the second sum takes it in binary32 or as 16-bit parts
+ * that keep 16 bits or more (22 in fp16, 24 for AWQ_F32 outputs in bf16), fp16's
+ * down to 2^-39 of a token's largest.  The two sums are added in binary32. */
+size_t awq_w4a16_adapted_workspace_size(int64_t n_tokens, int64_t in_features, int64_t out_features,
+                                        int group_size, int dtype, int y_dtype, int64_t n_adapters,
+                                        int rank, int keep_low);
+int awq_w4a16_adapted(const void* X, int dtype, int64_t n_tokens, int64_t in_features,
+                      int64_t out_features, int group_size, const int32_t* qweight,
+                      const void* step16, const void* zero16, const void* A, const void* B,
+                      const float* scale, int64_t n_adapters, int rank, const int32_t* adapter,
+                      void* Y, int y_dtype, float* low, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/* Its backward pass, the packed layer and the scales frozen: with a = adapter[t]
+ *   v[t, r] = scale[a] sum_o dY[t, o] B[a, o, r]
+ *   dX[t]   = dY[t] W + v[t] A[a]              (W as awq_w4a16_input_grad takes it)
+ *   dA[a, r, k] = sum over a's tokens of v[t, r] X[t, k]
+ *   dB[a, o, r] = scale[a] sum over a's tokens of dY[t, o] low[t, r]
+ *   dY: [n_tokens, out_features], X, dX: [n_tokens, in_features], dtype
+ *   low: as the forward pass left it, finite where an adapter is
+ *   dA, dB: A's and B's shapes in fp32, overwritten; zeros for an adapter without
+ *      tokens
+ * v and low are held in binary32; the gradients take them as parts of 22 bits
+ * (fp16: down to 2^-39 of the largest among the tokens taken together) or 24. */
+size_t awq_w4a16_adapted_backward_workspace_size(int64_t n_tokens, int64_t in_features,
+                                                 int64_t out_features, int group_size, int dtype,
+                                                 int64_t n_adapters, int rank);
+int awq_w4a16_adapted_backward(const void* dY, const void* X, const float* low, int dtype,
+                               int64_t n_tokens, int64_t in_features, int64_t out_features,
+                               int group_size, const int32_t* qweight, const void* step16,
+                               const void* zero16, const void* A, const void* B, const float* scale,
+                               int64_t n_adapters, int rank, const int32_t* adapter, void* dX,
+                               float* dA, float* dB, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
 /* ------------------------------------------------------------------------
  * A key/value cache held in 4 bits: the groups of the packed weights, along
  * the columns of a token's head, in pages.  For each token, head and group of

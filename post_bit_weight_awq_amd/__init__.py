@@ -27,7 +27,7 @@ __all__ = ["AwqConfig", "AwqError", "default_config", "awq_act_stats", "awq_act_
            "awq_act_stats_workspace_size", "awq_search_plan", "awq_search_workspace_size",
            "awq_search_layer", "awq_pack", "awq_w4a16_matmul", "awq_fold_inverse_scale", "awq_select_top_channels", "awq_weight_saliency",
            "awq_w4a16_linear", "awq_w4a16_gated", "awq_w4a16_input_grad", "awq_w4a16_gated_backward",
-           "awq_w4a16_param_grad", "Kv4Cache", "awq_kv4_cache", "awq_kv4_append", "awq_kv4_gather",
+           "awq_w4a16_param_grad", "awq_w4a16_adapted", "awq_w4a16_adapted_backward", "Kv4Cache", "awq_kv4_cache", "awq_kv4_append", "awq_kv4_gather",
            "awq_kv4_attention", "SearchResult", "load"]
 
 
@@ -259,7 +259,8 @@ def _w4_tracked(name: str):
     raise RuntimeError(
         f"{name} requires a gradient, and these calls record none: a result would silently be cut "
         "off from it. Call them under torch.no_grad() or inside a torch.autograd.Function, whose "
-        "backward calls awq_w4a16_input_grad, awq_w4a16_gated_backward and awq_w4a16_param_grad")
+        "backward calls awq_w4a16_input_grad, awq_w4a16_gated_backward, awq_w4a16_adapted_backward and "
+        "awq_w4a16_param_grad")
 
 
 def _w4_ptr(t, name: str, dtype: torch.dtype, shape, dev: int) -> int:
@@ -464,6 +465,80 @@ def awq_w4a16_param_grad(dY: torch.Tensor, X: torch.Tensor, qweight: torch.Tenso
     if rc:
         check(rc)
     return dstep, dzero
+
+
+def _w4_adapters(A, B, scale, adapter, lead, n: int, k: int, o: int, dev: int):
+    """Checks a stack of adapters; (count, rank, pointers)."""
+    if A.dim() != 3:
+        raise ValueError("A must be [adapters, rank, in_features]")
+    count, rank = A.shape[0], A.shape[1]
+    return count, rank, (_w4_ptr(A, "A", lead.dtype, (count, rank, k), dev),
+                         _w4_ptr(B, "B", lead.dtype, (count, o, rank), dev),
+                         _w4_ptr(scale, "scale", torch.float32, (count,), dev)), \
+        _w4_ptr(adapter, "adapter", torch.int32, (n,), dev)
+
+
+def awq_w4a16_adapted(X: torch.Tensor, qweight: torch.Tensor, step: torch.Tensor, zero: torch.Tensor,
+                      A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor, adapter: torch.Tensor, *,
+                      keep_low: bool = False, low: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None):
+    """Y = X W^T plus each token's own adapter: scale[a] (X A[a]^T) B[a]^T with
+    a = adapter[t].  The packed layer and X as awq_w4a16_linear takes them; A
+    [adapters, rank, in], B [adapters, out, rank] in X's type, scale [adapters] fp32,
+    adapter [tokens] int32 (a negative one: none); rank a multiple of 8 up to 128.
+    With keep_low (or a low buffer) returns (Y, low), low = X A^T [tokens, rank] fp32,
+    which the backward pass reads."""
+    lib = load()
+    dt, n, k, o, group, layer, dev = _w4_layer(X, "X", qweight, step, zero)
+    if out_dtype is None:
+        out_dtype = X.dtype if out is None else out.dtype
+    if out_dtype is not X.dtype and out_dtype is not torch.float32:
+        raise TypeError(f"out_dtype must be {X.dtype} or torch.float32, got {out_dtype}")
+    x = _w4_ptr(X, "X", X.dtype, (n, k), dev)
+    count, rank, stack, ids = _w4_adapters(A, B, scale, adapter, X, n, k, o, dev)
+    yt = _lib.DTYPE_F32 if out_dtype is torch.float32 else dt
+    p = None
+    with _on(stream):
+        out, y = _w4_out(out, "out", out_dtype, (n, o), X, dev)
+        if keep_low or low is not None:
+            low, p = _w4_out(low, "low", torch.float32, (n, rank), X, dev)
+        workspace, ws, size = _w4_workspace(lib.awq_w4a16_adapted_workspace_size,
+                                            (n, k, o, group, dt, yt, count, rank, p is not None), X,
+                                            workspace)
+    rc = lib.awq_w4a16_adapted(x, dt, n, k, o, group, *layer, *stack, count, rank, ids, y, yt, p, ws,
+                               size, _w4_stream(stream, dev))
+    if rc:
+        check(rc)
+    return out if low is None else (out, low)
+
+
+def awq_w4a16_adapted_backward(dY: torch.Tensor, X: torch.Tensor, low: torch.Tensor,
+                               qweight: torch.Tensor, step: torch.Tensor, zero: torch.Tensor,
+                               A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor,
+                               adapter: torch.Tensor, *, out: Optional[torch.Tensor] = None,
+                               dA: Optional[torch.Tensor] = None, dB: Optional[torch.Tensor] = None,
+                               workspace: Optional[torch.Tensor] = None, stream=None):
+    """(dX, dA, dB) of awq_w4a16_adapted from the gradient of Y and the kept low; dX
+    in dY's type, dA and dB fp32 in A's and B's shapes (zeros for an adapter without
+    tokens).  The packed layer and the scales are frozen."""
+    lib = load()
+    dt, n, k, o, group, layer, dev = _w4_layer(dY, "dY", qweight, step, zero)
+    d = _w4_ptr(dY, "dY", dY.dtype, (n, o), dev)
+    x = _w4_ptr(X, "X", dY.dtype, (n, k), dev)
+    count, rank, stack, ids = _w4_adapters(A, B, scale, adapter, dY, n, k, o, dev)
+    p = _w4_ptr(low, "low", torch.float32, (n, rank), dev)
+    with _on(stream):
+        out, dx = _w4_out(out, "out", dY.dtype, (n, k), dY, dev)
+        dA, da = _w4_out(dA, "dA", torch.float32, (count, rank, k), dY, dev)
+        dB, db = _w4_out(dB, "dB", torch.float32, (count, o, rank), dY, dev)
+        workspace, ws, size = _w4_workspace(lib.awq_w4a16_adapted_backward_workspace_size,
+                                            (n, k, o, group, dt, count, rank), dY, workspace)
+    rc = lib.awq_w4a16_adapted_backward(d, x, p, dt, n, k, o, group, *layer, *stack, count, rank, ids,
+                                        dx, da, db, ws, size, _w4_stream(stream, dev))
+    if rc:
+        check(rc)
+    return out, dA, dB
 
 
 # ------------------------------------------------- key/value cache in 4 bits

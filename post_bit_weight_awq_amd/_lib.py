@@ -30,6 +30,8 @@ EXPORTS = (
     "awq_w4a16_input_grad_workspace_size", "awq_w4a16_input_grad",
     "awq_w4a16_gated_backward_workspace_size", "awq_w4a16_gated_backward",
     "awq_w4a16_param_grad_workspace_size", "awq_w4a16_param_grad",
+    "awq_w4a16_adapted_workspace_size", "awq_w4a16_adapted",
+    "awq_w4a16_adapted_backward_workspace_size", "awq_w4a16_adapted_backward",
     "awq_kv4_append", "awq_kv4_gather", "awq_kv4_attention_workspace_size", "awq_kv4_attention",
 )
 DTYPE_F16, DTYPE_BF16, DTYPE_F32 = 0, 1, 2
@@ -118,6 +120,16 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.awq_w4a16_gated_backward.argtypes = [P, P, I32, I64, I64, I64, I32, I32, P, P, P, P, P,
                                              P, SZ, P]
     lib.awq_w4a16_param_grad.argtypes = [P, P, I32, I64, I64, I64, I32, P, P, P, P, P, P, SZ, P]
+    lib.awq_w4a16_adapted_workspace_size.argtypes = [I64, I64, I64, I32, I32, I32, I64, I32, I32]
+    lib.awq_w4a16_adapted_workspace_size.restype = SZ
+    lib.awq_w4a16_adapted.argtypes = [P, I32, I64, I64, I64, I32, P, P, P, P, P, P, I64, I32, P, P, I32,
+                                      P, P, SZ, P]
+    lib.awq_w4a16_adapted.restype = I32
+    lib.awq_w4a16_adapted_backward_workspace_size.argtypes = [I64, I64, I64, I32, I32, I64, I32]
+    lib.awq_w4a16_adapted_backward_workspace_size.restype = SZ
+    lib.awq_w4a16_adapted_backward.argtypes = [P, P, P, I32, I64, I64, I64, I32, P, P, P, P, P, P, I64,
+                                               I32, P, P, P, P, P, SZ, P]
+    lib.awq_w4a16_adapted_backward.restype = I32
     C = ctypes.POINTER(AwqKv4Cache)
     lib.awq_kv4_append.argtypes = [C, P, P, I32, I64, I64, I64, I64, I64, P, P]
     lib.awq_kv4_append.restype = I32

@@ -265,6 +265,74 @@ int kv4_attention_args(const awq_kv4_cache* cache, int64_t n_tokens, int64_t n_h
   return AWQ_OK;
 }
 
+int check_adapters(int64_t n_adapters, int rank, int64_t in_features, int64_t out_features) {
+  int rc;
+  if (rank < 8 || rank > 128 || rank % 8)
+    return fail(AWQ_ERR_UNSUPPORTED, "rank=%d: multiples of 8 from 8 to 128 are implemented", rank);
+  if ((rc = check_count(n_adapters, awq::kMaxAdapters, "n_adapters"))) return rc;
+  if (n_adapters * rank * in_features > kMaxWeights || n_adapters * rank * out_features > kMaxWeights)
+    return fail(AWQ_ERR_INVALID_ARG, "n_adapters=%lld of rank %d are more than %lld values",
+                (long long)n_adapters, rank, (long long)kMaxWeights);
+  return AWQ_OK;
+}
+int check_y_type(int dtype, int y_dtype) {
+  if (y_dtype != dtype && y_dtype != AWQ_F32)
+    return fail(AWQ_ERR_UNSUPPORTED, "y_dtype=%d: dtype (%d) or AWQ_F32", y_dtype, dtype);
+  return AWQ_OK;
+}
+
+int run_adapted(awq::W4Args& a, const awq::W4Adapt& d, bool backward, void* workspace,
+                size_t workspace_bytes, void* stream, const char* what) {
+  int rc;
+  if ((rc = check_ptr(d.A, "A")) || (rc = check_ptr(d.B, "B")) || (rc = check_index(d.scale, "scale")) ||
+      (rc = check_index(d.ids, "adapter")))
+    return rc;
+  const size_t need = awq::w4_adapt_workspace(a, d, backward);
+  if (need) {
+    if ((rc = check_ptr(workspace, "workspace"))) return rc;
+    if (workspace_bytes < need)
+      return fail(AWQ_ERR_WORKSPACE, "workspace %zu bytes < %zu required", workspace_bytes, need);
+  }
+  a.ws = workspace;
+  const int64_t x = 2 * a.N * a.K, y = (a.y_type == AWQ_F32 ? 4 : 2) * a.N * a.O;
+  const int64_t params = 2 * a.O * (a.K / a.group), na = d.count * (int64_t)d.rank * a.K,
+                nb = d.count * (int64_t)d.rank * a.O, low = 4 * a.N * d.rank;
+  const Span layer[7] = {{a.qweight, a.O * a.K / 2}, {a.step16, params}, {a.zero16, params},
+                         {d.A, 2 * na},              {d.B, 2 * nb},      {d.scale, 4 * (int64_t)d.count},
+                         {d.ids, 4 * a.N}};
+  Span r[14] = {{a.ws, (int64_t)need}};
+  int n = 1, written;
+  if (backward) {
+    r[n++] = {a.out0, x};
+    r[n++] = {d.dA, 4 * na};
+    r[n++] = {d.dB, 4 * nb};
+    written = n;
+    r[n++] = {a.in0, y};
+    r[n++] = {a.in1, x};
+    r[n++] = {d.low, low};
+  } else {
+    r[n++] = {a.out0, y};
+    r[n++] = {d.low, low};
+    written = n;
+    r[n++] = {a.in0, x};
+  }
+  for (const Span& s : layer) r[n++] = s;
+  if ((rc = check_spans(r, written, n))) return rc;
+  return hip_result(awq::launch_w4_adapt(a, d, backward, (hipStream_t)stream), what);
+}
+
+awq::W4Adapt adapt_args(const void* A, const void* B, const float* scale, int64_t n_adapters,
+                        int rank, const int32_t* adapter) {
+  awq::W4Adapt d{};
+  d.A = A;
+  d.B = B;
+  d.scale = scale;
+  d.ids = adapter;
+  d.count = (int)n_adapters;
+  d.rank = rank;
+  return d;
+}
+
 }  // namespace
 
 extern "C" {
@@ -435,8 +503,7 @@ int awq_w4a16_linear(const void* X, int dtype, int64_t n_tokens, int64_t in_feat
                      size_t workspace_bytes, void* stream) {
   int rc;
   if ((rc = check_w4(n_tokens, in_features, out_features, group_size, dtype))) return rc;
-  if (y_dtype != dtype && y_dtype != AWQ_F32)
-    return fail(AWQ_ERR_UNSUPPORTED, "y_dtype=%d: dtype (%d) or AWQ_F32", y_dtype, dtype);
+  if ((rc = check_y_type(dtype, y_dtype))) return rc;
   if ((rc = check_ptr(X, "X")) || (rc = check_layer(qweight, step16, zero16)) ||
       (rc = check_ptr(Y, "Y")))
     return rc;
@@ -563,6 +630,84 @@ int awq_w4a16_param_grad(const void* dY, const void* X, int dtype, int64_t n_tok
   const W4Bytes b{2 * a.N * a.O, 2 * a.N * a.K, params, params};
   return run_w4(awq::kOpParamGrad, a, b, workspace, workspace_bytes, stream,
                 "awq_w4a16_param_grad launch");
+}
+
+size_t awq_w4a16_adapted_workspace_size(int64_t n_tokens, int64_t in_features, int64_t out_features,
+                                        int group_size, int dtype, int y_dtype, int64_t n_adapters,
+                                        int rank, int keep_low) {
+  if (check_w4(n_tokens, in_features, out_features, group_size, dtype) ||
+      check_y_type(dtype, y_dtype) || check_adapters(n_adapters, rank, in_features, out_features))
+    return (size_t)-1;
+  ok();
+  awq::W4Args a = w4_args(n_tokens, in_features, out_features, group_size, dtype, 0, nullptr, nullptr,
+                          nullptr);
+  a.y_type = y_dtype;
+  awq::W4Adapt d = adapt_args(nullptr, nullptr, nullptr, n_adapters, rank, nullptr);
+  float kept;
+  d.low = keep_low ? &kept : nullptr;
+  return awq::w4_adapt_workspace(a, d, false);
+}
+
+int awq_w4a16_adapted(const void* X, int dtype, int64_t n_tokens, int64_t in_features,
+                      int64_t out_features, int group_size, const int32_t* qweight,
+                      const void* step16, const void* zero16, const void* A, const void* B,
+                      const float* scale, int64_t n_adapters, int rank, const int32_t* adapter,
+                      void* Y, int y_dtype, float* low, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  int rc;
+  if ((rc = check_w4(n_tokens, in_features, out_features, group_size, dtype)) ||
+      (rc = check_y_type(dtype, y_dtype)) ||
+      (rc = check_adapters(n_adapters, rank, in_features, out_features)) || (rc = check_ptr(X, "X")) ||
+      (rc = check_layer(qweight, step16, zero16)) || (rc = check_ptr(Y, "Y")) ||
+      (low && (rc = check_ptr(low, "low"))))
+    return rc;
+  awq::W4Args a = w4_args(n_tokens, in_features, out_features, group_size, dtype, 0, qweight, step16,
+                          zero16);
+  a.y_type = y_dtype;
+  a.in0 = X;
+  a.out0 = Y;
+  awq::W4Adapt d = adapt_args(A, B, scale, n_adapters, rank, adapter);
+  d.low = low;
+  return run_adapted(a, d, false, workspace, workspace_bytes, stream, "awq_w4a16_adapted launch");
+}
+
+size_t awq_w4a16_adapted_backward_workspace_size(int64_t n_tokens, int64_t in_features,
+                                                 int64_t out_features, int group_size, int dtype,
+                                                 int64_t n_adapters, int rank) {
+  if (check_w4(n_tokens, in_features, out_features, group_size, dtype) ||
+      check_adapters(n_adapters, rank, in_features, out_features))
+    return (size_t)-1;
+  ok();
+  return awq::w4_adapt_workspace(
+      w4_args(n_tokens, in_features, out_features, group_size, dtype, 0, nullptr, nullptr, nullptr),
+      adapt_args(nullptr, nullptr, nullptr, n_adapters, rank, nullptr), true);
+}
+
+int awq_w4a16_adapted_backward(const void* dY, const void* X, const float* low, int dtype,
+                               int64_t n_tokens, int64_t in_features, int64_t out_features,
+                               int group_size, const int32_t* qweight, const void* step16,
+                               const void* zero16, const void* A, const void* B, const float* scale,
+                               int64_t n_adapters, int rank, const int32_t* adapter, void* dX,
+                               float* dA, float* dB, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  int rc;
+  if ((rc = check_w4(n_tokens, in_features, out_features, group_size, dtype)) ||
+      (rc = check_adapters(n_adapters, rank, in_features, out_features)) ||
+      (rc = check_ptr(dY, "dY")) || (rc = check_ptr(X, "X")) || (rc = check_ptr(low, "low")) ||
+      (rc = check_layer(qweight, step16, zero16)) || (rc = check_ptr(dX, "dX")) ||
+      (rc = check_ptr(dA, "dA")) || (rc = check_ptr(dB, "dB")))
+    return rc;
+  awq::W4Args a = w4_args(n_tokens, in_features, out_features, group_size, dtype, 0, qweight, step16,
+                          zero16);
+  a.in0 = dY;
+  a.in1 = X;
+  a.out0 = dX;
+  awq::W4Adapt d = adapt_args(A, B, scale, n_adapters, rank, adapter);
+  d.low = const_cast<float*>(low);
+  d.dA = dA;
+  d.dB = dB;
+  return run_adapted(a, d, true, workspace, workspace_bytes, stream,
+                     "awq_w4a16_adapted_backward launch");
 }
 
 int awq_kv4_append(const awq_kv4_cache* cache, const void* k, const void* v, int dtype,

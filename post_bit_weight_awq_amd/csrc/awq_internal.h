@@ -100,6 +100,20 @@ bool w4_skinny_fits(const W4Args& a);
 hipError_t launch_w4_skinny(W4Op op, const W4Args& a, hipStream_t stream);
 hipError_t launch_w4(W4Op op, const W4Args& a, hipStream_t stream);
 
+// The same with adapters (w4_adapt.hip): a.O and a.K are the packed matrix's,
+// in0 X or dY, in1 X of the backward pass, out0 Y or dX.
+struct W4Adapt {
+  const void *A, *B;
+  const float* scale;
+  const int32_t* ids;
+  int count, rank;
+  float* low;       // kept by the forward pass (or NULL), read by the backward
+  float *dA, *dB;
+};
+constexpr int64_t kMaxAdapters = 32768;  // one grid row each
+size_t w4_adapt_workspace(const W4Args& a, const W4Adapt& d, bool backward);
+hipError_t launch_w4_adapt(const W4Args& a, const W4Adapt& d, bool backward, hipStream_t stream);
+
 hipError_t launch_fold(const void* src, const float* s, int64_t rows, int64_t cols, void* dst,
                        hipStream_t stream);
 

@@ -34,6 +34,7 @@
 // gated 5120 -> 2 x 13824 with [G | U] kept, 1.02-1.11 ms over the cards
 // measured (up to 1.13 PFLOP/s; with the codes converted where they are used 4 %
 // more); 333 tokens, 4096 -> 11008 in groups of 64, 68-70 us.
+#include "w4_adapt.h"
 #include "w4_internal.h"
 
 namespace awq {
@@ -192,11 +193,12 @@ __device__ __forceinline__ void add_lows(floatx4 (&acc)[MT][4], const Lows& l, R
   }
 }
 
-template <int GROUP, bool GATED, int MT, bool SPLIT>
+// AD: Adapters, whose term the part with the first columns adds, or none.
+template <int GROUP, bool GATED, int MT, bool SPLIT, typename AD>
 __global__ void __launch_bounds__(512, 2)
 k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
           const char* __restrict__ prm, Lows lows, float* __restrict__ parts, TileSplit sp,
-          Epilogue ep) {
+          Epilogue ep, AD ad) {
   using L = GemmLds<GROUP, MT, SPLIT>;
   constexpr int BM = (SPLIT ? 16 : 32) * MT;
   constexpr int GPB = 128 / GROUP, JG = 4 / GPB;
@@ -455,6 +457,10 @@ k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
   auto row_of = [&](int i) { return packed_row(64 * wn + i); };
   if constexpr (!SPLIT) {
     if (low) add_lows(acc, lows, row_of, N, O, ng, g0, g1, t0 + wm * MT * 16, lane);
+    if constexpr (AD::on)
+      if (un.s0 == 0)
+        add_adapters<MT>(acc, ad, ep.type, ep.back, [&](int n) { return row_of(16 * n + r16); }, O,
+                         t0 + wm * MT * 16, N, lane);
     leave<GATED, MT>(acc, parts, un, wave, (float*)smem + wave * kEpWave, ep, t0 + wm * MT * 16, ow,
                      lane);
   } else {
@@ -477,6 +483,10 @@ k_w4_gemm(const _Float16* __restrict__ A, int K, const char* __restrict__ qw,
 #pragma unroll
       for (int n = 0; n < 4; ++n) keep[m][n] += other[(m * 4 + n) * 64];
     if (low) add_lows(keep, lows, row_of, N, O, ng, g0, g1, t0 + wm * H * 16, lane);
+    if constexpr (AD::on)
+      if (un.s0 == 0)
+        add_adapters<H>(keep, ad, ep.type, ep.back, [&](int n) { return row_of(16 * n + r16); }, O,
+                        t0 + wm * H * 16, N, lane);
     leave<GATED, H>(keep, parts, un, wave, (float*)smem + wave * kEpWave, ep, t0 + wm * H * 16, ow,
                     lane);
   }
@@ -533,11 +543,11 @@ static GemmPlan gemm_plan(W4Op op, const W4Args& a) {
 size_t w4_gemm_workspace(W4Op op, const W4Args& a) { return gemm_plan(op, a).bytes; }
 
 // The tile is 32 MT tokens high.
-template <int GROUP, bool GATED, int MT>
-static hipError_t launch(const W4Args& a, const GemmPlan& p, hipStream_t stream) {
+template <int GROUP, bool GATED, int MT, typename AD>
+static hipError_t launch(const W4Args& a, const AD& ad, const GemmPlan& p, hipStream_t stream) {
   constexpr bool SPLIT = MT <= 4;
   constexpr int W = SPLIT ? 2 * MT : MT;  // token tiles of a wavefront
-  auto* kernel = &k_w4_gemm<GROUP, GATED, W, SPLIT>;
+  auto* kernel = &k_w4_gemm<GROUP, GATED, W, SPLIT, AD>;
   const int lds = GemmLds<GROUP, W, SPLIT>::kBytes;
   const hipError_t e =
       hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
@@ -551,30 +561,29 @@ static hipError_t launch(const W4Args& a, const GemmPlan& p, hipStream_t stream)
   float* parts = (float*)(ws + p.off_parts);
   hipLaunchKernelGGL(kernel, dim3((unsigned)(p.sp.full + p.sp.left * p.sp.parts)), dim3(512), lds,
                      stream, bf ? (const _Float16*)(ws + p.off_a) : (const _Float16*)a.in0, (int)a.K,
-                     (const char*)a.qweight, ws + p.off_prm, lows, parts, p.sp, ep);
+                     (const char*)a.qweight, ws + p.off_prm, lows, parts, p.sp, ep, ad);
   if (p.sp.parts > 1)
     hipLaunchKernelGGL(k_gemm_join<GATED>, dim3((unsigned)(p.sp.left * 4 * MT)), dim3(64), 0, stream,
                        parts, p.sp, ep, MT);
   return hipGetLastError();
 }
 
-template <int GROUP, bool GATED>
-static hipError_t by_tile(const W4Args& a, const GemmPlan& p, hipStream_t stream) {
-  if (p.mt == 2) return launch<GROUP, GATED, 2>(a, p, stream);
-  if (p.mt == 4) return launch<GROUP, GATED, 4>(a, p, stream);
-  if (p.mt == 6) return launch<GROUP, GATED, 6>(a, p, stream);
-  return launch<GROUP, GATED, 8>(a, p, stream);
+template <int GROUP, bool GATED, typename AD>
+static hipError_t by_tile(const W4Args& a, const AD& ad, const GemmPlan& p, hipStream_t stream) {
+  if (p.mt == 2) return launch<GROUP, GATED, 2>(a, ad, p, stream);
+  if (p.mt == 4) return launch<GROUP, GATED, 4>(a, ad, p, stream);
+  if (p.mt == 6) return launch<GROUP, GATED, 6>(a, ad, p, stream);
+  return launch<GROUP, GATED, 8>(a, ad, p, stream);
 }
 
-template <bool GATED>
-static hipError_t by_group(const W4Args& a, const GemmPlan& p, hipStream_t stream) {
-  if (a.group == 128) return by_tile<128, GATED>(a, p, stream);
-  if (a.group == 64) return by_tile<64, GATED>(a, p, stream);
-  return by_tile<32, GATED>(a, p, stream);
+template <bool GATED, typename AD>
+static hipError_t by_group(const W4Args& a, const AD& ad, const GemmPlan& p, hipStream_t stream) {
+  if (a.group == 128) return by_tile<128, GATED>(a, ad, p, stream);
+  if (a.group == 64) return by_tile<64, GATED>(a, ad, p, stream);
+  return by_tile<32, GATED>(a, ad, p, stream);
 }
 
-hipError_t launch_w4_gemm(W4Op op, const W4Args& a, hipStream_t stream) {
-  const GemmPlan p = gemm_plan(op, a);
+static hipError_t prepare(const W4Args& a, const GemmPlan& p, hipStream_t stream) {
   char* ws = (char*)a.ws;
   Prepare q{};
   q.step16 = (const _Float16*)a.step16;
@@ -590,9 +599,22 @@ hipError_t launch_w4_gemm(W4Op op, const W4Args& a, hipStream_t stream) {
   q.cols = q.ld_out = (int)a.K;
   q.out = ws + p.off_a;
   q.back = (int*)(ws + p.off_back);
-  const hipError_t e = launch_w4_prepare(q, a.type, 1, false, a.N, stream);
+  return launch_w4_prepare(q, a.type, 1, false, a.N, stream);
+}
+
+hipError_t launch_w4_gemm(W4Op op, const W4Args& a, hipStream_t stream) {
+  const GemmPlan p = gemm_plan(op, a);
+  const hipError_t e = prepare(a, p, stream);
   if (e != hipSuccess) return e;
-  return op == kOpGated ? by_group<true>(a, p, stream) : by_group<false>(a, p, stream);
+  return op == kOpGated ? by_group<true>(a, NoAdapters{}, p, stream)
+                        : by_group<false>(a, NoAdapters{}, p, stream);
+}
+
+hipError_t launch_w4_gemm_adapted(const W4Args& a, const Adapters& ad, hipStream_t stream) {
+  const GemmPlan p = gemm_plan(kOpLinear, a);
+  const hipError_t e = prepare(a, p, stream);
+  if (e != hipSuccess) return e;
+  return by_group<false>(a, ad, p, stream);
 }
 
 }  // namespace awq

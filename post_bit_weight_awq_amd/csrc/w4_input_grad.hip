@@ -31,6 +31,7 @@
 // Bound by the issue of MFMAs and conversions: 4096 x 5120 <- 27648 takes
 // 0.95-1.03 ms (1.13-1.22 PFLOP/s over the cards measured) of 1.13-1.18 with its
 // row scaling, 2048 x 4096 <- 12288 203-222 us of which 27 are the scaling.
+#include "w4_adapt.h"
 #include "w4_internal.h"
 
 namespace awq {
@@ -85,11 +86,12 @@ __device__ __forceinline__ void leave(const floatx4 (&acc)[MT][4], float* parts,
   store_dx<T, MT>(acc, back, N, K, t0, col, lane, dX);
 }
 
-template <typename T, int GROUP, int MT, bool SPLIT>
+// AD: Adapters, whose term the part with the first rows adds, or none.
+template <typename T, int GROUP, int MT, bool SPLIT, typename AD>
 __global__ void __launch_bounds__(512, 2)
 k_w4_dx(const _Float16* __restrict__ A, int lda, const int* __restrict__ back, int N, int K, int O,
         const char* __restrict__ qw, const char* __restrict__ prm, const int* __restrict__ big,
-        T* __restrict__ dX, float* __restrict__ parts, TileSplit sp) {
+        T* __restrict__ dX, float* __restrict__ parts, TileSplit sp, AD ad) {
   using L = DxLds<MT, SPLIT>;
   constexpr int BM = (SPLIT ? 16 : 32) * MT;
   constexpr int AL = MT / 2;           // direct loads of dY per wavefront and iteration
@@ -314,7 +316,12 @@ k_w4_dx(const _Float16* __restrict__ A, int lda, const int* __restrict__ back, i
   else
     sum();
   const int col = k0 + 128 * wb + 8 * r16 + 4 * half;
+  auto col_of = [&](int c) { return min(col, K - 4) + c; };
   if constexpr (!SPLIT) {
+    if constexpr (AD::on)
+      if (un.s0 == 0)
+        add_adapters<MT>(acc, ad, __is_same(T, _Float16) ? kF16 : kBF16, back, col_of, K,
+                         t0 + wm * MT * 16, N, lane);
     leave<T, MT>(acc, parts, un, wave, back, N, K, t0 + wm * MT * 16, col, lane, dX);
   } else {
     // each half of the wavefronts hands half of its tokens' sums to the other
@@ -335,6 +342,10 @@ k_w4_dx(const _Float16* __restrict__ A, int lda, const int* __restrict__ back, i
     for (int m = 0; m < H; ++m)
 #pragma unroll
       for (int c = 0; c < 4; ++c) keep[m][c] += other[(m * 4 + c) * 64];
+    if constexpr (AD::on)
+      if (un.s0 == 0)
+        add_adapters<H>(keep, ad, __is_same(T, _Float16) ? kF16 : kBF16, back, col_of, K,
+                        t0 + wm * H * 16, N, lane);
     leave<T, H>(keep, parts, un, wave, back, N, K, t0 + wm * H * 16, col, lane, dX);
   }
 }
@@ -384,11 +395,11 @@ static DxPlan dx_plan(const W4Args& a) {
 size_t w4_input_grad_workspace(const W4Args& a) { return dx_plan(a).bytes; }
 
 // The tile is 32 MT tokens high.
-template <typename T, int GROUP, int MT>
-static hipError_t launch(const W4Args& a, const void* dY, const DxPlan& p, hipStream_t stream) {
+template <typename T, int GROUP, int MT, typename AD>
+static hipError_t launch(const W4Args& a, const AD& ad, const void* dY, const DxPlan& p, hipStream_t stream) {
   constexpr bool SPLIT = MT <= 4;
   constexpr int W = SPLIT ? 2 * MT : MT;  // token tiles of a wavefront
-  auto* kernel = &k_w4_dx<T, GROUP, W, SPLIT>;
+  auto* kernel = &k_w4_dx<T, GROUP, W, SPLIT, AD>;
   const int lds = DxLds<W, SPLIT>::kBytes;
   hipError_t e =
       hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
@@ -399,30 +410,31 @@ static hipError_t launch(const W4Args& a, const void* dY, const DxPlan& p, hipSt
   hipLaunchKernelGGL(kernel, dim3((unsigned)(p.sp.full + p.sp.left * p.sp.parts)), dim3(512), lds,
                      stream, p.copy ? (const _Float16*)(ws + p.off_a) : (const _Float16*)dY, p.lda,
                      back, (int)a.N, (int)a.K, (int)a.O, (const char*)a.qweight, ws + p.off_prm,
-                     (const int*)(ws + p.off_big), (T*)a.out0, parts, p.sp);
+                     (const int*)(ws + p.off_big), (T*)a.out0, parts, p.sp, ad);
   if (p.sp.parts > 1)
     hipLaunchKernelGGL((k_dx_join<T>), dim3((unsigned)(p.sp.left * 4 * MT)), dim3(64), 0, stream,
                        parts, back, (int)a.N, (int)a.K, (T*)a.out0, p.sp, MT);
   return hipGetLastError();
 }
 
-template <typename T, int GROUP>
-static hipError_t by_tokens(const W4Args& a, const void* dY, const DxPlan& p, hipStream_t stream) {
-  if (p.mt == 2) return launch<T, GROUP, 2>(a, dY, p, stream);
-  if (p.mt == 4) return launch<T, GROUP, 4>(a, dY, p, stream);
-  if (p.mt == 6) return launch<T, GROUP, 6>(a, dY, p, stream);
-  return launch<T, GROUP, 8>(a, dY, p, stream);
+template <typename T, int GROUP, typename AD>
+static hipError_t by_tokens(const W4Args& a, const AD& ad, const void* dY, const DxPlan& p, hipStream_t stream) {
+  if (p.mt == 2) return launch<T, GROUP, 2>(a, ad, dY, p, stream);
+  if (p.mt == 4) return launch<T, GROUP, 4>(a, ad, dY, p, stream);
+  if (p.mt == 6) return launch<T, GROUP, 6>(a, ad, dY, p, stream);
+  return launch<T, GROUP, 8>(a, ad, dY, p, stream);
 }
 
-template <typename T>
-static hipError_t by_group(const W4Args& a, const void* dY, const DxPlan& p, hipStream_t stream) {
-  if (a.group == 128) return by_tokens<T, 128>(a, dY, p, stream);
-  if (a.group == 64) return by_tokens<T, 64>(a, dY, p, stream);
-  return by_tokens<T, 32>(a, dY, p, stream);
+template <typename T, typename AD>
+static hipError_t by_group(const W4Args& a, const AD& ad, const void* dY, const DxPlan& p, hipStream_t stream) {
+  if (a.group == 128) return by_tokens<T, 128>(a, ad, dY, p, stream);
+  if (a.group == 64) return by_tokens<T, 64>(a, ad, dY, p, stream);
+  return by_tokens<T, 32>(a, ad, dY, p, stream);
 }
 
 // Of a gated block the preparing launch forms dpre on the way.
-hipError_t launch_w4_input_grad(W4Op op, const W4Args& a, hipStream_t stream) {
+template <typename AD>
+static hipError_t run(W4Op op, const W4Args& a, const AD& ad, hipStream_t stream) {
   const bool gated = op == kOpGatedBackward;
   const DxPlan p = dx_plan(a);
   char* ws = (char*)a.ws;
@@ -445,7 +457,14 @@ hipError_t launch_w4_input_grad(W4Op op, const W4Args& a, hipStream_t stream) {
       launch_w4_prepare(q, a.type, 2, gated, p.copy || gated ? a.N : 0, stream);
   if (e != hipSuccess) return e;
   const void* dY = gated ? a.out1 : a.in0;
-  return a.type == kF16 ? by_group<_Float16>(a, dY, p, stream) : by_group<__bf16>(a, dY, p, stream);
+  return a.type == kF16 ? by_group<_Float16>(a, ad, dY, p, stream)
+                        : by_group<__bf16>(a, ad, dY, p, stream);
+}
+hipError_t launch_w4_input_grad(W4Op op, const W4Args& a, hipStream_t stream) {
+  return run(op, a, NoAdapters{}, stream);
+}
+hipError_t launch_w4_input_grad_adapted(const W4Args& a, const Adapters& ad, hipStream_t stream) {
+  return run(kOpInputGrad, a, ad, stream);
 }
 
 }  // namespace awq

@@ -33,6 +33,7 @@
 //     whole, and is left out.
 #include <type_traits>
 
+#include "w4_adapt.h"
 #include "w4_internal.h"
 
 namespace awq {
@@ -42,23 +43,27 @@ constexpr int kSkinnyLds = 160 * 1024;
 struct SkinnyPlan {
   int lds;       // bytes
   int off_ring;  // of the two stages, behind the (step, zero) pairs
+  int off_low;   // of the adapters' products, behind all
 };
-static SkinnyPlan skinny_plan(int64_t N, int64_t K, int group, int KS) {
+static SkinnyPlan skinny_plan(int64_t N, int64_t K, int group, int KS, int rank = 0) {
   const int WR = 8 / KS, rows = 32 * WR, MT = (int)((N + 15) / 16);
   const int64_t params = ((int64_t)rows * (K / group) * 4 + 1023) & ~1023;
   const int64_t sums = (int64_t)KS * 16 * MT * (rows + 1) * 4;
   const int64_t ring = params + 2 * (KS * (N <= 4 ? 1024 : MT * 4096) + 8 * 2048);
   SkinnyPlan p;
   p.off_ring = (int)params;
-  p.lds = ring > kSkinnyLds ? 0 : (int)(ring > sums ? ring : sums);
+  const int64_t low = ring > sums ? ring : sums;
+  p.off_low = (int)low;
+  p.lds = low + 4 * N * rank > kSkinnyLds ? 0 : (int)(low + 4 * N * rank);
   return p;
 }
 
-template <typename T, int GROUP, bool GATED, int MT, int KS, bool FEW>
+// AD: Adapters, whose term each output adds in fp32, or none.
+template <typename T, int GROUP, bool GATED, int MT, int KS, bool FEW, typename AD>
 __global__ void __launch_bounds__(512, 2)
 k_w4_skinny(const T* __restrict__ X, int M, int K, int O, const char* __restrict__ qw,
             const _Float16* __restrict__ step16, const _Float16* __restrict__ zero16, Epilogue ep,
-            int off_ring) {
+            int off_ring, int off_low, AD ad) {
   constexpr bool BF = !__is_same(T, _Float16);
   constexpr int WR = 8 / KS, R = 32 * WR;  // packed rows per block
   constexpr int GPB = 128 / GROUP;         // groups per block of 128 columns
@@ -116,6 +121,20 @@ k_w4_skinny(const T* __restrict__ X, int M, int K, int O, const char* __restrict
       dma16((const char*)X + 256 * kb, ox[i], l + kg * XB + (FEW ? 0 : (wr + i * WR) * 1024));
   };
   load(0);
+  if constexpr (AD::on) {
+    // scale low of every token, the splits of its sum in order
+    float* const low = (float*)(smem + off_low);
+    const int all = M * ad.rank;
+    for (int e = tid; e < all; e += 512) {
+      const int id = ad.ids[e / ad.rank];
+      float s = 0.0f;
+      if (id >= 0 && id < ad.count) {
+        for (int k = 0; k < ad.splits; ++k) s += ad.low[(size_t)k * all + e];
+        s *= ad.scale[id];
+      }
+      low[e] = s;
+    }
+  }
   uint16_t part = 0;  // of the zeros: bits of what they have behind the point,
   _Float16 top = 0;   // and the largest magnitude
   const int di = 512 / ng, dg = 512 - di * ng;
@@ -275,6 +294,20 @@ k_w4_skinny(const T* __restrict__ X, int M, int K, int O, const char* __restrict
       }
       s = (ep.act == kActSilu ? act_value<kActSilu>(s, nullptr) : act_value<kActGelu>(s, nullptr)) * v;
     }
+    if constexpr (AD::on) {
+      const int id = ad.ids[t];
+      if (id >= 0 && id < ad.count) {
+        const float* low = (const float*)(smem + off_low) + t * ad.rank;
+        const uint4* b = (const uint4*)(ad.mat + ((int64_t)id * O + rb + i) * ad.rank * 2);
+        for (int r = 0; r < ad.rank; r += 8) {
+          const uint4 w = b[r >> 3];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            s = fmaf(low[r + k],
+                     to_f32(__builtin_bit_cast(T, (uint16_t)(word_of(w, k >> 1) >> (16 * (k & 1))))), s);
+        }
+      }
+    }
     if (!GATED && ep.y_type == kF32)
       ((float*)ep.y)[at] = s;
     else
@@ -282,12 +315,15 @@ k_w4_skinny(const T* __restrict__ X, int M, int K, int O, const char* __restrict
   }
 }
 
-template <typename T, int GROUP, bool GATED, int MT, int KS, bool FEW>
-static hipError_t launch(const W4Args& a, hipStream_t stream) {
-  const SkinnyPlan p = skinny_plan(a.N, a.K, a.group, KS);
+inline int rank_of(const NoAdapters&) { return 0; }
+inline int rank_of(const Adapters& ad) { return ad.rank; }
+
+template <typename T, int GROUP, bool GATED, int MT, int KS, bool FEW, typename AD>
+static hipError_t launch(const W4Args& a, const AD& ad, hipStream_t stream) {
+  const SkinnyPlan p = skinny_plan(a.N, a.K, a.group, KS, rank_of(ad));
   const int per = GATED ? 16 * (8 / KS) : 32 * (8 / KS);
   const int64_t outs = GATED ? a.O / 2 : a.O;
-  auto* kernel = &k_w4_skinny<T, GROUP, GATED, MT, KS, FEW>;
+  auto* kernel = &k_w4_skinny<T, GROUP, GATED, MT, KS, FEW, AD>;
   if (p.lds > 65536) {
     const hipError_t e = hipFuncSetAttribute(
         (const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, p.lds);
@@ -296,7 +332,7 @@ static hipError_t launch(const W4Args& a, hipStream_t stream) {
   const Epilogue ep{nullptr, a.out0, a.out1, (int)a.N, (int)a.O, a.y_type, a.type, a.act};
   hipLaunchKernelGGL(kernel, dim3((unsigned)((outs + per - 1) / per)), dim3(512), p.lds, stream,
                      (const T*)a.in0, (int)a.N, (int)a.K, (int)a.O, (const char*)a.qweight,
-                     (const _Float16*)a.step16, (const _Float16*)a.zero16, ep, p.off_ring);
+                     (const _Float16*)a.step16, (const _Float16*)a.zero16, ep, p.off_ring, p.off_low, ad);
   return hipGetLastError();
 }
 
@@ -307,8 +343,8 @@ static hipError_t launch(const W4Args& a, hipStream_t stream) {
 // 5120 -> 15360 22.2 / 13.8 / 14.7, 16 tokens 5120 -> 5120 21.2 / 12.4 / 8.0,
 // gated 5120 -> 2 x 13824 29.2 / 24.5 / 36.0; 32 tokens, the same, 31.8 / 37.6,
 // 48 tokens 5120 -> 15360 32.5 / 22.2, gated 42.8 / 50.4.
-static int skinny_ks(const W4Args& a) {
-  auto fits = [&](int ks) { return skinny_plan(a.N, a.K, a.group, ks).lds > 0; };
+static int skinny_ks(const W4Args& a, int rank = 0) {
+  auto fits = [&](int ks) { return skinny_plan(a.N, a.K, a.group, ks, rank).lds > 0; };
   if (a.N > 64) return 0;
   int ks = 8;
   if (a.N > 16)
@@ -330,31 +366,31 @@ static int skinny_ks(const W4Args& a) {
 // The groups that a token count can take: up to four tokens take eight (which
 // fit wherever fewer do), up to 16 eight or four; LDS holds no more than four
 // with 17 to 48 tokens and two with more.
-template <typename T, int GROUP, bool GATED, int MT, bool FEW>
-static hipError_t by_ks(const W4Args& a, hipStream_t stream) {
-  const int ks = skinny_ks(a);
+template <typename T, int GROUP, bool GATED, int MT, bool FEW, typename AD>
+static hipError_t by_ks(const W4Args& a, const AD& ad, hipStream_t stream) {
+  const int ks = skinny_ks(a, rank_of(ad));
   if constexpr (MT == 1)
-    if (ks == 8) return launch<T, GROUP, GATED, MT, 8, FEW>(a, stream);
+    if (ks == 8) return launch<T, GROUP, GATED, MT, 8, FEW>(a, ad, stream);
   if constexpr (!FEW && MT <= 3)
-    if (ks == 4) return launch<T, GROUP, GATED, MT, 4, FEW>(a, stream);
+    if (ks == 4) return launch<T, GROUP, GATED, MT, 4, FEW>(a, ad, stream);
   if constexpr (MT >= 2)
-    if (ks == 2) return launch<T, GROUP, GATED, MT, 2, FEW>(a, stream);
+    if (ks == 2) return launch<T, GROUP, GATED, MT, 2, FEW>(a, ad, stream);
   return hipErrorInvalidValue;
 }
 
-template <typename T, int GROUP, bool GATED>
-static hipError_t by_tokens(const W4Args& a, hipStream_t stream) {
-  if (a.N <= 4) return by_ks<T, GROUP, GATED, 1, true>(a, stream);
-  if (a.N <= 16) return by_ks<T, GROUP, GATED, 1, false>(a, stream);
-  if (a.N <= 32) return by_ks<T, GROUP, GATED, 2, false>(a, stream);
-  if (a.N <= 48) return by_ks<T, GROUP, GATED, 3, false>(a, stream);
-  return by_ks<T, GROUP, GATED, 4, false>(a, stream);
+template <typename T, int GROUP, bool GATED, typename AD>
+static hipError_t by_tokens(const W4Args& a, const AD& ad, hipStream_t stream) {
+  if (a.N <= 4) return by_ks<T, GROUP, GATED, 1, true>(a, ad, stream);
+  if (a.N <= 16) return by_ks<T, GROUP, GATED, 1, false>(a, ad, stream);
+  if (a.N <= 32) return by_ks<T, GROUP, GATED, 2, false>(a, ad, stream);
+  if (a.N <= 48) return by_ks<T, GROUP, GATED, 3, false>(a, ad, stream);
+  return by_ks<T, GROUP, GATED, 4, false>(a, ad, stream);
 }
 
 template <typename T, int GROUP>
 static hipError_t by_op(W4Op op, const W4Args& a, hipStream_t stream) {
-  return op == kOpGated ? by_tokens<T, GROUP, true>(a, stream)
-                        : by_tokens<T, GROUP, false>(a, stream);
+  return op == kOpGated ? by_tokens<T, GROUP, true>(a, NoAdapters{}, stream)
+                        : by_tokens<T, GROUP, false>(a, NoAdapters{}, stream);
 }
 
 bool w4_skinny_fits(const W4Args& a) { return skinny_ks(a) != 0; }
@@ -368,6 +404,18 @@ hipError_t launch_w4_skinny(W4Op op, const W4Args& a, hipStream_t stream) {
   if (a.group == 128) return by_op<__bf16, 128>(op, a, stream);
   if (a.group == 64) return by_op<__bf16, 64>(op, a, stream);
   return by_op<__bf16, 32>(op, a, stream);
+}
+
+bool w4_skinny_fits_adapted(const W4Args& a, int rank) { return skinny_ks(a, rank) != 0; }
+
+template <typename T>
+static hipError_t adapted(const W4Args& a, const Adapters& ad, hipStream_t stream) {
+  if (a.group == 128) return by_tokens<T, 128, false>(a, ad, stream);
+  if (a.group == 64) return by_tokens<T, 64, false>(a, ad, stream);
+  return by_tokens<T, 32, false>(a, ad, stream);
+}
+hipError_t launch_w4_skinny_adapted(const W4Args& a, const Adapters& ad, hipStream_t stream) {
+  return a.type == kF16 ? adapted<_Float16>(a, ad, stream) : adapted<__bf16>(a, ad, stream);
 }
 
 }  // namespace awq
