@@ -4,13 +4,12 @@
 // offset of their groups, never rounded.
 //
 // One pass with a running maximum m and sum l (binary32, powers of 2).  A
-// wavefront takes 32 keys at a time for 16 MT rows; a row is one token and
-// one of the heads that share a kv head.
-//   * Scores: MFMA 16x16x32 of codes (keys by columns) with Q.  Four operations
-//     shift nibbles to the top of the mantissa below the exponent of 16, so the
-//     operand is 16 + code, exactly; it is step S + (offset - 16 step) sum Q
-//     per group, S the group's product, in binary32.  Q's columns are put in
-//     the nibbles' order once.
+// wavefront takes 32 keys at a time for 16 rows; a row is one token and one of
+// the heads that share a kv head.
+//   * Scores: MFMA 16x16x32 of codes (keys by columns) with Q.  Two operations
+//     per pair put a nibble at the top of the mantissa below the exponent of 16,
+//     so the operand is 16 + code, exactly; the sums begin at -16 sum Q.  Steps
+//     and offsets enter behind them, per group, in binary32.
 //   * A lane then holds keys 4 q .. 4 q + 3 of both tiles of 16 for one row:
 //     as the second operand of O^T = V^T P^T these are its eight of 32 keys, if
 //     V's codes are read for the same keys.  So P never leaves its lane.  Eight
@@ -19,13 +18,21 @@
 //   * P step, the operand, is held as two bf16 parts (16 bits): in one, or in
 //     fp16, it would add as much error as the output's rounding or leave the
 //     type's range.  With at most 8 rows the parts lie in lanes r and r + 8 of
-//     one MFMA.  The offsets' part, sum P (offset - 16 step), is summed per
-//     lane.
+//     one MFMA.  -16 of V's codes is taken back from the same rounded parts (one
+//     more MFMA), so a part's error meets the code and not 16 + code.  The
+//     offsets' part, sum P offset, is summed per lane.
 // Single tokens (k_kv4_decode): a block of four wavefronts takes 16 rows, each
-// wavefront every fourth 32 keys, and joins them through LDS; a long axis is
-// split over blocks and k_kv4_join joins the splits in order.  Runs of tokens
-// (k_kv4_chunk): a block takes 64 MT rows, each wavefront 16 MT of them and
-// all keys.
+// wavefront every fourth 32 keys through two stages of LDS of its own, filled by
+// direct loads; they are joined through LDS.  A long axis is split over blocks
+// and k_kv4_join joins the splits in order.  Bound by the stream of codes on long
+// caches (64 ragged sequences of up to 4096 keys, 40 heads of 128: 183 us, 4.4
+// TB/s; with the tiles in registers, at half the wavefronts in flight, 200), by
+// the way to the first keys and the join on short ones (one sequence of 777: 9.5
+// us).  Runs of tokens (k_kv4_chunk): a block of eight wavefronts takes 128 rows;
+// they prepare a tile's operands in LDS together, each an eighth.  Bound by VALU
+// issue and the barrier of each tile: 4 x 256 to 512 tokens behind up to 4096
+// keys, 32 heads on 8: 202 us, 304 TFLOP/s (each wavefront by itself, for two row
+// tiles: 268; four wavefronts of two row tiles: 204; products a tile ahead: 255).
 #include "kv4_device.h"
 #include "w4_internal.h"
 
@@ -39,8 +46,11 @@ struct AttnArgs {
   int64_t q_token, q_head;
   int tokens, seqs, per_seq;
   const int32_t *starts, *table, *lens;
-  float scale;  // times log2(e)
-  int splits, tiles;  // tiles: of rows, over all sequences
+  float scale, slack;  // scale: |scale| log2(e); slack: 8 / scale
+  int flip;            // the scale is negative: Q changes sign
+  int splits, per;    // blocks of a unit, the keys of each
+  int tiles;          // of rows, over all sequences
+  int rows;           // of a tile that k_kv4_join looks at
   float* parts;  // [unit][split][16][D + 2]
 };
 
@@ -87,15 +97,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, r);
 }
 
-// What a wavefront keeps of 16 MT rows: lane l has row l % 16 of each tile.
-template <int D, int G, int MT>
+// What a wavefront keeps of 16 rows: lane l has row l % 16.
+template <int D, int G>
 struct Rows {
-  static constexpr int J = D / 32, NG = D / G, JG = G / 32, N = D / 16;
-  uint4 q[MT][J];
-  float qs[MT][NG];  // sum of Q over a group
-  float m[MT], l[MT], off[MT][NG];
-  floatx4 o[MT][N];  // O^T: tile n, columns 4 (l / 16) + r, see column()
-  int lim[MT];       // keys that the row sees
+  static constexpr int J = D / 32, NG = D / G, JG = G / 32, N = D / 16, TG = G / 16;
+  uint4 q[J];
+  float qs[NG];  // sum of Q over a group
+  float m, l, off[NG];
+  floatx4 o[N];   // O^T: tile n, columns 4 (l / 16) + r, see column()
+  floatx4 c[NG];  // -16 sum of the operand P step
+  int lim;        // keys that the row sees
 };
 
 // Column of register r of tile n in lane group q: the word 4 q + r of a group
@@ -106,301 +117,420 @@ __device__ __forceinline__ int column(int n, int i) {
   return (n / TG) * G + 8 * (i % WG) + TG * (i / WG) + n % TG;
 }
 
-template <typename T, int D, int G, int MT>
-__device__ __forceinline__ void load_rows(const AttnArgs& a, const Unit& u, int row0, int lane,
-                                          Rows<D, G, MT>& w, int* rlim) {
-  using R = Rows<D, G, MT>;
+// Returns the keys that all 16 rows see.
+template <typename T, int D, int G>
+__device__ __forceinline__ int load_rows(const AttnArgs& a, const Unit& u, int row0, int lane, Rows<D, G>& w) {
+  using R = Rows<D, G>;
+  const uint32_t sign = a.flip ? 0x80008000u : 0u;
   const int r16 = lane & 15, q4 = lane >> 4;
-  int low = 0x7fffffff;
+  const int row = min(row0 + r16, u.rows - 1);
+  const int t = row / a.per_kv;
+  const T* p = (const T*)a.q + (int64_t)(u.first + t) * a.q_token +
+               (int64_t)(u.head * a.per_kv + row - t * a.per_kv) * a.q_head;
+  w.lim = min(max(u.len - u.run + t + 1, 0), u.len);
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int row = min(row0 + 16 * m + r16, u.rows - 1);
-    const int t = row / a.per_kv;
-    const T* p = (const T*)a.q + (int64_t)(u.first + t) * a.q_token +
-                 (int64_t)(u.head * a.per_kv + row - t * a.per_kv) * a.q_head;
-    w.lim[m] = min(max(u.len - u.run + t + 1, 0), u.len);
-    low = min(low, w.lim[m]);
-#pragma unroll
-    for (int j = 0; j < R::J; ++j) {
-      const uint4 v = *(const uint4*)(p + 32 * j + 8 * q4);
-      // columns 0 4, 1 5, 2 6, 3 7, as the words' nibbles come
-      w.q[m][j] = make_uint4(__builtin_amdgcn_perm(v.z, v.x, 0x05040100u),
-                             __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
-                             __builtin_amdgcn_perm(v.w, v.y, 0x05040100u),
-                             __builtin_amdgcn_perm(v.w, v.y, 0x07060302u));
-    }
-#pragma unroll
-    for (int g = 0; g < R::NG; ++g) {
-      float s = 0.0f;
-#pragma unroll
-      for (int j = 0; j < R::JG; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          s += to_f32(__builtin_bit_cast(
-              T, (uint16_t)(word_of(w.q[m][g * R::JG + j], i >> 1) >> (16 * (i & 1)))));
-      s += __shfl_xor(s, 16);
-      s += __shfl_xor(s, 32);
-      w.qs[m][g] = s;
-      w.off[m][g] = 0.0f;
-    }
-    w.m[m] = -INFINITY;
-    w.l[m] = 0.0f;
-#pragma unroll
-    for (int n = 0; n < R::N; ++n) w.o[m][n] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int j = 0; j < R::J; ++j) {
+    uint4 v = *(const uint4*)(p + 32 * j + 8 * q4);
+    v.x ^= sign, v.y ^= sign, v.z ^= sign, v.w ^= sign;
+    // columns 0 4, 1 5, 2 6, 3 7, as the words' nibbles come
+    w.q[j] = make_uint4(__builtin_amdgcn_perm(v.z, v.x, 0x05040100u),
+                        __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
+                        __builtin_amdgcn_perm(v.w, v.y, 0x05040100u),
+                        __builtin_amdgcn_perm(v.w, v.y, 0x07060302u));
   }
+#pragma unroll
+  for (int g = 0; g < R::NG; ++g) {
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < R::JG; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        s += to_f32(
+            __builtin_bit_cast(T, (uint16_t)(word_of(w.q[g * R::JG + j], i >> 1) >> (16 * (i & 1)))));
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    w.qs[g] = s;
+    w.off[g] = 0.0f;
+    w.c[g] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  w.m = -INFINITY;
+  w.l = 0.0f;
+#pragma unroll
+  for (int n = 0; n < R::N; ++n) w.o[n] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+  int low = w.lim;
 #pragma unroll
   for (int s = 1; s < 16; s *= 2) low = min(low, __shfl_xor(low, s));
-  *rlim = __builtin_amdgcn_readfirstlane(low);
+  return __builtin_amdgcn_readfirstlane(low);
 }
 
-// Codes and parameters of 32 keys as a lane takes them.
+// First of the 16 keys from `key` on, which lie in one page.
+__device__ __forceinline__ int64_t key_token(const Kv4& c, int page, int head, int key) {
+  return kv4_token(c, max(page, 0), head, key & ((1 << c.shift) - 1));
+}
+// An address in scalar registers: lanes add 32 bits.
+__device__ __forceinline__ const char* uniform(const void* p) {
+  const uint64_t v = (uint64_t)p;
+  return (const char*)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 |
+                       (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
+}
+// Codes and parameters of 32 keys in a wavefront's own LDS, moved there by
+// direct loads: they are in flight for two tiles' time and cost no registers.
 template <int D, int G>
-struct Tile {
-  static constexpr int J = D / 32, NG = D / G, WG = G / 8;
-  uint32_t k[2][J];
-  uint4 v[2][NG];
-  uint32_t kp[2][4 * NG], vp[2][4 * NG];  // keys 4 q .., [key][group]
+struct Stage {
+  static constexpr int NG = D / G, kCodes = 32 * D / 2, kParams = 32 * NG * 4;
+  static constexpr int kK = 0, kV = kCodes, kKp = 2 * kCodes, kVp = kKp + kParams;
+  static constexpr int kBytes = kVp + kParams;
+  static constexpr int kLoads = (D == 128 ? 4 : 2) + NG;
 };
+// Direct loads from each lane's own address.
+__device__ __forceinline__ void dma16_from(const char* p, uint32_t l) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(p), "{m0}"(l) : "memory");
+}
+__device__ __forceinline__ void dma4_from(const char* p, uint32_t l) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" : : "v"(p), "{m0}"(l) : "memory");
+}
 template <int D, int G>
-__device__ __forceinline__ void load_tile(const Kv4& c, const int (&page)[2], int head, int key,
-                                          int lane, Tile<D, G>& t) {
-  using X = Tile<D, G>;
-  const int r16 = lane & 15, q4 = lane >> 4;
+__device__ __forceinline__ void load_stage(const Kv4& c, const int (&page)[2], int head, int key, uint32_t lane,
+                                           uint32_t lds) {
+  using S = Stage<D, G>;
+  const char *k[2], *v[2], *kp[2], *vp[2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const int i = (key + 16 * u) & ((1 << c.shift) - 1);
-    const int64_t token = kv4_token(c, max(page[u], 0), head, i);  // a multiple of 16
-    const uint32_t* pk = c.k_codes + token * (D / 8) + r16 * (D / 8) + q4 * X::J;
-    if constexpr (X::J == 4) {
-      const uint4 w = *(const uint4*)pk;
-      t.k[u][0] = w.x, t.k[u][1] = w.y, t.k[u][2] = w.z, t.k[u][3] = w.w;
-    } else {
-      const uint2 w = *(const uint2*)pk;
-      t.k[u][0] = w.x, t.k[u][1] = w.y;
-    }
-#pragma unroll
-    for (int g = 0; g < X::NG; ++g)
-      t.v[u][g] = *(const uint4*)(c.v_codes + token * (D / 8) + 16 * (g * X::WG + r16 % X::WG) + 4 * q4);
-    const uint4* pp = (const uint4*)(c.k_params + (token + 4 * q4) * X::NG);
-    const uint4* pv = (const uint4*)(c.v_params + (token + 4 * q4) * X::NG);
-#pragma unroll
-    for (int g = 0; g < X::NG; ++g) {
-      const uint4 x = pp[g], y = pv[g];
-      t.kp[u][4 * g] = x.x, t.kp[u][4 * g + 1] = x.y, t.kp[u][4 * g + 2] = x.z, t.kp[u][4 * g + 3] = x.w;
-      t.vp[u][4 * g] = y.x, t.vp[u][4 * g + 1] = y.y, t.vp[u][4 * g + 2] = y.z, t.vp[u][4 * g + 3] = y.w;
-    }
+    const int64_t token = key_token(c, page[u], head, key + 16 * u);
+    k[u] = uniform(c.k_codes + token * (D / 8));
+    v[u] = uniform(c.v_codes + token * (D / 8));
+    kp[u] = uniform(c.k_params + token * S::NG);
+    vp[u] = uniform(c.v_params + token * S::NG);
   }
-}
-
-// Eight nibbles of a word as 16 + code: pairs 0 4, 1 5, 2 6, 3 7.
-template <typename T>
-__device__ __forceinline__ uint4 codes16(uint32_t w) {
-  if constexpr (__is_same(T, _Float16)) {
-    constexpr uint32_t M = 0x03C003C0u, E = 0x4C004C00u;
-    return make_uint4(((w << 6) & M) | E, ((w << 2) & M) | E, ((w >> 2) & M) | E, ((w >> 6) & M) | E);
+  if constexpr (D == 128) {
+    // lane l fetches what it will read: 16 bytes l % 16, l / 16 of the 16 x 64
+    const uint32_t at = (lane & 15) * 64 + (lane >> 4) * 16;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      dma16(k[u], at, lds + S::kK + 1024 * u);
+      dma16(v[u], at, lds + S::kV + 1024 * u);
+    }
   } else {
-    constexpr uint32_t M = 0x00780078u, E = 0x41804180u;
-    return make_uint4(((w << 3) & M) | E, ((w >> 1) & M) | E, ((w >> 5) & M) | E, ((w >> 9) & M) | E);
+    const uint32_t at = (lane & 31) * 16;  // twice 512 bytes as they lie
+    dma16_from((lane & 32 ? k[1] : k[0]) + at, lds + S::kK);
+    dma16_from((lane & 32 ? v[1] : v[0]) + at, lds + S::kV);
+  }
+  if constexpr (S::NG == 1) {
+    const char* x = lane & 32 ? (lane & 16 ? vp[1] : vp[0]) : lane & 16 ? kp[1] : kp[0];
+    dma4_from(x + 4 * (lane & 15), lds + S::kKp);
+  } else if constexpr (S::NG == 2) {
+    dma4_from((lane & 32 ? kp[1] : kp[0]) + 4 * (lane & 31), lds + S::kKp);
+    dma4_from((lane & 32 ? vp[1] : vp[0]) + 4 * (lane & 31), lds + S::kVp);
+  } else {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      dma4(kp[u], 4 * lane, lds + S::kKp + 256 * u);
+      dma4(vp[u], 4 * lane, lds + S::kVp + 256 * u);
+    }
   }
 }
+// Parameters of keys 4 q .. 4 q + 3 of both 16: [key][group].
+template <int NG>
+__device__ __forceinline__ void read_params(const char* base, uint32_t q4, uint32_t (&p)[2][4 * NG]) {
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const uint4 y = *(const uint4*)(base + 64 * NG * u + 16 * NG * q4 + 16 * g);
+      p[u][4 * g] = y.x, p[u][4 * g + 1] = y.y, p[u][4 * g + 2] = y.z, p[u][4 * g + 3] = y.w;
+    }
+}
 
-// 32 keys for all rows.  MASK: some rows do not see all of them.  PAIR: the two
-// parts of P in lanes r and r + 8 (rows r, twice).
-template <typename T, int D, int G, int MT, bool PAIR, bool MASK>
-__device__ __forceinline__ void take(Rows<D, G, MT>& w, const Tile<D, G>& t, const int (&page)[2],
-                                     int key, float scale, int lane) {
-  using R = Rows<D, G, MT>;
-  const int q4 = lane >> 4, r16 = lane & 15;
-  float s[MT][2][4];
-  uint32_t seen[MT];
+// The mask of a nibble below the exponent and the exponent of 16, for T's
+// pairs, in a scalar and a vector register whose values the compiler does not
+// see: "and, or" is then one operation (it takes no constants, and one scalar).
+template <typename T>
+struct Sixteen {
+  uint32_t mask, exponent;
+  __device__ __forceinline__ Sixteen() {
+    if constexpr (__is_same(T, _Float16)) {
+      asm("s_mov_b32 %0, 0x03c003c0" : "=s"(mask));
+      asm("v_mov_b32 %0, 0x4c004c00" : "=v"(exponent));
+    } else {
+      asm("s_mov_b32 %0, 0x00780078" : "=s"(mask));
+      asm("v_mov_b32 %0, 0x41804180" : "=v"(exponent));
+    }
+  }
+  // Nibble n (0 to 3) of both halves of w as 16 + code.
+  __device__ __forceinline__ uint32_t pair(uint32_t w, int n) const {
+    constexpr int up = __is_same(T, _Float16) ? 6 : 3;
+    const int by = up - 4 * n;
+    return ((by >= 0 ? w << by : w >> -by) & mask) | exponent;
+  }
+  // Eight nibbles: pairs 0 4, 1 5, 2 6, 3 7.
+  __device__ __forceinline__ uint4 word(uint32_t w) const {
+    return make_uint4(pair(w, 0), pair(w, 1), pair(w, 2), pair(w, 3));
+  }
+};
+
+// Scores of 32 keys, in units of the scale, in two steps: the groups' products,
+// whose sums begin at -16 sum Q, which takes the codes' 16 back, and what steps
+// and offsets make of them.  kf(u, j): columns 32 j .. of keys 16 u ..
+template <typename T, int D, int G, typename KF>
+__device__ __forceinline__ void products(const Rows<D, G>& w, KF kf, floatx4 (&acc)[2][D / G]) {
+  using R = Rows<D, G>;
 #pragma unroll
   for (int u = 0; u < 2; ++u)
 #pragma unroll
     for (int g = 0; g < R::NG; ++g) {
-      floatx4 acc[MT];
+      const float z = -16.0f * w.qs[g];
+      acc[u][g] = floatx4{z, z, z, z};
 #pragma unroll
-      for (int m = 0; m < MT; ++m) acc[m] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int j = 0; j < R::JG; ++j) {
-        const uint4 kc = codes16<T>(t.k[u][g * R::JG + j]);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) acc[m] = mfma16<T>(kc, w.q[m][g * R::JG + j], acc[m]);
-      }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const uint32_t p = t.kp[u][r * R::NG + g];
-        const float step = f16_lo(p) * scale, off = fmaf(f16_hi(p), scale, -16.0f * step);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const float x = off * w.qs[m][g];
-          s[m][u][r] = g == 0 ? fmaf(step, acc[m][r], x) : fmaf(step, acc[m][r], x + s[m][u][r]);
-        }
-      }
+      for (int j = 0; j < R::JG; ++j)
+        acc[u][g] = mfma16<T>(kf(u, g * R::JG + j), w.q[g * R::JG + j], acc[u][g]);
     }
-  uint4 hi[MT], lo[MT];  // P step of the group at hand
+}
+template <int D, int G>
+__device__ __forceinline__ void scores(const Rows<D, G>& w, const uint32_t (&p)[2][4 * (D / G)],
+                                       const floatx4 (&acc)[2][D / G], float (&s)[8]) {
+  constexpr int NG = D / G;
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    float top = -INFINITY;
-    seen[m] = 0;
+  for (int u = 0; u < 2; ++u)
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int g = 0; g < NG; ++g)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        if (MASK) {
-          const bool v = page[u] >= 0 && key + 16 * u + 4 * q4 + r < w.lim[m];
-          seen[m] |= (uint32_t)v << (4 * u + r);
-          s[m][u][r] = v ? s[m][u][r] : -INFINITY;
-        }
-        top = fmaxf(top, s[m][u][r]);
+        const uint32_t x = p[u][r * NG + g];
+        float& y = s[4 * u + r];
+        y = fmaf(f16_hi(x), w.qs[g], g == 0 ? 0.0f : y);  // one operation of mixed types
+        y = fmaf(f16_lo(x), acc[u][g][r], y);
       }
+}
+
+// Whether a lane's row sees its key i of the 32 from `key` on.
+__device__ __forceinline__ bool sees(int lim, const int (&page)[2], int key, int q4, int i) {
+  return page[i >> 2] >= 0 && key + 16 * (i >> 2) + 4 * q4 + (i & 3) < lim;
+}
+// The scores of keys that are not seen become -inf, their values' parameters 0,
+// whatever lies there.
+template <int N>
+__device__ __forceinline__ void hide(int lim, const int (&page)[2], int key, int q4, float (&s)[8],
+                                     uint32_t (&p)[2][N]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const bool v = sees(lim, page, key, q4, i);
+    s[i] = v ? s[i] : -INFINITY;
+#pragma unroll
+    for (int g = 0; g < N / 4; ++g) {
+      uint32_t& x = p[i >> 2][(i & 3) * (N / 4) + g];
+      x = v ? x : 0u;
+    }
+  }
+}
+
+// Scores to weights.  The maximum follows only when a score passes it by more
+// than 2^8 in the weights (which binary32 and bf16 hold), so most tiles need no
+// exchange between the lane groups.
+template <int D, int G>
+__device__ __forceinline__ void weigh(Rows<D, G>& w, float scale, float slack, float (&s)[8]) {
+  using R = Rows<D, G>;
+  float top = fmaxf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])), fmaxf(fmaxf(s[4], s[5]), fmaxf(s[6], s[7])));
+  if (__any(top > w.m + slack)) {
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
-    if (__any(top > w.m[m])) {
-      const float now = fmaxf(w.m[m], top);
-      const float a = w.m[m] == now ? 1.0f : __builtin_amdgcn_exp2f(w.m[m] - now);
-      w.m[m] = now;
-      w.l[m] *= a;
+    const float now = fmaxf(w.m, top);
+    const float a = w.m == now         ? 1.0f
+                    : w.m == -INFINITY ? 0.0f
+                                       : __builtin_amdgcn_exp2f((w.m - now) * scale);
+    w.m = now;
+    w.l *= a;
 #pragma unroll
-      for (int g = 0; g < R::NG; ++g) w.off[m][g] *= a;
+    for (int g = 0; g < R::NG; ++g) {
+      w.off[g] *= a;
 #pragma unroll
-      for (int n = 0; n < R::N; ++n)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) w.o[m][n][r] *= a;
+      for (int r = 0; r < 4; ++r) w.c[g][r] *= a;
     }
-    const float base = MASK && w.m[m] == -INFINITY ? 0.0f : w.m[m];
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int n = 0; n < R::N; ++n)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        s[m][u][r] = __builtin_amdgcn_exp2f(s[m][u][r] - base);
-        w.l[m] += s[m][u][r];
-      }
+      for (int r = 0; r < 4; ++r) w.o[n][r] *= a;
   }
+  const float base = w.m == -INFINITY ? 0.0f : -w.m * scale;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], scale, base));
+    w.l += s[i];
+  }
+}
+
+// P step of a group as two bf16 parts; PAIR: lanes 8 to 15 take the second.
+struct Parts {
+  uint4 hi, lo;
+};
+template <int NG, bool PAIR>
+__device__ __forceinline__ Parts parts_of(const uint32_t (&p)[2][4 * NG], int g, const float (&s)[8], float& off,
+                                          int r16) {
+  float ps[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t x = p[i >> 2][(i & 3) * NG + g];
+    ps[i] = fmaf(s[i], f16_lo(x), 0.0f);
+    off = fmaf(s[i], f16_hi(x), off);
+  }
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[i] = pack_bf16(ps[2 * i], ps[2 * i + 1]);
+    l[i] = pack_bf16(ps[2 * i] - __uint_as_float(h[i] << 16),
+                     ps[2 * i + 1] - __uint_as_float(h[i] & 0xffff0000u));
+    if (PAIR) h[i] = r16 & 8 ? l[i] : h[i];
+  }
+  return {make_uint4(h[0], h[1], h[2], h[3]), make_uint4(l[0], l[1], l[2], l[3])};
+}
+
+// Adds the values of 32 keys, a group of columns after another.  vf.group(g),
+// then vf(n): tile n of the group's columns.
+template <int D, int G, bool PAIR, typename VF>
+__device__ __forceinline__ void gather(Rows<D, G>& w, const uint32_t (&p)[2][4 * (D / G)], const float (&s)[8],
+                                       VF& vf, int r16) {
+  using R = Rows<D, G>;
+  const uint4 ones = make_uint4(0xc180c180u, 0xc180c180u, 0xc180c180u, 0xc180c180u);  // -16
 #pragma unroll
   for (int g = 0; g < R::NG; ++g) {
+    vf.group(g);
+    const Parts x = parts_of<R::NG, PAIR>(p, g, s, w.off[g], r16);
+    w.c[g] = mfma16<__bf16>(ones, x.hi, w.c[g]);
+    if (!PAIR) w.c[g] = mfma16<__bf16>(ones, x.lo, w.c[g]);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      float ps[8];
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint32_t p = t.vp[u][r * R::NG + g];
-          const float step = f16_lo(p), off = fmaf(step, -16.0f, f16_hi(p));
-          float a = s[m][u][r] * step, b = s[m][u][r] * off;
-          if (MASK && !((seen[m] >> (4 * u + r)) & 1)) a = b = 0.0f;  // whatever lies there
-          ps[4 * u + r] = a;
-          w.off[m][g] += b;
-        }
-      uint32_t h[4], l[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        h[i] = pack_bf16(ps[2 * i], ps[2 * i + 1]);
-        l[i] = pack_bf16(ps[2 * i] - __uint_as_float(h[i] << 16),
-                         ps[2 * i + 1] - __uint_as_float(h[i] & 0xffff0000u));
-        if (PAIR) h[i] = r16 & 8 ? l[i] : h[i];
-      }
-      hi[m] = make_uint4(h[0], h[1], h[2], h[3]);
-      lo[m] = make_uint4(l[0], l[1], l[2], l[3]);
+    for (int n = 0; n < R::TG; ++n) {
+      const uint4 b = vf(n);
+      floatx4& o = w.o[g * R::TG + n];
+      o = mfma16<__bf16>(b, x.hi, o);
+      if (!PAIR) o = mfma16<__bf16>(b, x.lo, o);
+      if (VF::kTight && (n & 1)) __builtin_amdgcn_sched_barrier(0);  // few codes wait at a time
     }
-    // V's codes of the group: key pairs of the lane's words
-    constexpr uint32_t M = 0x00780078u, E = 0x41804180u;
-    constexpr int TG = G / 16;
-    uint32_t c[TG][4];
+  }
+}
+
+// A lane's words of V (see column()) from a stage: eight keys' words, paired,
+// and of these the halves or bytes that hold the lane's columns.
+template <int D, int G>
+struct ValueWords {
+  static constexpr int WG = G / 8, HG = G == 128 ? 2 : 1;
+  static constexpr bool kTight = true;
+  const char* base;
+  Sixteen<__bf16> v16;
+  int lane;
+  uint32_t h[HG][4];
+  __device__ __forceinline__ void group(int g) {
+    const uint32_t r16 = lane & 15, q4 = lane >> 4, word = g * WG + r16 % WG;
+    uint4 x[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      x[u] = D == 128 ? *(const uint4*)(base + 1024 * u + 16 * (word + 16 * q4))
+                      : *(const uint4*)(base + 512 * u + 64 * word + 16 * q4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint4& x = t.v[i >> 1][g];
-      const uint32_t a = i & 1 ? x.z : x.x, b = i & 1 ? x.w : x.y;
+      const uint32_t a = i & 1 ? x[i >> 1].z : x[i >> 1].x, b = i & 1 ? x[i >> 1].w : x[i >> 1].y;
       if constexpr (G == 128) {
-        const uint32_t p0 = __builtin_amdgcn_perm(b, a, 0x05040100u);
-        const uint32_t p1 = __builtin_amdgcn_perm(b, a, 0x07060302u);
-        c[0][i] = ((p0 << 3) & M) | E;
-        c[1][i] = ((p0 >> 1) & M) | E;
-        c[2][i] = ((p0 >> 5) & M) | E;
-        c[3][i] = ((p0 >> 9) & M) | E;
-        c[4][i] = ((p1 << 3) & M) | E;
-        c[5][i] = ((p1 >> 1) & M) | E;
-        c[6][i] = ((p1 >> 5) & M) | E;
-        c[7][i] = ((p1 >> 9) & M) | E;
-      } else if constexpr (G == 64) {
-        const uint32_t p0 = __builtin_amdgcn_perm(b, a, r16 & 8 ? 0x07060302u : 0x05040100u);
-        c[0][i] = ((p0 << 3) & M) | E;
-        c[1][i] = ((p0 >> 1) & M) | E;
-        c[2][i] = ((p0 >> 5) & M) | E;
-        c[3][i] = ((p0 >> 9) & M) | E;
+        h[0][i] = __builtin_amdgcn_perm(b, a, 0x05040100u);
+        h[1][i] = __builtin_amdgcn_perm(b, a, 0x07060302u);
       } else {
-        const uint32_t p0 = __builtin_amdgcn_perm(b, a, 0x0c040c00u + (uint32_t)(r16 >> 2) * 0x00010001u);
-        c[0][i] = ((p0 << 3) & M) | E;
-        c[1][i] = ((p0 >> 1) & M) | E;
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < TG; ++n) {
-      const uint4 b = make_uint4(c[n][0], c[n][1], c[n][2], c[n][3]);
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        floatx4& o = w.o[m][g * TG + n];
-        o = mfma16<__bf16>(b, hi[m], o);
-        if (!PAIR) o = mfma16<__bf16>(b, lo[m], o);
+        h[0][i] = __builtin_amdgcn_perm(
+            b, a, G == 64 ? (r16 & 8 ? 0x07060302u : 0x05040100u) : 0x0c040c00u + (r16 >> 2) * 0x00010001u);
       }
     }
   }
-}
-
-// The pages of keys key .. key + 31; -1 where there is none or a bad one.
-__device__ __forceinline__ void pages_of(const AttnArgs& a, const int32_t* table, int key, int len,
-                                         int (&page)[2]) {
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int k = key + 16 * u;
-    int p = k < len ? table[k >> a.c.shift] : -1;
-    if (p >= a.c.pages) p = -1;
-    page[u] = __builtin_amdgcn_readfirstlane(max(p, -1));
+  __device__ __forceinline__ uint4 operator()(int n) const {
+    const uint32_t(&p)[4] = h[HG > 1 ? n >> 2 : 0];
+    return make_uint4(v16.pair(p[0], n & 3), v16.pair(p[1], n & 3), v16.pair(p[2], n & 3), v16.pair(p[3], n & 3));
   }
-}
+};
 
-// Keys k0, k0 + stride, .. below k1 (32 at a time) for all rows.
-template <typename T, int D, int G, int MT, bool PAIR>
-__device__ __forceinline__ void walk(const AttnArgs& a, const Unit& u, Rows<D, G, MT>& w, int low,
-                                     int k0, int k1, int stride, int lane) {
-  const int32_t* table = a.table + (int64_t)u.seq * a.per_seq;
-  int page[2], next[2];
-  Tile<D, G> t, tn;
+// A sequence's pages, 64 entries of its table at a time, one per lane: a load
+// for each tile would be waited for with the tile's reads of LDS.
+struct Pages {
+  const int32_t* table;
+  int len, shift, first, held;
+  int64_t pages;
+  __device__ __forceinline__ Pages(const AttnArgs& a, const Unit& u)
+      : table(a.table + (int64_t)u.seq * a.per_seq), len(u.len), shift(a.c.shift), first(-64), held(0),
+        pages(a.c.pages) {}
+  // The pages of keys key .. key + 31; -1 where there is none or a bad one.
+  __device__ __forceinline__ void of(int key, int lane, int (&page)[2]) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int k = key + 16 * u, i = k >> shift;
+      page[u] = -1;
+      if (k >= len) continue;
+      if (i - first >= 64) {  // keys rise
+        first = i;
+        const int at = i + lane, last = (len - 1) >> shift;
+        const int p = table[min(at, last)];
+        held = p < pages ? max(p, -1) : -1;
+      }
+      page[u] = __builtin_amdgcn_readlane(held, i - first);
+    }
+  }
+};
+
+// Keys k0, k0 + stride, .. below k1 (32 at a time) for 16 rows, through two
+// stages from `lds` on.
+template <typename T, int D, int G, bool PAIR>
+__device__ __forceinline__ void walk(const AttnArgs& a, const Unit& u, Rows<D, G>& w, int low,
+                                     int k0, int k1, int stride, int lane, const char* smem) {
+  using S = Stage<D, G>;
   if (k0 >= k1) return;
-  pages_of(a, table, k0, u.len, page);
-  load_tile(a.c, page, u.head, k0, lane, t);
-  pages_of(a, table, k0 + stride, u.len, next);
+  Pages pages(a, u);
+  const uint32_t lds = (uint32_t)(uintptr_t)smem;
+  const float scale = a.scale, slack = a.slack;
+  const Sixteen<T> k16;
+  const uint32_t r16 = lane & 15, q4 = (uint32_t)lane >> 4;
+  int page[2], next[2], after[2];
+  pages.of(k0, lane, page);
+  pages.of(k0 + stride, lane, next);
+  load_stage<D, G>(a.c, page, u.head, k0, lane, lds);
+  if (k0 + stride < k1) load_stage<D, G>(a.c, next, u.head, k0 + stride, lane, lds + S::kBytes);
+  pages.of(k0 + 2 * stride, lane, after);
+  int at = 0;
   for (int key = k0; key < k1; key += stride) {
-    int after[2] = {-1, -1};
-    if (key + stride < k1) {
-      load_tile(a.c, next, u.head, key + stride, lane, tn);
-      pages_of(a, table, key + 2 * stride, u.len, after);
-    }
-    if (key + 32 <= low && page[0] >= 0 && page[1] >= 0)
-      take<T, D, G, MT, PAIR, false>(w, t, page, key, a.scale, lane);
+    if (key + stride < k1)
+      wait_vm<S::kLoads>();
     else
-      take<T, D, G, MT, PAIR, true>(w, t, page, key, a.scale, lane);
-    t = tn;
+      wait_vm<0>();
+    asm volatile("" ::: "memory");
+    const char* st = smem + at;
+    float s[8];
+    uint32_t p[2][4 * S::NG];
+    floatx4 acc[2][S::NG];
+    products<T>(w, [&](int v, int j) {
+      const char* x = st + S::kK + (D == 128 ? 1024 * v + 16 * lane : 512 * v + 32 * r16 + 8 * q4);
+      return k16.word(*(const uint32_t*)(x + 4 * j));
+    }, acc);
+    read_params<S::NG>(st + S::kKp, q4, p);
+    scores(w, p, acc, s);
+    read_params<S::NG>(st + S::kVp, q4, p);
+    if (key + 32 > low || (page[0] | page[1]) < 0) hide(w.lim, page, key, q4, s, p);
+    weigh(w, scale, slack, s);
+    __builtin_amdgcn_sched_barrier(0);
+    ValueWords<D, G> vf{st + S::kV, {}, lane};
+    gather<D, G, PAIR>(w, p, s, vf, r16);
+    // the stage has been read
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (key + 2 * stride < k1) load_stage<D, G>(a.c, after, u.head, key + 2 * stride, lane, lds + at);
+    at ^= S::kBytes;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      page[i] = next[i];
-      next[i] = after[i];
-    }
+    for (int i = 0; i < 2; ++i) page[i] = next[i], next[i] = after[i];
+    pages.of(key + 3 * stride, lane, after);
   }
 }
 
-// The lane groups' shares of l and the offsets.
-template <int D, int G, int MT>
-__device__ __forceinline__ void finish_sums(Rows<D, G, MT>& w) {
+// The lane groups' shares of l and the offsets, and the parts of O together.
+template <int D, int G>
+__device__ __forceinline__ void finish_sums(Rows<D, G>& w) {
+  w.l += __shfl_xor(w.l, 16);
+  w.l += __shfl_xor(w.l, 32);
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    w.l[m] += __shfl_xor(w.l[m], 16);
-    w.l[m] += __shfl_xor(w.l[m], 32);
+  for (int g = 0; g < D / G; ++g) {
+    w.off[g] += __shfl_xor(w.off[g], 16);
+    w.off[g] += __shfl_xor(w.off[g], 32);
 #pragma unroll
-    for (int g = 0; g < D / G; ++g) {
-      w.off[m][g] += __shfl_xor(w.off[m][g], 16);
-      w.off[m][g] += __shfl_xor(w.off[m][g], 32);
-    }
+    for (int n = 0; n < G / 16; ++n) w.o[g * (G / 16) + n] += w.c[g];
   }
 }
 
@@ -413,10 +543,15 @@ __device__ __forceinline__ T* out_row(const AttnArgs& a, const Unit& u, int row)
 constexpr int kDecodeRows = 16, kDecodeWaves = 4, kSplitKeys = 256;
 
 template <typename T, int D, int G, bool PAIR>
-__global__ void __launch_bounds__(64 * kDecodeWaves)
+__global__ void __launch_bounds__(64 * kDecodeWaves, D / G == 4 ? 3 : 4)
 k_kv4_decode(AttnArgs a) {
+  using S = Stage<D, G>;
   constexpr int P = D + 4;  // of a row in LDS
-  __shared__ float so[kDecodeWaves][16][P];
+  constexpr int ROWS = PAIR ? 8 : 16;
+  constexpr int kRing = 2 * S::kBytes, kSums = ROWS * P * 4;
+  // a wavefront's stages, then its sums
+  constexpr int kOwn = kRing > kSums ? kRing : kSums;
+  __shared__ __attribute__((aligned(16))) char smem[kDecodeWaves * kOwn];
   __shared__ float sm[kDecodeWaves][16], sl[kDecodeWaves][16];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -426,35 +561,38 @@ k_kv4_decode(AttnArgs a) {
   const int count = min(u.rows - u.row0, 16);
   // the last row sees the most keys
   const int end = min(max(u.len - u.run + (u.row0 + count - 1) / a.per_kv + 1, 0), u.len);
-  const int per = (max((end + a.splits - 1) / a.splits, kSplitKeys) + 31) & ~31;
-  const int from = min((int64_t)split * per, (int64_t)end), to = min(from + per, end);
-  Rows<D, G, 1> w;
-  int low;
+  const int per = max(((end + a.splits - 1) / a.splits + 127) & ~127, a.per);
+  const int from = (int)min((int64_t)split * per, (int64_t)end), to = min(from + per, end);
+  Rows<D, G> w;
   // PAIR: rows of lanes 8 to 15 are those of 0 to 7
-  load_rows<T>(a, u, PAIR ? u.row0 - (lane & 8) : u.row0, lane, w, &low);
-  walk<T, D, G, 1, PAIR>(a, u, w, low, from + 32 * wave, to, 32 * kDecodeWaves, lane);
+  const int low = load_rows<T>(a, u, PAIR ? u.row0 - (lane & 8) : u.row0, lane, w);
+  walk<T, D, G, PAIR>(a, u, w, low, from + 32 * wave, to, 32 * kDecodeWaves, lane, smem + wave * kOwn);
   finish_sums(w);
   const int r16 = lane & 15, q4 = lane >> 4;
   if constexpr (PAIR) {
 #pragma unroll
     for (int n = 0; n < D / 16; ++n)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) w.o[0][n][r] += __shfl_xor(w.o[0][n][r], 8);
+      for (int r = 0; r < 4; ++r)  // of lane l ^ 8
+        w.o[n][r] += __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(w.o[n][r]), 0x128, 0xf, 0xf, false));
   }
   if (q4 == 0) {
-    sm[wave][r16] = w.m[0];
-    sl[wave][r16] = w.l[0];
+    sm[wave][r16] = w.m;
+    sl[wave][r16] = w.l;
   }
+  if (r16 < count) {
+    float* so = (float*)(smem + wave * kOwn) + r16 * P;
 #pragma unroll
-  for (int n = 0; n < D / 16; ++n)
+    for (int n = 0; n < D / 16; n += 2)
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      so[wave][r16][column<G>(n, 4 * q4 + r)] = w.o[0][n][r] + w.off[0][n / (G / 16)];
+      for (int r = 0; r < 4; ++r)
+        *(float2*)(so + column<G>(n, 4 * q4 + r)) =
+            make_float2(w.o[n][r] + w.off[n / (G / 16)], w.o[n + 1][r] + w.off[n / (G / 16)]);
+  }
   __syncthreads();
   // a thread takes eight columns of a row
-  for (int e = tid; e < 16 * (D / 8); e += 64 * kDecodeWaves) {
+  for (int e = tid; e < count * (D / 8); e += 64 * kDecodeWaves) {
     const int row = e / (D / 8), c = 8 * (e % (D / 8));
-    if (row >= count) continue;
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kDecodeWaves; ++i) m = fmaxf(m, sm[i][row]);
@@ -462,10 +600,11 @@ k_kv4_decode(AttnArgs a) {
 #pragma unroll
     for (int i = 0; i < kDecodeWaves; ++i) {
       // a wavefront without keys has -inf, 0 and zeros; one with NaN sums keeps them
-      const float f = sm[i][row] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(sm[i][row] - m);
+      const float f = sm[i][row] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((sm[i][row] - m) * a.scale);
+      const float* so = (const float*)(smem + i * kOwn) + row * P + c;
       l = fmaf(f, sl[i][row], l);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = fmaf(f, so[i][row][c + k], v[k]);
+      for (int k = 0; k < 8; ++k) v[k] = fmaf(f, so[k], v[k]);
     }
     if (a.splits > 1) {
       float* p = a.parts + ((int64_t)blockIdx.x * 16 + row) * (D + 4);
@@ -484,72 +623,230 @@ k_kv4_decode(AttnArgs a) {
   }
 }
 
-// One row per D / 8 threads: its splits, in order.
-template <typename T, int D>
+// A row per block: thread groups take every 256 / (D / 8)-th split each, with
+// four in flight, and are joined through LDS, all in fixed order.
+template <typename T, int D, int R>
 __global__ void __launch_bounds__(256)
 k_kv4_join(AttnArgs a) {
-  const int per = 256 / (16 * (D / 8));  // units of a block
-  const int row = threadIdx.x / (D / 8) % 16, c = 8 * (threadIdx.x % (D / 8));
-  const int64_t id = (int64_t)blockIdx.x * per + threadIdx.x / (16 * (D / 8));
-  if (id >= (int64_t)a.tiles * a.c.heads) return;
-  const Unit u = unit_of<kDecodeRows>(a, (int)(id / a.c.heads), (int)(id % a.c.heads));
+  constexpr int C = D / 8, N = 256 / C;  // threads of a row's columns, groups
+  __shared__ float sm[128], sl[N], so[N][D + 4];
+  const int tid = threadIdx.x, c = 8 * (tid % C), part = tid / C;
+  const int row = blockIdx.x % a.rows;
+  const int id = blockIdx.x / a.rows;
+  const Unit u = unit_of<R>(a, id / a.c.heads, id % a.c.heads);
   if (u.row0 + row >= u.rows) return;
-  const float* p = a.parts + (id * a.splits * 16 + row) * (D + 4);
+  const float* p = a.parts + ((int64_t)id * a.splits * R + row) * (D + 4);
+  constexpr int64_t S = R * (D + 4);
+  if (tid < a.splits) sm[tid] = p[tid * S + D];
+  __syncthreads();
   float m = -INFINITY;
-  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, p[(int64_t)s * 16 * (D + 4) + D]);
+  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, sm[s]);
   float l = 0.0f, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (int s = 0; s < a.splits; ++s) {
-    const float* x = p + (int64_t)s * 16 * (D + 4);
-    const float f = x[D] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(x[D] - m);
-    l = fmaf(f, x[D + 1], l);
-    const float4 y = *(const float4*)(x + c), z = *(const float4*)(x + c + 4);
-    v[0] = fmaf(f, y.x, v[0]), v[1] = fmaf(f, y.y, v[1]), v[2] = fmaf(f, y.z, v[2]), v[3] = fmaf(f, y.w, v[3]);
-    v[4] = fmaf(f, z.x, v[4]), v[5] = fmaf(f, z.y, v[5]), v[6] = fmaf(f, z.z, v[6]), v[7] = fmaf(f, z.w, v[7]);
-  }
-  const float f = l == 0.0f ? 0.0f : 1.0f / l;
+  for (int s = part; s < a.splits; s += 4 * N) {
+    float4 y[4], z[4];
+    float f[4], w[4];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] *= f;
-  store8(out_row<T, D>(a, u, u.row0 + row) + c, v, 8, true);
+    for (int i = 0; i < 4; ++i) {
+      const int k = s + i * N, at = min(k, a.splits - 1);
+      const float* x = p + at * S;
+      y[i] = *(const float4*)(x + c), z[i] = *(const float4*)(x + c + 4);
+      w[i] = x[D + 1];
+      f[i] = sm[at] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((sm[at] - m) * a.scale);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (s + i * N >= a.splits) break;
+      l = fmaf(f[i], w[i], l);
+      v[0] = fmaf(f[i], y[i].x, v[0]), v[1] = fmaf(f[i], y[i].y, v[1]);
+      v[2] = fmaf(f[i], y[i].z, v[2]), v[3] = fmaf(f[i], y[i].w, v[3]);
+      v[4] = fmaf(f[i], z[i].x, v[4]), v[5] = fmaf(f[i], z[i].y, v[5]);
+      v[6] = fmaf(f[i], z[i].z, v[6]), v[7] = fmaf(f[i], z[i].w, v[7]);
+    }
+  }
+  if (c == 0) sl[part] = l;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) so[part][c + k] = v[k];
+  __syncthreads();
+  if (tid >= D) return;
+  l = 0.0f;
+  float o = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    l += sl[i];
+    o += so[i][tid];
+  }
+  out_row<T, D>(a, u, u.row0 + row)[tid] = from_f32<T>(l == 0.0f ? 0.0f : o * (1.0f / l));
 }
 
-constexpr int kChunkTiles = 2, kChunkRows = 4 * 16 * kChunkTiles;
+constexpr int kChunkWaves = 8, kChunkRows = 16 * kChunkWaves;
+
+// Operands of 32 keys for the wavefronts of a block, in LDS: fragments of keys
+// and values as 16 + code, 1 KB each in the lanes' order, and parameters.
+template <int D, int G>
+struct Shared {
+  static constexpr int NG = D / G, J = D / 32, N = D / 16;
+  static constexpr int kK = 0, kV = 2 * J * 1024, kKp = kV + N * 1024, kVp = kKp + 128 * NG;
+  static constexpr int kBytes = kVp + 128 * NG;
+};
+// A wavefront's share of them on the way.  Heads of 128: a word of one of the 16
+// keys of a half, and the eight keys' words of V that give one tile of columns;
+// of 64: wavefronts 0 to 3 have a word of keys, 4 to 7 a tile of columns.
+template <int D, int G>
+struct Share {
+  uint32_t k, p;
+  uint4 v[2];
+};
+template <int D, int G>
+__device__ __forceinline__ void load_share(const Kv4& c, const int (&page)[2], int head, int key, int wave,
+                                           uint32_t lane, Share<D, G>& q) {
+  constexpr uint32_t NG = D / G, TG = G / 16, WG = G / 8, J = D / 32;
+  const uint32_t r16 = lane & 15, q4 = lane >> 4;
+  const int64_t token[2] = {key_token(c, page[0], head, key), key_token(c, page[1], head, key + 16)};
+  if (D == 128 || wave < 4) {
+    const int u = wave / J, j = wave % J;
+    q.k = *(const uint32_t*)(uniform(c.k_codes + (u ? token[1] : token[0]) * (D / 8)) +
+                             (r16 * (D / 2) + q4 * (D / 8) + 4u * j));
+  }
+  if (D == 128 || wave >= 4) {
+    const uint32_t n = D == 128 ? wave : wave - 4, word = n / TG * WG + r16 % WG;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      q.v[u] = *(const uint4*)(uniform(c.v_codes + token[u] * (D / 8)) + (64 * word + 16 * q4));
+  }
+  // parameters: threads 0 .. 32 NG - 1 the keys', as many behind them the values'
+  const uint32_t tid = 64 * wave + lane, i = tid % (32 * NG);
+  if (tid < 64 * NG) {
+    const uint32_t* base = tid < 32 * NG ? c.k_params : c.v_params;
+    q.p = base[(i < 16 * NG ? token[0] : token[1]) * NG + i % (16 * NG)];
+  }
+}
+template <typename T, int D, int G>
+__device__ __forceinline__ void store_share(const Share<D, G>& q, int wave, uint32_t lane, char* st,
+                                            const Sixteen<T>& k16, const Sixteen<__bf16>& v16) {
+  using S = Shared<D, G>;
+  constexpr uint32_t TG = G / 16;
+  const uint32_t r16 = lane & 15;
+  if (D == 128 || wave < 4) *(uint4*)(st + S::kK + wave * 1024 + 16 * lane) = k16.word(q.k);
+  if (D == 128 || wave >= 4) {
+    const int tile = D == 128 ? wave : wave - 4;
+    const uint32_t n = tile % TG;  // in its group: nibble n of the lane's halves or bytes
+    const uint32_t sel = G == 128  ? (n & 4 ? 0x07060302u : 0x05040100u)
+                         : G == 64 ? (r16 & 8 ? 0x07060302u : 0x05040100u)
+                                   : 0x0c040c00u + (r16 >> 2) * 0x00010001u;
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4& x = q.v[i >> 1];
+      h[i] = v16.pair(__builtin_amdgcn_perm(i & 1 ? x.w : x.y, i & 1 ? x.z : x.x, sel) >> (4 * (n & 3)), 0);
+    }
+    *(uint4*)(st + S::kV + tile * 1024 + 16 * lane) = make_uint4(h[0], h[1], h[2], h[3]);
+  }
+  const uint32_t tid = 64 * wave + lane;
+  if (tid < 64 * S::NG) *(uint32_t*)(st + S::kKp + 4 * tid) = q.p;
+}
+template <int D, int G>
+struct ValueFragments {
+  static constexpr bool kTight = false;
+  const char* base;  // of the lane
+  int g;
+  __device__ __forceinline__ void group(int i) { g = i; }
+  __device__ __forceinline__ uint4 operator()(int n) const {
+    return *(const uint4*)(base + (g * (G / 16) + n) * 1024);
+  }
+};
 
 template <typename T, int D, int G>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(64 * kChunkWaves, 2)
 k_kv4_chunk(AttnArgs a) {
-  constexpr int MT = kChunkTiles;
+  using S = Shared<D, G>;
+  __shared__ __attribute__((aligned(16))) char smem[2 * S::kBytes];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const Unit u = unit_of<kChunkRows>(a, blockIdx.x / a.c.heads, blockIdx.x % a.c.heads);
-  const int row0 = u.row0 + 16 * MT * wave;
-  if (row0 >= u.rows) return;
-  const int last = min(row0 + 16 * MT, u.rows) - 1;
-  const int end = min(max(u.len - u.run + last / a.per_kv + 1, 0), u.len);
-  Rows<D, G, MT> w;
-  int low;
-  load_rows<T>(a, u, row0, lane, w, &low);
-  walk<T, D, G, MT, false>(a, u, w, low, 0, end, 32, lane);
-  finish_sums(w);
-  const int r16 = lane & 15, q4 = lane >> 4;
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int row = row0 + 16 * m + r16;
-    if (row >= u.rows) continue;
-    T* p = out_row<T, D>(a, u, row);
-    const float f = w.l[m] == 0.0f ? 0.0f : 1.0f / w.l[m];
-    constexpr int TG = G / 16;
-#pragma unroll
-    for (int g = 0; g < D / G; ++g)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        typedef T Tx __attribute__((ext_vector_type(TG)));
-        Tx v;  // neighbouring columns
-#pragma unroll
-        for (int n = 0; n < TG; ++n)
-          v[n] = from_f32<T>((w.o[m][g * TG + n][r] + w.off[m][g]) * f);
-        *(Tx*)(p + column<G>(g * TG, 4 * q4 + r)) = v;
-      }
+  const int split = blockIdx.x % a.splits, id = blockIdx.x / a.splits;
+  const Unit u = unit_of<kChunkRows>(a, id / a.c.heads, id % a.c.heads);
+  if (u.row0 >= u.rows) return;
+  auto seen_by = [&](int row) { return min(max(u.len - u.run + row / a.per_kv + 1, 0), u.len); };
+  const int end = seen_by(min(u.row0 + kChunkRows, u.rows) - 1);
+  const int per = max(((end + a.splits - 1) / a.splits + 31) & ~31, a.per);
+  const int from = (int)min((int64_t)split * per, (int64_t)end), to = min(from + per, end);
+  // a wavefront behind the sequence's rows prepares its share alone
+  const int row0 = u.row0 + 16 * wave;
+  const bool live = row0 < u.rows;
+  const int mine = live ? min(to, seen_by(min(row0 + 16, u.rows) - 1)) : 0;
+  Rows<D, G> w;
+  const int low = load_rows<T>(a, u, row0, lane, w);
+  const Sixteen<T> k16;
+  const Sixteen<__bf16> v16;
+  Pages pages(a, u);
+  const uint32_t q4 = (uint32_t)lane >> 4;
+  const float scale = a.scale, slack = a.slack;
+  int page[3][2];
+  Share<D, G> share;
+  if (from < to) {
+    pages.of(from, lane, page[0]);
+    pages.of(from + 32, lane, page[1]);
+    pages.of(from + 64, lane, page[2]);
+    load_share(a.c, page[0], u.head, from, wave, lane, share);
+    store_share(share, wave, lane, smem, k16, v16);
+    if (from + 32 < to) load_share(a.c, page[1], u.head, from + 32, wave, lane, share);
   }
+  int at = 0;
+  for (int key = from; key < to; key += 32) {
+    // this tile's operands are there, and nobody reads the other stage any more
+    __syncthreads();
+    if (key + 32 < to) {
+      store_share(share, wave, lane, smem + (at ^ S::kBytes), k16, v16);
+      if (key + 64 < to) load_share(a.c, page[2], u.head, key + 64, wave, lane, share);
+    }
+    if (key < mine) {
+      const char* st = smem + at;
+      float s[8];
+      floatx4 acc[2][S::NG];
+      uint32_t p[2][4 * S::NG];
+      products<T>(w, [&](int v, int j) { return *(const uint4*)(st + S::kK + (v * S::J + j) * 1024 + 16 * lane); }, acc);
+      read_params<S::NG>(st + S::kKp, q4, p);
+      scores(w, p, acc, s);
+      read_params<S::NG>(st + S::kVp, q4, p);
+      if (key + 32 > low || (page[0][0] | page[0][1]) < 0) hide(w.lim, page[0], key, q4, s, p);
+      weigh(w, scale, slack, s);
+      ValueFragments<D, G> vf{st + S::kV + 16 * lane, 0};
+      gather<D, G, false>(w, p, s, vf, 0);
+    }
+    at ^= S::kBytes;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) page[i][0] = page[i + 1][0], page[i][1] = page[i + 1][1];
+    pages.of(key + 96, lane, page[2]);
+  }
+  if (!live) return;
+  finish_sums(w);
+  const int row = row0 + (lane & 15);
+  if (row >= u.rows) return;
+  constexpr int TG = G / 16;
+  if (a.splits > 1) {
+    float* x = a.parts + ((int64_t)blockIdx.x * kChunkRows + row - u.row0) * (D + 4);
+#pragma unroll
+    for (int n = 0; n < D / 16; n += 2)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        *(float2*)(x + column<G>(n, 4 * q4 + r)) = make_float2(w.o[n][r] + w.off[n / TG], w.o[n + 1][r] + w.off[n / TG]);
+    if (q4 == 0) {
+      x[D] = w.m;
+      x[D + 1] = w.l;
+    }
+    return;
+  }
+  T* x = out_row<T, D>(a, u, row);
+  const float f = w.l == 0.0f ? 0.0f : 1.0f / w.l;
+#pragma unroll
+  for (int g = 0; g < D / G; ++g)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      typedef T Tx __attribute__((ext_vector_type(TG)));
+      Tx v;  // neighbouring columns
+#pragma unroll
+      for (int n = 0; n < TG; ++n) v[n] = from_f32<T>((w.o[g * TG + n][r] + w.off[g]) * f);
+      *(Tx*)(x + column<G>(g * TG, 4 * q4 + r)) = v;
+    }
 }
 
 // Few rows for each sequence go to the decoding kernel: it splits the keys of
@@ -562,18 +859,30 @@ static int64_t row_tiles(const Kv4Attention& a, int rows) {
   const int64_t per = a.heads / a.cache.heads;
   return a.starts == nullptr ? a.seqs * ((per + rows - 1) / rows) : a.tokens * per / rows + a.seqs;
 }
-static int decode_splits(const Kv4Attention& a) {
-  const int64_t units = row_tiles(a, kDecodeRows) * a.cache.heads;
+// A unit's keys go to `splits` blocks, `per` or more to each.
+struct Split {
+  int rows, splits, per;
+};
+static Split split_of(const Kv4Attention& a) {
+  const bool decode = takes_decode(a);
+  Split s;
+  s.rows = decode ? kDecodeRows : kChunkRows;
+  const int64_t units = row_tiles(a, s.rows) * a.cache.heads;
   const int64_t keys = a.per_seq << a.cache.shift;
-  const int64_t most = (keys + kSplitKeys - 1) / kSplitKeys;
-  int64_t n = (4 * kCUs + units - 1) / units;
-  n = n < most ? n : most;
-  return (int)(n < 1 ? 1 : n > 128 ? 128 : n);
+  // Single tokens: four blocks of four wavefronts fit a compute unit.  Where the
+  // units fill them by themselves a part costs more than it hides: 64 x 500 keys,
+  // 8 kv heads: 12.0 us whole, 16.6 in two; one sequence of 8192, 8 kv heads: 10.5
+  // us in parts of 256, 12.4 of 192 and 11.9 of 512.  Runs: two blocks of eight.
+  const int64_t target = decode ? 4 * kCUs : 2 * kCUs;
+  s.per = !decode ? 512 : units < kCUs ? 256 : 320;
+  int64_t n = (target + units / 2) / units, most = keys / s.per;
+  if (n > most) n = most;
+  s.splits = (int)(n > 128 ? 128 : n < 1 ? 1 : n);
+  return s;
 }
 size_t kv4_attention_workspace(const Kv4Attention& a) {
-  if (!takes_decode(a)) return 0;
-  const int s = decode_splits(a);
-  return s == 1 ? 0 : (size_t)row_tiles(a, kDecodeRows) * a.cache.heads * s * 16 * (a.cache.dim + 4) * 4;
+  const Split s = split_of(a);
+  return s.splits == 1 ? 0 : (size_t)row_tiles(a, s.rows) * a.cache.heads * s.splits * s.rows * (a.cache.dim + 4) * 4;
 }
 
 template <typename T, int D, int G>
@@ -592,29 +901,32 @@ static hipError_t run(const Kv4Attention& k, hipStream_t stream) {
   a.starts = k.starts;
   a.table = k.table;
   a.lens = k.lens;
-  a.scale = k.scale * 1.4426950408889634f;
-  a.splits = 1;
+  // below 1e-30 all weights are 1, and -inf, a hidden key's score, keeps its product
+  a.scale = fmaxf(fabsf(k.scale) * 1.4426950408889634f, 1e-30f);
+  a.slack = 8.0f / a.scale;
+  a.flip = k.scale < 0.0f;
   a.parts = (float*)k.ws;
-  if (takes_decode(k)) {
-    a.splits = decode_splits(k);
-    a.tiles = (int)row_tiles(k, kDecodeRows);
-    const int64_t units = (int64_t)a.tiles * a.c.heads;
-    const dim3 grid((unsigned)(units * a.splits));
-    // a unit has at most per_kv rows where each sequence has one token
-    if (k.starts == nullptr && a.per_kv <= 8)
-      hipLaunchKernelGGL((k_kv4_decode<T, D, G, true>), grid, dim3(64 * kDecodeWaves), 0, stream, a);
+  const Split split = split_of(k);
+  a.splits = split.splits;
+  a.per = split.per;
+  a.tiles = (int)row_tiles(k, split.rows);
+  const int64_t units = (int64_t)a.tiles * a.c.heads;
+  const dim3 grid((unsigned)(units * a.splits));
+  // rows of a tile at most
+  a.rows = k.starts == nullptr && a.per_kv < split.rows ? a.per_kv : split.rows;
+  if (!takes_decode(k))
+    hipLaunchKernelGGL((k_kv4_chunk<T, D, G>), grid, dim3(64 * kChunkWaves), 0, stream, a);
+  else if (a.rows <= 8)
+    hipLaunchKernelGGL((k_kv4_decode<T, D, G, true>), grid, dim3(64 * kDecodeWaves), 0, stream, a);
+  else
+    hipLaunchKernelGGL((k_kv4_decode<T, D, G, false>), grid, dim3(64 * kDecodeWaves), 0, stream, a);
+  if (a.splits > 1) {
+    const dim3 rows((unsigned)(units * a.rows));
+    if (split.rows == kDecodeRows)
+      hipLaunchKernelGGL((k_kv4_join<T, D, kDecodeRows>), rows, dim3(256), 0, stream, a);
     else
-      hipLaunchKernelGGL((k_kv4_decode<T, D, G, false>), grid, dim3(64 * kDecodeWaves), 0, stream, a);
-    if (a.splits > 1) {
-      const int per = 256 / (16 * (D / 8));
-      hipLaunchKernelGGL((k_kv4_join<T, D>), dim3((unsigned)((units + per - 1) / per)), dim3(256), 0,
-                         stream, a);
-    }
-    return hipGetLastError();
+      hipLaunchKernelGGL((k_kv4_join<T, D, kChunkRows>), rows, dim3(256), 0, stream, a);
   }
-  a.tiles = (int)row_tiles(k, kChunkRows);
-  hipLaunchKernelGGL((k_kv4_chunk<T, D, G>), dim3((unsigned)((int64_t)a.tiles * a.c.heads)), dim3(256), 0,
-                     stream, a);
   return hipGetLastError();
 }
 template <typename T>
