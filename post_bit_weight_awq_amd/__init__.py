@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 from dataclasses import dataclass
 from typing import Optional
 
@@ -542,35 +543,42 @@ def awq_w4a16_adapted_backward(dY: torch.Tensor, X: torch.Tensor, low: torch.Ten
 
 
 # ------------------------------------------------- key/value cache in 4 bits
-@dataclass(frozen=True)
 class Kv4Cache:
     """The arrays of a 4-bit key/value cache (include/awq_mi355x.h has their
-    order); awq_kv4_cache makes one, and a program may bring its own memory.
-    Place p * page_size + i is token i of page p."""
-    k_codes: torch.Tensor   # [n_pages, n_heads, page_size, head_dim / 8] int32
-    v_codes: torch.Tensor   # [n_pages, n_heads, page_size / 16, head_dim / 8, 16] int32
-    k_params: torch.Tensor  # [n_pages, n_heads, page_size, head_dim / group_size, 2] fp16
-    v_params: torch.Tensor  # the same
+    order): k_codes [n_pages, n_heads, page_size, head_dim / 8] and v_codes
+    [n_pages, n_heads, page_size / 16, head_dim / 8, 16] int32, k_params and
+    v_params [n_pages, n_heads, page_size, head_dim / group_size, 2] fp16.
+    awq_kv4_cache makes one; a program may bring its own memory.  Place
+    p * page_size + i is token i of page p.  The arrays are checked here and not
+    by each call: they are not resized or moved while the object lives."""
+    __slots__ = ("k_codes", "v_codes", "k_params", "v_params", "n_pages", "n_heads", "page_size",
+                 "head_dim", "group_size", "_device", "_ref")
 
-    @property
-    def n_pages(self) -> int:
-        return self.k_codes.shape[0]
-
-    @property
-    def n_heads(self) -> int:
-        return self.k_codes.shape[1]
-
-    @property
-    def page_size(self) -> int:
-        return self.k_codes.shape[2]
-
-    @property
-    def head_dim(self) -> int:
-        return 8 * self.k_codes.shape[3]
-
-    @property
-    def group_size(self) -> int:
-        return self.head_dim // self.k_params.shape[3]
+    def __init__(self, k_codes: torch.Tensor, v_codes: torch.Tensor, k_params: torch.Tensor,
+                 v_params: torch.Tensor):
+        p, h, s, w = k_codes.shape
+        if k_params.dim() != 5 or not k_params.shape[3] or 8 * w % k_params.shape[3]:
+            raise ValueError(f"k_params {tuple(k_params.shape)} does not fit k_codes {tuple(k_codes.shape)}")
+        g = k_params.shape[3]
+        device = k_codes.device
+        for name, t, dtype, shape in (("k_codes", k_codes, torch.int32, (p, h, s, w)),
+                                      ("v_codes", v_codes, torch.int32, (p, h, s // 16, w, 16)),
+                                      ("k_params", k_params, torch.float16, (p, h, s, g, 2)),
+                                      ("v_params", v_params, torch.float16, (p, h, s, g, 2))):
+            if t.dtype is not dtype:
+                raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+            if t.shape != shape:
+                raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+            if t.device != device:
+                raise ValueError(f"{name} is on {t.device}, k_codes on {device}")
+        self.k_codes, self.v_codes, self.k_params, self.v_params = k_codes, v_codes, k_params, v_params
+        self.n_pages, self.n_heads, self.page_size = p, h, s
+        self.head_dim, self.group_size = 8 * w, 8 * w // g
+        self._device = device.index if device.type == "cuda" else -1
+        self._ref = ctypes.byref(AwqKv4Cache(k_codes.data_ptr(), v_codes.data_ptr(), k_params.data_ptr(),
+                                             v_params.data_ptr(), p, h, s, 8 * w, 8 * w // g))
 
 
 def awq_kv4_cache(n_pages: int, n_heads: int, page_size: int, head_dim: int, group_size: int = 64,
@@ -591,45 +599,39 @@ def awq_kv4_cache(n_pages: int, n_heads: int, page_size: int, head_dim: int, gro
         torch.zeros((n_pages, n_heads, page_size, g, 2), dtype=torch.float16, device=device))
 
 
-def _kv4(cache: Kv4Cache, dev: int) -> AwqKv4Cache:
-    """The C struct of a cache, its arrays checked against each other."""
+def _kv4(cache: Kv4Cache, dev: int):
+    """The C struct of a cache on GPU ``dev``."""
     if not isinstance(cache, Kv4Cache):
         raise TypeError("cache must be a Kv4Cache")
-    kc, kp = cache.k_codes, cache.k_params
-    if kc.dim() != 4 or kp.dim() != 5 or kp.shape[3] == 0:
-        raise ValueError("k_codes must be 4-D and k_params 5-D, with a group")
-    p, h, s, w = kc.shape
-    g = kp.shape[3]
-    if (8 * w) % g:
-        raise ValueError(f"k_params has {g} groups for head_dim={8 * w}")
-    c = AwqKv4Cache()
-    c.k_codes = _w4_ptr(kc, "k_codes", torch.int32, (p, h, s, w), dev)
-    c.v_codes = _w4_ptr(cache.v_codes, "v_codes", torch.int32, (p, h, s // 16, w, 16), dev)
-    c.k_params = _w4_ptr(kp, "k_params", torch.float16, (p, h, s, g, 2), dev)
-    c.v_params = _w4_ptr(cache.v_params, "v_params", torch.float16, (p, h, s, g, 2), dev)
-    c.n_pages, c.n_heads, c.page_size, c.head_dim, c.group_size = p, h, s, 8 * w, 8 * w // g
-    return c
+    if cache._device != dev:
+        if cache._device < 0:
+            raise ValueError("cache must be on the GPU")
+        raise ValueError(f"cache is on cuda:{cache._device}, the current device is cuda:{dev}")
+    return cache._ref
 
 
 def _kv4_rows(t, name: str, heads, dim: int, dtype, dev: int):
-    """(pointer, token stride, head stride) of [tokens, heads, dim] rows, whose
-    strides may be a slice's; heads None: any number."""
+    """(pointer, tokens, heads, token stride, head stride) of [tokens, heads, dim]
+    rows, whose strides may be a slice's; heads None: any number."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in _DTYPES or (dtype is not None and t.dtype is not dtype):
         raise TypeError(f"{name} must be {dtype or 'torch.float16 or torch.bfloat16'}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {dim}], got {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {dim}], got {tuple(shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on the GPU")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
     if t.requires_grad and torch.is_grad_enabled():
         _w4_tracked(name)
-    if t.stride(2) != 1:
+    n, h, _ = shape
+    ts, hs, ds = t.stride()
+    if ds != 1:
         raise ValueError(f"{name}'s last dimension must be dense")
     # a dimension of one row has no stride of its own
-    return (t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+    return t.data_ptr(), n, h, ts if n > 1 else 0, hs if h > 1 else 0
 
 
 def _kv4_device(t, name: str) -> int:
@@ -640,6 +642,14 @@ def _kv4_device(t, name: str) -> int:
     return torch._C._cuda_getDevice()
 
 
+@functools.lru_cache(maxsize=1024)
+def _kv4_attention_need(pages: int, heads: int, page: int, dim: int, group: int, n: int, h: int, seqs: int,
+                        per: int, ragged: bool) -> int:
+    """awq_kv4_attention_workspace_size, which depends on the sizes alone."""
+    c = AwqKv4Cache(None, None, None, None, pages, heads, page, dim, group)
+    return load().awq_kv4_attention_workspace_size(ctypes.byref(c), n, h, seqs, per, ragged)
+
+
 def awq_kv4_append(k: torch.Tensor, v: torch.Tensor, cache: Kv4Cache, slots: torch.Tensor, *,
                    stream=None) -> None:
     """Quantizes the keys and values of some tokens ([tokens, n_heads, head_dim]
@@ -648,14 +658,13 @@ def awq_kv4_append(k: torch.Tensor, v: torch.Tensor, cache: Kv4Cache, slots: tor
     have the same slot."""
     lib, dev = load(), _kv4_device(k, "k")
     c = _kv4(cache, dev)
-    kp, kt, kh = _kv4_rows(k, "k", c.n_heads, c.head_dim, None, dev)
-    vp, vt, vh = _kv4_rows(v, "v", c.n_heads, c.head_dim, k.dtype, dev)
-    n = k.shape[0]
-    if v.shape[0] != n:
-        raise ValueError(f"k has {n} tokens, v {v.shape[0]}")
+    dtype = k.dtype
+    kp, n, h, kt, kh = _kv4_rows(k, "k", cache.n_heads, cache.head_dim, None, dev)
+    vp, m, h, vt, vh = _kv4_rows(v, "v", cache.n_heads, cache.head_dim, dtype, dev)
+    if m != n:
+        raise ValueError(f"k has {n} tokens, v {m}")
     sp = _w4_ptr(slots, "slots", torch.int32, (n,), dev)
-    rc = lib.awq_kv4_append(ctypes.byref(c), kp, vp, _DTYPES[k.dtype], n, kt, kh, vt, vh, sp,
-                            _w4_stream(stream, dev))
+    rc = lib.awq_kv4_append(c, kp, vp, _DTYPES[dtype], n, kt, kh, vt, vh, sp, _w4_stream(stream, dev))
     if rc:
         check(rc)
 
@@ -670,11 +679,11 @@ def awq_kv4_gather(cache: Kv4Cache, slots: torch.Tensor, *, dtype: torch.dtype =
         raise TypeError(f"dtype must be torch.float16 or torch.bfloat16, got {dtype}")
     n = slots.numel()
     sp = _w4_ptr(slots, "slots", torch.int32, (n,), dev)
-    shape = (n, c.n_heads, c.head_dim)
+    shape = (n, cache.n_heads, cache.head_dim)
     with _on(stream):
         k, kp = _w4_out(k, "k", dtype, shape, slots, dev)
         v, vp = _w4_out(v, "v", dtype, shape, slots, dev)
-    rc = lib.awq_kv4_gather(ctypes.byref(c), sp, n, kp, vp, _DTYPES[dtype], _w4_stream(stream, dev))
+    rc = lib.awq_kv4_gather(c, sp, n, kp, vp, _DTYPES[dtype], _w4_stream(stream, dev))
     if rc:
         check(rc)
     return k, v
@@ -695,20 +704,19 @@ def awq_kv4_attention(q: torch.Tensor, cache: Kv4Cache, table: torch.Tensor, len
     rows behind the last sequence are left as they are."""
     lib, dev = load(), _kv4_device(q, "q")
     c = _kv4(cache, dev)
-    qp, qt, qh = _kv4_rows(q, "q", None, c.head_dim, None, dev)
-    n, h, d = q.shape
+    d = cache.head_dim
+    qp, n, h, qt, qh = _kv4_rows(q, "q", None, d, None, dev)
     if table.dim() != 2:
         raise ValueError("table must be [seqs, max_pages]")
     b, pages = table.shape
     tp = _w4_ptr(table, "table", torch.int32, (b, pages), dev)
     lp = _w4_ptr(lens, "lens", torch.int32, (b,), dev)
     sp = None if starts is None else _w4_ptr(starts, "starts", torch.int32, (b + 1,), dev)
+    sizes = (cache.n_pages, cache.n_heads, cache.page_size, d, cache.group_size, n, h, b, pages, starts is not None)
     with _on(stream):
         out, op = _w4_out(out, "out", q.dtype, (n, h, d), q, dev)
-        workspace, ws, size = _w4_workspace(lib.awq_kv4_attention_workspace_size,
-                                            (ctypes.byref(c), n, h, b, pages, starts is not None), q,
-                                            workspace)
-    rc = lib.awq_kv4_attention(ctypes.byref(c), qp, _DTYPES[q.dtype], n, h, qt, qh, b, sp, tp, pages, lp,
+        workspace, ws, size = _w4_workspace(_kv4_attention_need, sizes, q, workspace)
+    rc = lib.awq_kv4_attention(c, qp, _DTYPES[q.dtype], n, h, qt, qh, b, sp, tp, pages, lp,
                                d ** -0.5 if scale is None else scale, op, ws, size,
                                _w4_stream(stream, dev))
     if rc:

@@ -8,9 +8,12 @@
 //   k_adapt_order  the backward pass's copies A^T and B^T, whose rows are what the
 //                  products read, and each adapter's tokens in order
 //   k_adapt_grad   dA[a] = sum over a's tokens of v[t]^T X[t], dB[a] likewise of dY
-//                  and low: the left side's fp32 values as sums of 16-bit parts,
-//                  the right side transposed in registers; a long list of tokens is
-//                  taken in chunks, k_adapt_join adds them in order
+//                  and low: the left side's fp32 values as sums of 16-bit parts
+//                  (k_adapt_left), the right side transposed in registers; a long
+//                  list of tokens is taken in chunks, k_adapt_join adds them in
+//                  order
+#include <type_traits>
+
 #include "w4_adapt.h"
 
 namespace awq {
@@ -48,49 +51,49 @@ __device__ __forceinline__ int up_of(float top) {
   return e - 15;
 }
 
+constexpr int kLowWaves = 8;
+
 struct LowArgs {
   const uint16_t *X, *A;  // [N, K] dense; [count][rank][lda]
   const int32_t* ids;
   const float* scale;  // of the parts
-  float* low;          // [splits, N, rank] or NULL
-  uint16_t* parts;     // or NULL
-  int* up;             // fp16's parts
+  float* low;          // [splits, N, rank]
+  float* out;          // [N, rank] or NULL
+  uint16_t* parts;
+  int* up;  // fp16's parts
   int N, K, lda, count, rank, width, nparts, splits;
-  int scaled;          // low takes the scale too
+  int scaled;  // out takes the scale too
 };
 
-constexpr int kLowWaves = 8;
-
-// Tile of 16 MT tokens by 16 RT ranks (all).  SLOTS: block z takes the z-th
-// adapter of its tile and every splits-th piece of the sum; else a block takes
-// all of them one by one and leaves parts.
-template <typename T, int MT, int RT, bool SLOTS>
+// Tile of 16 MT tokens by 16 RT ranks (all), eight wavefronts along the sum, of
+// which block x takes a piece.  Single tokens (SLOTS): block z takes the z-th
+// adapter of its tile; else a block takes all of them one by one.  Pieces' sums
+// lie in `low` one behind the other; k_adapt_parts adds them.  FULL: K is a
+// multiple of 32, so rows are aligned and no step needs a check: a wavefront then
+// has U steps' loads in flight.
+// Bound by what a compute unit gets from L2 (about 30 bytes a ns here): high tiles
+// read A less often, pieces keep all units busy (4096 tokens, 15360 columns, rank
+// 64: 83 us with 16 tokens and whole sums, PERF_LOW with 64 and quarters).
+template <typename T, int MT, int RT, int U, bool SLOTS, bool FULL>
 __global__ void __launch_bounds__(64 * kLowWaves)
 k_adapt_low(LowArgs a) {
-  constexpr int R = 16 * RT, RP = R + 1, M = 16 * MT;
-  extern __shared__ float red[];  // [wavefront][M][RP]
+  constexpr int R = 16 * RT, RP = R + 1, M = 16 * MT, W = kLowWaves;
+  extern __shared__ float red[];  // [wavefront][16][RP]
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, q4 = lane >> 4;
-  const int t0 = blockIdx.y * M;
+  const int t0 = blockIdx.y * M, split = blockIdx.x;
   int id = -1;
   if (lane < M && t0 + lane < a.N) id = a.ids[t0 + lane];
   if (id >= a.count) id = -1;
-  const int split = SLOTS ? blockIdx.x : 0;
   uint64_t wait = __ballot(id >= 0);
+  float* const low = a.low + (size_t)split * a.N * a.rank;
   // tokens without an adapter have zeros
-  const bool first = !SLOTS || blockIdx.z == 0;
-  auto leave = [&](int t, float v0, float v1) {  // ranks lane and lane + 64
-    const int token = t0 + t;
-    if (a.low) {
-      float* p = a.low + ((size_t)split * a.N + token) * a.rank;
-      if (lane < a.rank) p[lane] = v0;
-      if (lane + 64 < a.rank) p[lane + 64] = v1;
+  if (!SLOTS || blockIdx.z == 0)
+    for (int e = tid; e < M * a.rank; e += 64 * W) {
+      const int t = e / a.rank;
+      if (t0 + t < a.N && !((wait >> t) & 1)) low[(size_t)t0 * a.rank + e] = 0.0f;
     }
-  };
-  if (first)
-    for (int t = wave; t < M && t0 + t < a.N; t += kLowWaves)
-      if (!((wait >> t) & 1)) leave(t, 0.0f, 0.0f);
   if (SLOTS) {
     for (int z = blockIdx.z; z > 0 && wait; --z) {
       const int one = __builtin_amdgcn_readlane(id, __builtin_ctzll(wait));
@@ -100,6 +103,9 @@ k_adapt_low(LowArgs a) {
   }
   const int steps = (a.K + 31) >> 5;
   const int s0 = (int)((int64_t)steps * split / a.splits), s1 = (int)((int64_t)steps * (split + 1) / a.splits);
+  const uint16_t* x[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) x[m] = a.X + (int64_t)min(t0 + 16 * m + r16, a.N - 1) * a.K + 8 * q4;
   while (wait) {
     const int one = __builtin_amdgcn_readlane(id, __builtin_ctzll(wait));
     const uint64_t mine = __ballot(id == one);
@@ -109,100 +115,165 @@ k_adapt_low(LowArgs a) {
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int n = 0; n < RT; ++n) acc[m][n] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-    const uint16_t* x[MT];
     const uint16_t* w[RT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) x[m] = a.X + (int64_t)min(t0 + 16 * m + r16, a.N - 1) * a.K + 8 * q4;
 #pragma unroll
     for (int n = 0; n < RT; ++n)
       w[n] = a.A + ((int64_t)one * a.rank + min(16 * n + r16, a.rank - 1)) * a.lda + 8 * q4;
-    // two neighbouring steps of 32 columns at a time
-    for (int s = s0 + 2 * wave; s < s1; s += 2 * kLowWaves) {
+    auto take = [&](int s, auto count) {
+      constexpr int C = decltype(count)::value;
+      uint4 xv[C][MT], wv[C][RT];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int c = s + h;
-        const int left = c < s1 ? a.K - 32 * c - 8 * q4 : 0;
-        uint4 xv[MT], wv[RT];
+      for (int h = 0; h < C; ++h) {
+        const int c = 32 * (s + h), left = a.K - c - 8 * q4;
 #pragma unroll
-        for (int m = 0; m < MT; ++m) xv[m] = load8(x[m] + 32 * c, left);
+        for (int m = 0; m < MT; ++m) xv[h][m] = FULL ? *(const uint4*)(x[m] + c) : load8(x[m] + c, left);
 #pragma unroll
-        for (int n = 0; n < RT; ++n) wv[n] = load8(w[n] + 32 * c, left);
+        for (int n = 0; n < RT; ++n) wv[h][n] = FULL ? *(const uint4*)(w[n] + c) : load8(w[n] + c, left);
+      }
+#pragma unroll
+      for (int h = 0; h < C; ++h)
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int n = 0; n < RT; ++n) acc[m][n] = mfma16<T>(xv[m], wv[n], acc[m][n]);
-      }
+          for (int n = 0; n < RT; ++n) acc[m][n] = mfma16<T>(xv[h][m], wv[h][n], acc[m][n]);
+    };
+    // U neighbouring steps of 32 columns at a time
+    for (int s = s0 + U * wave; s < s1; s += U * W) {
+      if (s + U <= s1)
+        take(s, std::integral_constant<int, U>{});
+      else
+        for (int h = s; h < s1; ++h) take(h, std::integral_constant<int, 1>{});
     }
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < MT; ++m) {
+      if (m > 0) __syncthreads();
 #pragma unroll
       for (int n = 0; n < RT; ++n)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          red[(wave * M + 16 * m + 4 * q4 + r) * RP + 16 * n + r16] = acc[m][n][r];
-    __syncthreads();
-    const float scale = a.scale[one];
-    for (int t = wave; t < M; t += kLowWaves) {
-      if (!((mine >> t) & 1)) continue;
-      float v[2] = {0.0f, 0.0f};
+        for (int r = 0; r < 4; ++r) red[(wave * 16 + 4 * q4 + r) * RP + 16 * n + r16] = acc[m][n][r];
+      __syncthreads();
+      for (int e = tid; e < 16 * a.rank; e += 64 * W) {
+        const int t = e / a.rank, r = e - t * a.rank;
+        if (!((mine >> (16 * m + t)) & 1)) continue;
+        float v = 0.0f;
 #pragma unroll
-      for (int i = 0; i < kLowWaves; ++i) {
-        if (lane < R) v[0] += red[(i * M + t) * RP + lane];
-        if (lane + 64 < R) v[1] += red[(i * M + t) * RP + lane + 64];
-      }
-      const float k = a.scaled ? scale : 1.0f;
-      leave(t, v[0] * k, v[1] * k);
-      if (!SLOTS && a.parts) {
-        v[0] = lane < a.rank ? v[0] * scale : 0.0f;
-        v[1] = lane + 64 < a.rank ? v[1] * scale : 0.0f;
-        uint16_t* p = a.parts + (int64_t)(t0 + t) * a.width;
-        if constexpr (__is_same(T, _Float16)) {
-          float top = 0.0f;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) top = fmaxf(top, fabsf(v[i]) < INFINITY ? fabsf(v[i]) : 0.0f);
-#pragma unroll
-          for (int s = 1; s < 64; s *= 2) top = fmaxf(top, __shfl_xor(top, s));
-          const int e = up_of(top);
-          if (lane == 0) a.up[t0 + t] = e;
-          v[0] = ldexpf(v[0], -e);
-          v[1] = ldexpf(v[1], -e);
-        }
-        uint16_t h[2][3];
-        split_parts<T>(v[0], h[0]);
-        split_parts<T>(v[1], h[1]);
-        for (int i = 0; i < a.nparts; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (lane + 64 * j < a.rank)
-              p[i * a.rank + lane + 64 * j] = i == 0 ? h[j][0] : i == 1 ? h[j][1] : h[j][2];
-        const int end = a.nparts * a.rank;  // less than 32 zeros
-        if (lane < a.width - end) p[end + lane] = 0;
+        for (int i = 0; i < W; ++i) v += red[(i * 16 + t) * RP + r];
+        low[(size_t)(t0 + 16 * m) * a.rank + e] = v;
       }
     }
     if (!SLOTS) __syncthreads();
   }
 }
 
-template <typename T, bool SLOTS>
-static hipError_t launch_low(const LowArgs& a, hipStream_t stream) {
+// A wavefront per token: the pieces' sums in order, as `out` (times the scale
+// where `scaled`) and, times the scale, as parts.
+template <typename T>
+__global__ void __launch_bounds__(256)
+k_adapt_parts(LowArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= a.N) return;
+  int id = a.ids[t];
+  if (id >= a.count) id = -1;
+  const float scale = id < 0 ? 0.0f : a.scale[id];
+  float v[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int r = lane + 64 * j;
+    if (r >= a.rank) continue;
+    const float* p = a.low + (size_t)t * a.rank + r;
+    float s = 0.0f;
+    for (int k = 0; k < a.splits; k += 4) {
+      float y[4];  // past the end the last one, not added
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = p[(size_t)min(k + i, a.splits - 1) * a.N * a.rank];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s += k + i < a.splits ? y[i] : 0.0f;
+    }
+    v[j] = id < 0 ? 0.0f : s;
+    if (a.out) a.out[(size_t)t * a.rank + r] = a.scaled ? v[j] * scale : v[j];
+    v[j] *= scale;
+  }
+  uint16_t* p = a.parts + (int64_t)t * a.width;
+  if constexpr (__is_same(T, _Float16)) {
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) top = fmaxf(top, fabsf(v[i]) < INFINITY ? fabsf(v[i]) : 0.0f);
+#pragma unroll
+    for (int s = 1; s < 64; s *= 2) top = fmaxf(top, __shfl_xor(top, s));
+    const int e = up_of(top);
+    if (lane == 0) a.up[t] = e;
+    v[0] = ldexpf(v[0], -e);
+    v[1] = ldexpf(v[1], -e);
+  }
+  uint16_t h[2][3];
+  split_parts<T>(v[0], h[0]);
+  split_parts<T>(v[1], h[1]);
+  for (int i = 0; i < a.nparts; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (lane + 64 * j < a.rank) p[i * a.rank + lane + 64 * j] = i == 0 ? h[j][0] : i == 1 ? h[j][1] : h[j][2];
+  const int end = a.nparts * a.rank;  // less than 32 zeros
+  if (lane < a.width - end) p[end + lane] = 0;
+}
+
+// Token tiles of the sum of low: 64 high where the ranks' registers allow it and
+// there are enough tokens, and pieces of at least 512 columns until each unit has
+// a block.
+struct LowPlan {
+  int mt, splits;
+};
+static LowPlan low_plan(int64_t N, int64_t K, int rank) {
+  LowPlan p;
+  p.mt = N <= 128 ? 1 : rank > 64 || N <= 512 ? 2 : 4;
+  const int64_t tiles = (N + 16 * p.mt - 1) / (16 * p.mt);
+  int64_t n = kCUs / tiles;
+  if (n > K / 512) n = K / 512;
+  p.splits = (int)(n < 1 ? 1 : n > 8 ? 8 : n);
+  return p;
+}
+
+template <typename T, bool SLOTS, bool FULL>
+static hipError_t launch_low(const LowArgs& a, int mt, hipStream_t stream) {
   const int rt = (a.rank + 15) / 16;
-  auto go = [&](auto* kernel, int mt, int r) {
-    const int M = 16 * mt, lds = kLowWaves * M * (16 * r + 1) * 4;
+  auto go = [&](auto* kernel, int r) {
+    const int lds = kLowWaves * 16 * (16 * r + 1) * 4;
     if (lds > 65536) {
       const hipError_t e =
           hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
       if (e != hipSuccess) return e;
     }
-    const unsigned tiles = (unsigned)((a.N + M - 1) / M);
-    const dim3 grid(SLOTS ? a.splits : 1, tiles, SLOTS ? (unsigned)(a.N < 16 ? a.N : 16) : 1);
+    const dim3 grid(a.splits, (unsigned)((a.N + 16 * mt - 1) / (16 * mt)),
+                    SLOTS ? (unsigned)(a.N < 16 ? a.N : 16) : 1);
     hipLaunchKernelGGL(kernel, grid, dim3(64 * kLowWaves), lds, stream, a);
     return hipGetLastError();
   };
-  constexpr int MT = SLOTS ? 1 : 2;
-  if (rt == 1) return go(&k_adapt_low<T, MT, 1, SLOTS>, MT, 1);
-  if (rt == 2) return go(&k_adapt_low<T, MT, 2, SLOTS>, MT, 2);
-  if (rt <= 4) return go(&k_adapt_low<T, MT, 4, SLOTS>, MT, 4);
-  return go(&k_adapt_low<T, MT, 8, SLOTS>, MT, 8);
+  if constexpr (!SLOTS) {
+    constexpr int U = FULL ? 2 : 1;
+    if (mt == 4) {
+      if (rt == 1) return go(&k_adapt_low<T, 4, 1, U, false, FULL>, 1);
+      if (rt == 2) return go(&k_adapt_low<T, 4, 2, U, false, FULL>, 2);
+      return go(&k_adapt_low<T, 4, 4, U, false, FULL>, 4);
+    }
+    if (mt == 2) {
+      if (rt == 1) return go(&k_adapt_low<T, 2, 1, U, false, FULL>, 1);
+      if (rt == 2) return go(&k_adapt_low<T, 2, 2, U, false, FULL>, 2);
+      if (rt <= 4) return go(&k_adapt_low<T, 2, 4, U, false, FULL>, 4);
+      return go(&k_adapt_low<T, 2, 8, 1, false, FULL>, 8);
+    }
+  }
+  constexpr int U = FULL ? 2 : 1;
+  if (rt == 1) return go(&k_adapt_low<T, 1, 1, U, SLOTS, FULL>, 1);
+  if (rt == 2) return go(&k_adapt_low<T, 1, 2, U, SLOTS, FULL>, 2);
+  if (rt <= 4) return go(&k_adapt_low<T, 1, 4, U, SLOTS, FULL>, 4);
+  return go(&k_adapt_low<T, 1, 8, U, SLOTS, FULL>, 8);
+}
+template <typename T, bool FULL>
+static hipError_t launch_parts(const LowArgs& a, int mt, hipStream_t stream) {
+  const hipError_t e = launch_low<T, false, FULL>(a, mt, stream);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((k_adapt_parts<T>), dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, stream, a);
+  return hipGetLastError();
 }
 
 // ------------------------------------------------------------ backward pass
@@ -218,7 +289,8 @@ struct OrderArgs {
 // columns of A or B of an adapter, transposed through LDS.
 __global__ void __launch_bounds__(kOrder)
 k_adapt_order(OrderArgs a) {
-  __shared__ uint16_t tile[64 * 129];
+  constexpr int kTileRow = 136;
+  __shared__ __attribute__((aligned(16))) uint16_t tile[64 * kTileRow];
   __shared__ int wsum[kOrder / 64][2];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   if ((int)blockIdx.x < a.count) {
@@ -278,27 +350,38 @@ k_adapt_order(OrderArgs a) {
     }
     return;
   }
-  const int ka = (a.K + 63) / 64, kb = (a.ldb + 63) / 64;
+  const int ka = a.K / 64, kb = (a.ldb + 63) / 64, rb = a.rank >> 3;
   const int64_t id = (int64_t)blockIdx.x - a.count;
   const int which = (int)(id % (ka + kb));
   const int64_t ad = id / (ka + kb);
   if (which < ka) {
-    const int c0 = 64 * which;  // K is a multiple of 128
+    const int c0 = 64 * which;
     const uint16_t* s = a.A + ad * a.rank * a.K + c0;
-    for (int e = tid; e < 64 * a.rank; e += kOrder)
-      tile[(e & 63) * 129 + (e >> 6)] = s[(int64_t)(e >> 6) * a.K + (e & 63)];
+    for (int e = tid; e < 8 * a.rank; e += kOrder) {  // eight columns of a rank
+      const int r = e >> 3, c = 8 * (e & 7);
+      const uint4 v = *(const uint4*)(s + (int64_t)r * a.K + c);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) tile[(c + i) * kTileRow + r] = (uint16_t)(word_of(v, i >> 1) >> (16 * (i & 1)));
+    }
     __syncthreads();
-    uint16_t* d = a.At + (ad * a.K + c0) * a.rank;
-    for (int e = tid; e < 64 * a.rank; e += kOrder) d[e] = tile[(e / a.rank) * 129 + e % a.rank];
+    uint4* d = (uint4*)(a.At + (ad * a.K + c0) * a.rank);
+    for (int e = tid; e < 64 * rb; e += kOrder) d[e] = *(const uint4*)(tile + (e / rb) * kTileRow + 8 * (e % rb));
   } else {
     const int o0 = 64 * (which - ka);
-    const uint16_t* s = a.B + (ad * a.O + o0) * a.rank;
-    for (int e = tid; e < 64 * a.rank; e += kOrder)
-      tile[(e / a.rank) * 129 + e % a.rank] = o0 + e / a.rank < a.O ? s[e] : (uint16_t)0;
+    const uint4* s = (const uint4*)(a.B + (ad * a.O + o0) * a.rank);
+    for (int e = tid; e < 64 * rb; e += kOrder)
+      *(uint4*)(tile + (e / rb) * kTileRow + 8 * (e % rb)) = o0 + e / rb < a.O ? s[e] : make_uint4(0, 0, 0, 0);
     __syncthreads();
     uint16_t* d = a.Bt + ad * a.rank * a.ldb + o0;
-    for (int e = tid; e < 64 * a.rank; e += kOrder)
-      if (o0 + (e & 63) < a.ldb) d[(int64_t)(e >> 6) * a.ldb + (e & 63)] = tile[(e & 63) * 129 + (e >> 6)];
+    for (int e = tid; e < 8 * a.rank; e += kOrder) {  // eight rows of a rank
+      const int r = e >> 3, o = 8 * (e & 7);
+      if (o0 + o >= a.ldb) continue;
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = tile[(o + 2 * i) * kTileRow + r] | (uint32_t)tile[(o + 2 * i + 1) * kTileRow + r] << 16;
+      *(uint4*)(d + (int64_t)r * a.ldb + o) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   }
 }
 
@@ -306,26 +389,24 @@ struct GradArgs {
   const uint16_t *X, *dY;
   const float *v, *low, *scale;  // [N, rank]
   const int32_t *order, *start;
-  float *dA, *dB;      // [count][rank][K], [count][O][rank]
-  float *pA, *pB;      // of a unit
-  int N, K, O, count, rank, chunk;
+  uint16_t* left;  // [v, low][part][ranks][stride]: see k_adapt_left
+  int* up;         // [unit][v, low][ranks], fp16
+  float *dA, *dB;  // [count][rank][K], [count][O][rank]
+  float *pA, *pB;  // of the units of adapters with more than one: part_of
+  int64_t stride;
+  int N, K, O, count, rank, ranks, chunk;  // ranks: rounded up to 16
 };
 // Unit u: adapter a owns the units from start[a] / chunk + a on.
 __device__ __forceinline__ int unit_base(const GradArgs& g, int a) { return g.start[a] / g.chunk + a; }
-
-constexpr int kGradWaves = 4, kGradCols = 128;
-
-// 16 RT ranks from 64 z on by 128 columns of X, then of dY; each wavefront takes
-// every fourth 32 tokens of the chunk.
-template <typename T, int RT>
-__global__ void __launch_bounds__(64 * kGradWaves, 1)
-k_adapt_grad(GradArgs g) {
-  constexpr int R = 16 * RT, P = __is_same(T, _Float16) ? 2 : 3, CP = kGradCols + 4;
-  extern __shared__ float red[];  // [2][R][CP]
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r16 = lane & 15, q4 = lane >> 4;
-  const int unit = blockIdx.y, r0 = 64 * blockIdx.z;
+// An adapter of c >= chunk tokens finds room for its ceil(c / chunk) units'
+// sums: floor(2 c / chunk) is as many at least.
+__device__ __forceinline__ int64_t part_of(const GradArgs& g, int a) { return 2 * (int64_t)g.start[a] / g.chunk; }
+// The tokens p0 .. p1 - 1 of a unit in `order`; false where it has none.
+struct GradUnit {
+  int a, p0, p1, all;  // all: the adapter's tokens
+  int piece;           // of them
+};
+__device__ __forceinline__ bool grad_unit(const GradArgs& g, int unit, GradUnit* u) {
   int a = 0, hi = g.count;  // unit_base(a) <= unit < unit_base(hi)
   while (hi - a > 1) {
     const int mid = (a + hi) >> 1;
@@ -334,65 +415,145 @@ k_adapt_grad(GradArgs g) {
     else
       hi = mid;
   }
-  const int begin = g.start[a], count = g.start[a + 1] - begin;
-  const int piece = unit - unit_base(g, a);
-  if (piece * g.chunk >= count) return;
-  const int p0 = begin + piece * g.chunk, p1 = min(p0 + g.chunk, begin + count);
+  const int begin = g.start[a], end = g.start[a + 1];
+  u->a = a;
+  u->all = end - begin;
+  u->piece = unit - unit_base(g, a);
+  u->p0 = begin + u->piece * g.chunk;
+  u->p1 = min(u->p0 + g.chunk, end);
+  return u->p0 < end;
+}
+// Place of a unit's first token in the rows of `left`: adapters begin on 16 bytes.
+__device__ __forceinline__ int64_t left_place(const GradArgs& g, const GradUnit& u) {
+  return ((g.start[u.a] + 7) & ~7) + 8 * (int64_t)u.a + (int64_t)u.piece * g.chunk;
+}
+
+template <typename T>
+constexpr int kLeftParts = __is_same(T, _Float16) ? 2 : 3;
+
+// The left operands of the gradients once instead of in every block: v and low of
+// a unit's tokens as 16-bit parts, a rank's tokens in a row.  fp16's are in units
+// of the largest of the rank's tokens.
+template <typename T>
+__global__ void __launch_bounds__(256)
+k_adapt_left(GradArgs g) {
+  constexpr int P = kLeftParts<T>;
+  __shared__ float tile[16][68];
+  __shared__ float tops[16][17];
+  const int tid = threadIdx.x;
+  const int unit = blockIdx.x, side = blockIdx.y & 1, r0 = 16 * (blockIdx.y >> 1);
+  GradUnit u;
+  if (!grad_unit(g, unit, &u)) return;
+  const float* L = side ? g.low : g.v;
+  const int ti = tid >> 2, tr = 4 * (tid & 3);  // one of 64 tokens, four ranks
+  auto load = [&](int at) {  // of token p0 + at
+    floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (u.p0 + at < u.p1 && r0 + tr < g.rank) v = *(const floatx4*)(L + (int64_t)g.order[u.p0 + at] * g.rank + r0 + tr);
+    return v;
+  };
+  const int r = tid >> 4, i4 = 4 * (tid & 15);  // a rank, four tokens
+  int e = 0;
+  if constexpr (__is_same(T, _Float16)) {
+    float top[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int at = ti; u.p0 + at < u.p1; at += 64) {
+      const floatx4 v = load(at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], fabsf(v[i]) < INFINITY ? fabsf(v[i]) : 0.0f);
+    }
+    // of the 16 tokens that a wavefront has, then of the wavefronts
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int s = 4; s < 64; s *= 2) top[i] = fmaxf(top[i], __shfl_xor(top[i], s));
+      if ((tid & 60) == 0) tops[tr + i][tid >> 6] = top[i];
+    }
+    __syncthreads();
+    e = up_of(fmaxf(fmaxf(tops[r][0], tops[r][1]), fmaxf(tops[r][2], tops[r][3])));
+    if (blockIdx.z == 0 && i4 == 0) g.up[(unit * 2 + side) * g.ranks + r0 + r] = e;
+  }
+  uint16_t* d = g.left + ((int64_t)side * P * g.ranks + r0 + r) * g.stride + left_place(g, u);
+  const int n = u.p1 - u.p0;
+  for (int b = 128 * blockIdx.z; b < 128 * (int)blockIdx.z + 128; b += 64) {
+    const floatx4 v = load(b + ti);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tile[tr + i][ti] = v[i];
+    __syncthreads();
+    uint16_t h[4][P];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split_parts<T>(ldexpf(tile[r][i4 + i], -e), h[i]);
+    // up to seven places behind the last token are this adapter's too
+    if (b + i4 < n)
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+        *(uint2*)(d + (int64_t)p * g.ranks * g.stride + b + i4) =
+            make_uint2(h[0][p] | (uint32_t)h[1][p] << 16, h[2][p] | (uint32_t)h[3][p] << 16);
+  }
+}
+
+constexpr int kGradWaves = 4, kGradCols = 128;
+
+// 16 RT ranks from 64 z on by 128 columns of X, then of dY; each wavefront takes
+// every fourth 32 tokens of the unit.
+template <typename T, int RT>
+__global__ void __launch_bounds__(64 * kGradWaves, 2)
+k_adapt_grad(GradArgs g) {
+  constexpr int R = 16 * RT, P = kLeftParts<T>, CP = kGradCols + 4;
+  extern __shared__ float red[];  // [2][R][CP]
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r16 = lane & 15, q4 = lane >> 4;
+  const int unit = blockIdx.y, r0 = 64 * blockIdx.z;
+  GradUnit u;
+  if (!grad_unit(g, unit, &u)) return;
   const int ka = g.K / kGradCols;
   const bool right = (int)blockIdx.x >= ka;  // dB
   const int C = right ? g.O : g.K, c0 = kGradCols * (right ? blockIdx.x - ka : blockIdx.x);
-  const uint16_t* Y = right ? g.dY : g.X;
-  const float* L = right ? g.low : g.v;
-
-  int up = 0;
-  if constexpr (__is_same(T, _Float16)) {
-    // fp16's parts are in units of the wavefront's largest value
-    float top = 0.0f;
-    const int per = min(R, g.rank - r0);
-    for (int s = p0 + 32 * wave; s < p1; s += 32 * kGradWaves) {
-      const int n = min(32, p1 - s) * per;
-      for (int e = lane; e < n; e += 64) {
-        const float v = fabsf(L[(int64_t)g.order[s + e / per] * g.rank + r0 + e % per]);
-        top = fmaxf(top, v < INFINITY ? v : 0.0f);
-      }
-    }
-#pragma unroll
-    for (int s = 1; s < 64; s *= 2) top = fmaxf(top, __shfl_xor(top, s));
-    up = up_of(top);
-  }
+  const uint16_t* Y = (right ? g.dY : g.X) + c0 + 8 * r16;
+  const uint16_t* L = g.left + ((int64_t)right * P * g.ranks + r0 + r16) * g.stride + left_place(g, u) + 8 * q4;
+  const int m_last = (g.ranks - r0) / 16 - 1;  // tiles of ranks behind it repeat it
   floatx4 acc[RT][8];
 #pragma unroll
   for (int m = 0; m < RT; ++m)
 #pragma unroll
     for (int n = 0; n < 8; ++n) acc[m][n] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
   const int left = C - c0 - 8 * r16;  // columns from the lane's first on
-  for (int s = p0 + 32 * wave; s < p1; s += 32 * kGradWaves) {
-    uint4 y[8];
-    float l[RT][8];
+  const bool plain = C - c0 >= kGradCols && C % 8 == 0;
+  int token[8];
+  auto tokens = [&](int s) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int at = s + 8 * q4 + i;
-      const bool in = at < p1;
-      const int64_t t = g.order[min(at, p1 - 1)];
-      y[i] = load8(Y + t * C + c0 + 8 * r16, in ? left : 0);
+    for (int i = 0; i < 8; ++i) token[i] = g.order[min(s + 8 * q4 + i, u.p1 - 1)];
+  };
+  if (u.p0 + 32 * wave < u.p1) tokens(u.p0 + 32 * wave);
+  for (int s = u.p0 + 32 * wave; s < u.p1; s += 32 * kGradWaves) {
+    uint4 y[8], lp[RT][P];
+    if (plain) {
 #pragma unroll
-      for (int m = 0; m < RT; ++m) {
-        const int r = r0 + 16 * m + r16;
-        const float v = L[t * g.rank + min(r, g.rank - 1)];
-        l[m][i] = in && r < g.rank ? v : 0.0f;
-      }
+      for (int i = 0; i < 8; ++i) y[i] = *(const uint4*)(Y + (int64_t)token[i] * C);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = load8(Y + (int64_t)token[i] * C, left);
     }
-    uint4 lp[RT][P];
 #pragma unroll
-    for (int m = 0; m < RT; ++m) {
-      uint16_t h[8][P];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        split_parts<T>(__is_same(T, _Float16) ? ldexpf(l[m][i], -up) : l[m][i], h[i]);
+    for (int m = 0; m < RT; ++m)
 #pragma unroll
       for (int p = 0; p < P; ++p)
-        lp[m][p] = make_uint4(h[0][p] | (uint32_t)h[1][p] << 16, h[2][p] | (uint32_t)h[3][p] << 16,
-                              h[4][p] | (uint32_t)h[5][p] << 16, h[6][p] | (uint32_t)h[7][p] << 16);
+        lp[m][p] = *(const uint4*)(L + (int64_t)(p * g.ranks + 16 * min(m, m_last)) * g.stride + (s - u.p0));
+    if (s + 32 * kGradWaves < u.p1) tokens(s + 32 * kGradWaves);
+    if (s + 32 > u.p1) {
+      // behind the unit's last token both sides are 0
+      const int n = u.p1 - s - 8 * q4;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i >= n) y[i] = make_uint4(0, 0, 0, 0);
+      uint32_t k[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) k[i] = 2 * i >= n ? 0u : 2 * i + 1 >= n ? 0xffffu : 0xffffffffu;
+#pragma unroll
+      for (int m = 0; m < RT; ++m)
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          lp[m][p] = make_uint4(lp[m][p].x & k[0], lp[m][p].y & k[1], lp[m][p].z & k[2], lp[m][p].w & k[3]);
     }
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
@@ -415,8 +576,7 @@ k_adapt_grad(GradArgs g) {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int n = 0; n < 8; ++n)
-          p[(16 * m + 4 * q4 + r) * CP + 8 * r16 + n] = ldexpf(acc[m][n][r], up);
+        for (int n = 0; n < 8; ++n) p[(16 * m + 4 * q4 + r) * CP + 8 * r16 + n] = acc[m][n][r];
   };
   auto add = [&](const float* p) {
 #pragma unroll
@@ -424,9 +584,7 @@ k_adapt_grad(GradArgs g) {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int n = 0; n < 8; ++n)
-          acc[m][n][r] = ldexpf(acc[m][n][r], up) + p[(16 * m + 4 * q4 + r) * CP + 8 * r16 + n];
-    up = 0;
+        for (int n = 0; n < 8; ++n) acc[m][n][r] += p[(16 * m + 4 * q4 + r) * CP + 8 * r16 + n];
   };
   if (wave >= 2) put(red + (wave - 2) * R * CP);
   __syncthreads();
@@ -440,20 +598,23 @@ k_adapt_grad(GradArgs g) {
   }
   __syncthreads();
   const int rows = min(R, g.rank - r0), cols = min(kGradCols, C - c0);
-  const bool whole = count <= g.chunk;
-  const float f = right && whole ? g.scale[a] : 1.0f;
-  const int64_t to = whole ? a : unit;
+  const bool whole = u.all <= g.chunk;
+  const float f = right && whole ? g.scale[u.a] : 1.0f;
+  const int64_t to = whole ? u.a : part_of(g, u.a) + u.piece;
+  const int* up = g.up ? g.up + (unit * 2 + right) * g.ranks + r0 : nullptr;
   if (right) {
     float* d = (whole ? g.dB : g.pB) + (to * g.O + c0) * g.rank + r0;
     for (int e = tid; e < cols * rows; e += 64 * kGradWaves) {
       const int c = e / rows, r = e - c * rows;
-      d[(int64_t)c * g.rank + r] = red[r * CP + c] * f;
+      const float v = red[r * CP + c];
+      d[(int64_t)c * g.rank + r] = (up ? ldexpf(v, up[r]) : v) * f;
     }
   } else {
     float* d = (whole ? g.dA : g.pA) + (to * g.rank + r0) * g.K + c0;
     for (int e = tid; e < rows * kGradCols; e += 64 * kGradWaves) {
       const int r = e / kGradCols, c = e % kGradCols;
-      d[(int64_t)r * g.K + c] = red[r * CP + c];
+      const float v = red[r * CP + c];
+      d[(int64_t)r * g.K + c] = up ? ldexpf(v, up[r]) : v;
     }
   }
 }
@@ -470,7 +631,7 @@ k_adapt_join(GradArgs g) {
   if (e >= na + nb) return;
   const bool right = e >= na;
   const int64_t at = right ? e - na : e, n = right ? nb : na;
-  const float* p = (right ? g.pB : g.pA) + unit_base(g, a) * n + at;
+  const float* p = (right ? g.pB : g.pA) + part_of(g, a) * n + at;
   floatx4 s = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int i = 0; i * g.chunk < count; ++i) s += *(const floatx4*)(p + i * n);
   if (right) {
@@ -484,8 +645,10 @@ k_adapt_join(GradArgs g) {
 // ------------------------------------------------------------------- plans
 struct AdaptPlan {
   bool skinny;
-  int splits, width, nparts, ldb, chunk, units;
-  size_t off_low, off_parts, off_up, off_At, off_Bt, off_order, off_start, off_pA, off_pB, bytes;
+  int mt, splits, width, nparts, ldb, ranks, chunk, units;
+  int64_t stride;
+  size_t off_low, off_v, off_parts, off_up, off_At, off_Bt, off_order, off_start, off_left, off_lup, off_pA, off_pB,
+      bytes;
 };
 static AdaptPlan adapt_plan(const W4Args& a, const W4Adapt& d, bool backward) {
   AdaptPlan p{};
@@ -502,12 +665,16 @@ static AdaptPlan adapt_plan(const W4Args& a, const W4Adapt& d, bool backward) {
     // pieces of the sum of at least 256 columns, as many as give each unit a block;
     // a kept low is written whole
     const int64_t slots = (a.N + 15) / 16 * (a.N < 16 ? a.N : 16);
-    int64_t n = kCUs / slots, most = a.K / 256;
-    n = n > 16 ? 16 : n;
+    int64_t n = 2 * kCUs / slots, most = a.K / 256;
+    n = n > 8 ? 8 : n;
     n = n > most ? most : n;
     p.splits = d.low || n < 1 ? 1 : (int)n;
     p.off_low = take(d.low ? 0 : (size_t)p.splits * a.N * d.rank * 4);
   } else {
+    const LowPlan low = low_plan(a.N, backward ? a.O : a.K, d.rank);
+    p.mt = low.mt;
+    p.splits = low.splits;
+    p.off_low = take((size_t)p.splits * a.N * d.rank * 4);
     p.nparts = a.type == kBF16 && a.y_type == kF32 ? 3 : 2;
     p.width = (p.nparts * d.rank + 31) & ~31;
     p.off_parts = take((size_t)a.N * p.width * 2);
@@ -515,7 +682,7 @@ static AdaptPlan adapt_plan(const W4Args& a, const W4Adapt& d, bool backward) {
   }
   if (backward) {
     p.ldb = (int)((a.O + 31) & ~(int64_t)31);
-    p.off_low = take((size_t)a.N * d.rank * 4);
+    p.off_v = take((size_t)a.N * d.rank * 4);
     p.off_At = take((size_t)d.count * a.K * d.rank * 2);
     p.off_Bt = take((size_t)d.count * p.ldb * d.rank * 2);
     p.off_order = take((size_t)a.N * 4);
@@ -526,11 +693,19 @@ static AdaptPlan adapt_plan(const W4Args& a, const W4Adapt& d, bool backward) {
     const int64_t tiles = (a.K + a.O + kGradCols - 1) / kGradCols * (d.rank > 64 ? 2 : 1);
     int64_t chunk = a.N * tiles / (4 * kCUs);
     if (chunk < 8 * d.rank) chunk = 8 * d.rank;
+    if (chunk > a.N) chunk = a.N;
     p.chunk = (int)((chunk + 127) & ~(int64_t)127);
     p.units = (int)(a.N / p.chunk) + d.count;
+    p.ranks = (d.rank + 15) & ~15;
+    // the adapters' tokens, each from a multiple of eight on, and what a last
+    // step of 32 reads behind them
+    p.stride = ((a.N + 7) & ~(int64_t)7) + 8 * (int64_t)d.count + 32;
+    p.off_left = take((size_t)6 * p.ranks * p.stride * 2);
+    p.off_lup = take((size_t)p.units * 2 * p.ranks * 4);
     const bool many = a.N > p.chunk;  // else no adapter has two chunks
-    p.off_pA = take(many ? (size_t)p.units * d.rank * a.K * 4 : 0);
-    p.off_pB = take(many ? (size_t)p.units * d.rank * a.O * 4 : 0);
+    const size_t parts = many ? 2 * a.N / p.chunk + 1 : 0;
+    p.off_pA = take(parts * d.rank * a.K * 4);
+    p.off_pB = take(parts * d.rank * a.O * 4);
   }
   p.bytes = at;
   return p;
@@ -547,7 +722,8 @@ static hipError_t forward(const W4Args& a, const W4Adapt& d, const AdaptPlan& p,
   l.A = (const uint16_t*)d.A;
   l.ids = d.ids;
   l.scale = d.scale;
-  l.low = d.low ? d.low : p.skinny ? (float*)(ws + p.off_low) : nullptr;
+  l.low = d.low && p.skinny ? d.low : (float*)(ws + p.off_low);
+  l.out = d.low;
   l.N = (int)a.N;
   l.K = l.lda = (int)a.K;
   l.count = d.count;
@@ -562,7 +738,7 @@ static hipError_t forward(const W4Args& a, const W4Adapt& d, const AdaptPlan& p,
   if (p.skinny) {
     ad.low = l.low;
     ad.splits = p.splits;
-    const hipError_t e = launch_low<T, true>(l, stream);
+    const hipError_t e = launch_low<T, true, true>(l, 1, stream);
     return e != hipSuccess ? e : launch_w4_skinny_adapted(a, ad, stream);
   }
   l.parts = (uint16_t*)(ws + p.off_parts);
@@ -571,7 +747,7 @@ static hipError_t forward(const W4Args& a, const W4Adapt& d, const AdaptPlan& p,
   l.nparts = ad.nparts = p.nparts;
   ad.parts = (const char*)l.parts;
   ad.up = l.up;
-  const hipError_t e = launch_low<T, false>(l, stream);
+  const hipError_t e = launch_parts<T, true>(l, p.mt, stream);
   return e != hipSuccess ? e : launch_w4_gemm_adapted(a, ad, stream);
 }
 
@@ -600,6 +776,7 @@ static hipError_t backward(const W4Args& a, const W4Adapt& d, const AdaptPlan& p
   l.ids = d.ids;
   l.scale = d.scale;
   l.low = (float*)(ws + p.off_low);
+  l.out = (float*)(ws + p.off_v);
   l.scaled = 1;
   l.parts = (uint16_t*)(ws + p.off_parts);
   l.up = a.type == kF16 ? (int*)(ws + p.off_up) : nullptr;
@@ -610,8 +787,8 @@ static hipError_t backward(const W4Args& a, const W4Adapt& d, const AdaptPlan& p
   l.rank = d.rank;
   l.width = p.width;
   l.nparts = p.nparts;
-  l.splits = 1;
-  hipError_t e = launch_low<T, false>(l, stream);
+  l.splits = p.splits;
+  hipError_t e = a.O % 32 ? launch_parts<T, false>(l, p.mt, stream) : launch_parts<T, true>(l, p.mt, stream);
   if (e != hipSuccess) return e;
   Adapters ad{};
   ad.ids = d.ids;
@@ -627,7 +804,7 @@ static hipError_t backward(const W4Args& a, const W4Adapt& d, const AdaptPlan& p
   GradArgs g{};
   g.X = (const uint16_t*)a.in1;
   g.dY = (const uint16_t*)a.in0;
-  g.v = l.low;
+  g.v = l.out;
   g.low = d.low;
   g.scale = d.scale;
   g.order = o.order;
@@ -642,6 +819,11 @@ static hipError_t backward(const W4Args& a, const W4Adapt& d, const AdaptPlan& p
   g.count = d.count;
   g.rank = d.rank;
   g.chunk = p.chunk;
+  g.ranks = p.ranks;
+  g.stride = p.stride;
+  g.left = (uint16_t*)(ws + p.off_left);
+  g.up = a.type == kF16 ? (int*)(ws + p.off_lup) : nullptr;
+  hipLaunchKernelGGL((k_adapt_left<T>), dim3(p.units, 2 * p.ranks / 16, p.chunk / 128), dim3(256), 0, stream, g);
   auto go = [&](auto* kernel, int rt, int z) {
     const int lds = 2 * 16 * rt * (kGradCols + 4) * 4;
     if (lds > 65536) {

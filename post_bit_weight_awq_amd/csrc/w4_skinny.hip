@@ -43,7 +43,7 @@ constexpr int kSkinnyLds = 160 * 1024;
 struct SkinnyPlan {
   int lds;       // bytes
   int off_ring;  // of the two stages, behind the (step, zero) pairs
-  int off_low;   // of the adapters' products, behind all
+  int off_low;   // of the adapters' products
 };
 static SkinnyPlan skinny_plan(int64_t N, int64_t K, int group, int KS, int rank = 0) {
   const int WR = 8 / KS, rows = 32 * WR, MT = (int)((N + 15) / 16);
@@ -52,9 +52,10 @@ static SkinnyPlan skinny_plan(int64_t N, int64_t K, int group, int KS, int rank 
   const int64_t ring = params + 2 * (KS * (N <= 4 ? 1024 : MT * 4096) + 8 * 2048);
   SkinnyPlan p;
   p.off_ring = (int)params;
-  const int64_t low = ring > sums ? ring : sums;
-  p.off_low = (int)low;
-  p.lds = low + 4 * N * rank > kSkinnyLds ? 0 : (int)(low + 4 * N * rank);
+  // low lies behind the sums, where the stages were
+  p.off_low = (int)sums;
+  const int64_t end = sums + 4 * N * rank;
+  p.lds = ring > kSkinnyLds || end > kSkinnyLds ? 0 : (int)(ring > end ? ring : end);
   return p;
 }
 
@@ -121,20 +122,15 @@ k_w4_skinny(const T* __restrict__ X, int M, int K, int O, const char* __restrict
       dma16((const char*)X + 256 * kb, ox[i], l + kg * XB + (FEW ? 0 : (wr + i * WR) * 1024));
   };
   load(0);
-  if constexpr (AD::on) {
-    // scale low of every token, the splits of its sum in order
-    float* const low = (float*)(smem + off_low);
-    const int all = M * ad.rank;
-    for (int e = tid; e < all; e += 512) {
-      const int id = ad.ids[e / ad.rank];
-      float s = 0.0f;
-      if (id >= 0 && id < ad.count) {
-        for (int k = 0; k < ad.splits; ++k) s += ad.low[(size_t)k * all + e];
-        s *= ad.scale[id];
-      }
-      low[e] = s;
+  __shared__ int ids[AD::on ? 64 : 1];  // a token's adapter or -1, and its scale
+  __shared__ float scales[AD::on ? 64 : 1];
+  if constexpr (AD::on)
+    if (tid < M) {
+      const int id = ad.ids[tid];
+      const bool there = id >= 0 && id < ad.count;
+      ids[tid] = there ? id : -1;
+      scales[tid] = there ? ad.scale[id] : 0.0f;
     }
-  }
   uint16_t part = 0;  // of the zeros: bits of what they have behind the point,
   _Float16 top = 0;   // and the largest magnitude
   const int di = 512 / ng, dg = 512 - di * ng;
@@ -275,8 +271,63 @@ k_w4_skinny(const T* __restrict__ X, int M, int K, int O, const char* __restrict
       for (int r = 0; r < 4; ++r)
         red[(kg * 16 * MT + 16 * m + 4 * q4 + r) * RP +
             (GATED ? u * (R / 2) + 16 * wr : 32 * wr + 16 * u) + r16] = acc[m][u][r];
+  if constexpr (AD::on) {
+    // scale low of every token, the splits of its sum in order
+    float* const low = (float*)(smem + off_low);
+    const int all = M * ad.rank;
+#pragma unroll 2
+    for (int e = tid; e < all; e += 512) {
+      const int t = e / ad.rank;
+      const bool mine = ids[t] >= 0;
+      float s = 0.0f, v[8];  // past the end the last split's, not added
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = mine ? ad.low[(size_t)min(k, ad.splits - 1) * all + e] : 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += k < ad.splits ? v[k] : 0.0f;
+      low[e] = s * scales[t];
+    }
+  }
   __syncthreads();
   constexpr int C = GATED ? R / 2 : R;
+  if constexpr (AD::on) {
+    // A wavefront per token: the block's rows of its adapter lie one behind the
+    // other, a team of lanes takes a row, eight ranks each.  (A thread per
+    // output and row: 48 tokens, 13824 -> 5120, rank 64, 31 us instead of
+    // PERF_TEAM.)
+    const float* const low = (const float*)(smem + off_low);
+    const int rb8 = ad.rank >> 3;
+    int team = 1;
+    while (team < rb8) team *= 2;
+    const int part = lane & (team - 1), first = lane / team, step = 64 / team;
+    for (int t = wave; t < M; t += 8) {
+      const int id = __builtin_amdgcn_readfirstlane(ids[t]);
+      if (id < 0) continue;
+      const char* b = ad.mat + ((int64_t)id * O + rb) * ad.rank * 2 + 16 * min(part, rb8 - 1);
+      float u[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) u[k] = part < rb8 ? low[t * ad.rank + 8 * part + k] : 0.0f;
+      for (int i0 = 0; i0 < C; i0 += 4 * step) {
+        uint4 w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = min(i0 + j * step + first, min(C, rows - rb) - 1);
+          w[j] = *(const uint4*)(b + (int64_t)i * ad.rank * 2);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float s = 0.0f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            s = fmaf(u[k], to_f32(__builtin_bit_cast(T, (uint16_t)(word_of(w[j], k >> 1) >> (16 * (k & 1))))), s);
+          s = part < rb8 ? s : 0.0f;
+          for (int k = 1; k < team; k *= 2) s += __shfl_xor(s, k);
+          const int i = i0 + j * step + first;
+          if (part == 0 && i < C) red[t * RP + i] += s;
+        }
+      }
+    }
+    __syncthreads();
+  }
   for (int e = tid; e < M * C; e += 512) {
     const int t = e / C, i = e - t * C;
     if (rb + i >= rows) continue;
@@ -293,20 +344,6 @@ k_w4_skinny(const T* __restrict__ X, int M, int K, int O, const char* __restrict
         ((T*)ep.pre)[(size_t)t * O + F + rb + i] = from_f32<T>(v);
       }
       s = (ep.act == kActSilu ? act_value<kActSilu>(s, nullptr) : act_value<kActGelu>(s, nullptr)) * v;
-    }
-    if constexpr (AD::on) {
-      const int id = ad.ids[t];
-      if (id >= 0 && id < ad.count) {
-        const float* low = (const float*)(smem + off_low) + t * ad.rank;
-        const uint4* b = (const uint4*)(ad.mat + ((int64_t)id * O + rb + i) * ad.rank * 2);
-        for (int r = 0; r < ad.rank; r += 8) {
-          const uint4 w = b[r >> 3];
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            s = fmaf(low[r + k],
-                     to_f32(__builtin_bit_cast(T, (uint16_t)(word_of(w, k >> 1) >> (16 * (k & 1))))), s);
-        }
-      }
     }
     if (!GATED && ep.y_type == kF32)
       ((float*)ep.y)[at] = s;
