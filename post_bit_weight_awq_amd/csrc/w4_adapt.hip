@@ -12,24 +12,11 @@
 //                  (k_adapt_left), the right side transposed in registers; a long
 //                  list of tokens is taken in chunks, k_adapt_join adds them in
 //                  order
-#include <type_traits>
-
 #include "w4_adapt.h"
 
 namespace awq {
 
 constexpr int kOrder = 256;
-
-// An unaligned 16-byte load of eight values, those from `left` on as 0.
-__device__ __forceinline__ uint4 load8(const uint16_t* p, int left) {
-  typedef uint16_t u16x8 __attribute__((ext_vector_type(8), aligned(2)));
-  if (left >= 8) return __builtin_bit_cast(uint4, *(const u16x8*)p);
-  uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < left) w[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
 
 // v as a sum of 16-bit values, the first the nearest.  What is not finite is the
 // first one alone.
@@ -51,118 +38,11 @@ __device__ __forceinline__ int up_of(float top) {
   return e - 15;
 }
 
-constexpr int kLowWaves = 8;
-
-struct LowArgs {
-  const uint16_t *X, *A;  // [N, K] dense; [count][rank][lda]
-  const int32_t* ids;
-  const float* scale;  // of the parts
-  float* low;          // [splits, N, rank]
-  float* out;          // [N, rank] or NULL
-  uint16_t* parts;
-  int* up;  // fp16's parts
-  int N, K, lda, count, rank, width, nparts, splits;
-  int scaled;  // out takes the scale too
-};
-
-// Tile of 16 MT tokens by 16 RT ranks (all), eight wavefronts along the sum, of
-// which block x takes a piece.  Single tokens (SLOTS): block z takes the z-th
-// adapter of its tile; else a block takes all of them one by one.  Pieces' sums
-// lie in `low` one behind the other; k_adapt_parts adds them.  FULL: K is a
-// multiple of 32, so rows are aligned and no step needs a check: a wavefront then
-// has U steps' loads in flight.
-// Bound by what a compute unit gets from L2 (about 30 bytes a ns here): high tiles
-// read A less often, pieces keep all units busy (4096 tokens, 15360 columns, rank
-// 64: 83 us with 16 tokens and whole sums, PERF_LOW with 64 and quarters).
-template <typename T, int MT, int RT, int U, bool SLOTS, bool FULL>
+template <typename T, int MT, int RT, int U, bool FULL>
 __global__ void __launch_bounds__(64 * kLowWaves)
 k_adapt_low(LowArgs a) {
-  constexpr int R = 16 * RT, RP = R + 1, M = 16 * MT, W = kLowWaves;
-  extern __shared__ float red[];  // [wavefront][16][RP]
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r16 = lane & 15, q4 = lane >> 4;
-  const int t0 = blockIdx.y * M, split = blockIdx.x;
-  int id = -1;
-  if (lane < M && t0 + lane < a.N) id = a.ids[t0 + lane];
-  if (id >= a.count) id = -1;
-  uint64_t wait = __ballot(id >= 0);
-  float* const low = a.low + (size_t)split * a.N * a.rank;
-  // tokens without an adapter have zeros
-  if (!SLOTS || blockIdx.z == 0)
-    for (int e = tid; e < M * a.rank; e += 64 * W) {
-      const int t = e / a.rank;
-      if (t0 + t < a.N && !((wait >> t) & 1)) low[(size_t)t0 * a.rank + e] = 0.0f;
-    }
-  if (SLOTS) {
-    for (int z = blockIdx.z; z > 0 && wait; --z) {
-      const int one = __builtin_amdgcn_readlane(id, __builtin_ctzll(wait));
-      wait &= ~__ballot(id == one);
-    }
-    if (!wait) return;
-  }
-  const int steps = (a.K + 31) >> 5;
-  const int s0 = (int)((int64_t)steps * split / a.splits), s1 = (int)((int64_t)steps * (split + 1) / a.splits);
-  const uint16_t* x[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) x[m] = a.X + (int64_t)min(t0 + 16 * m + r16, a.N - 1) * a.K + 8 * q4;
-  while (wait) {
-    const int one = __builtin_amdgcn_readlane(id, __builtin_ctzll(wait));
-    const uint64_t mine = __ballot(id == one);
-    wait = SLOTS ? 0 : wait & ~mine;
-    floatx4 acc[MT][RT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int n = 0; n < RT; ++n) acc[m][n] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-    const uint16_t* w[RT];
-#pragma unroll
-    for (int n = 0; n < RT; ++n)
-      w[n] = a.A + ((int64_t)one * a.rank + min(16 * n + r16, a.rank - 1)) * a.lda + 8 * q4;
-    auto take = [&](int s, auto count) {
-      constexpr int C = decltype(count)::value;
-      uint4 xv[C][MT], wv[C][RT];
-#pragma unroll
-      for (int h = 0; h < C; ++h) {
-        const int c = 32 * (s + h), left = a.K - c - 8 * q4;
-#pragma unroll
-        for (int m = 0; m < MT; ++m) xv[h][m] = FULL ? *(const uint4*)(x[m] + c) : load8(x[m] + c, left);
-#pragma unroll
-        for (int n = 0; n < RT; ++n) wv[h][n] = FULL ? *(const uint4*)(w[n] + c) : load8(w[n] + c, left);
-      }
-#pragma unroll
-      for (int h = 0; h < C; ++h)
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int n = 0; n < RT; ++n) acc[m][n] = mfma16<T>(xv[h][m], wv[h][n], acc[m][n]);
-    };
-    // U neighbouring steps of 32 columns at a time
-    for (int s = s0 + U * wave; s < s1; s += U * W) {
-      if (s + U <= s1)
-        take(s, std::integral_constant<int, U>{});
-      else
-        for (int h = s; h < s1; ++h) take(h, std::integral_constant<int, 1>{});
-    }
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      if (m > 0) __syncthreads();
-#pragma unroll
-      for (int n = 0; n < RT; ++n)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) red[(wave * 16 + 4 * q4 + r) * RP + 16 * n + r16] = acc[m][n][r];
-      __syncthreads();
-      for (int e = tid; e < 16 * a.rank; e += 64 * W) {
-        const int t = e / a.rank, r = e - t * a.rank;
-        if (!((mine >> (16 * m + t)) & 1)) continue;
-        float v = 0.0f;
-#pragma unroll
-        for (int i = 0; i < W; ++i) v += red[(i * 16 + t) * RP + r];
-        low[(size_t)(t0 + 16 * m) * a.rank + e] = v;
-      }
-    }
-    if (!SLOTS) __syncthreads();
-  }
+  extern __shared__ float red[];  // [wavefront][16][16 RT + 1]
+  sum_low<T, MT, RT, U, false, FULL>(a, red, blockIdx.x, blockIdx.y, 0, 0);
 }
 
 // A wavefront per token: the pieces' sums in order, as `out` (times the scale
@@ -233,8 +113,9 @@ static LowPlan low_plan(int64_t N, int64_t K, int rank) {
   return p;
 }
 
-template <typename T, bool SLOTS, bool FULL>
+template <typename T, bool FULL>
 static hipError_t launch_low(const LowArgs& a, int mt, hipStream_t stream) {
+  constexpr int U = FULL ? 2 : 1;
   const int rt = (a.rank + 15) / 16;
   auto go = [&](auto* kernel, int r) {
     const int lds = kLowWaves * 16 * (16 * r + 1) * 4;
@@ -243,37 +124,107 @@ static hipError_t launch_low(const LowArgs& a, int mt, hipStream_t stream) {
           hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
       if (e != hipSuccess) return e;
     }
-    const dim3 grid(a.splits, (unsigned)((a.N + 16 * mt - 1) / (16 * mt)),
-                    SLOTS ? (unsigned)(a.N < 16 ? a.N : 16) : 1);
+    const dim3 grid(a.splits, (unsigned)((a.N + 16 * mt - 1) / (16 * mt)));
     hipLaunchKernelGGL(kernel, grid, dim3(64 * kLowWaves), lds, stream, a);
     return hipGetLastError();
   };
-  if constexpr (!SLOTS) {
-    constexpr int U = FULL ? 2 : 1;
-    if (mt == 4) {
-      if (rt == 1) return go(&k_adapt_low<T, 4, 1, U, false, FULL>, 1);
-      if (rt == 2) return go(&k_adapt_low<T, 4, 2, U, false, FULL>, 2);
-      return go(&k_adapt_low<T, 4, 4, U, false, FULL>, 4);
-    }
-    if (mt == 2) {
-      if (rt == 1) return go(&k_adapt_low<T, 2, 1, U, false, FULL>, 1);
-      if (rt == 2) return go(&k_adapt_low<T, 2, 2, U, false, FULL>, 2);
-      if (rt <= 4) return go(&k_adapt_low<T, 2, 4, U, false, FULL>, 4);
-      return go(&k_adapt_low<T, 2, 8, 1, false, FULL>, 8);
-    }
+  if (mt == 4) {
+    if (rt == 1) return go(&k_adapt_low<T, 4, 1, U, FULL>, 1);
+    if (rt == 2) return go(&k_adapt_low<T, 4, 2, U, FULL>, 2);
+    return go(&k_adapt_low<T, 4, 4, U, FULL>, 4);
   }
-  constexpr int U = FULL ? 2 : 1;
-  if (rt == 1) return go(&k_adapt_low<T, 1, 1, U, SLOTS, FULL>, 1);
-  if (rt == 2) return go(&k_adapt_low<T, 1, 2, U, SLOTS, FULL>, 2);
-  if (rt <= 4) return go(&k_adapt_low<T, 1, 4, U, SLOTS, FULL>, 4);
-  return go(&k_adapt_low<T, 1, 8, U, SLOTS, FULL>, 8);
+  if (mt == 2) {
+    if (rt == 1) return go(&k_adapt_low<T, 2, 1, U, FULL>, 1);
+    if (rt == 2) return go(&k_adapt_low<T, 2, 2, U, FULL>, 2);
+    if (rt <= 4) return go(&k_adapt_low<T, 2, 4, U, FULL>, 4);
+    return go(&k_adapt_low<T, 2, 8, 1, FULL>, 8);
+  }
+  if (rt == 1) return go(&k_adapt_low<T, 1, 1, U, FULL>, 1);
+  if (rt == 2) return go(&k_adapt_low<T, 1, 2, U, FULL>, 2);
+  if (rt <= 4) return go(&k_adapt_low<T, 1, 4, U, FULL>, 4);
+  return go(&k_adapt_low<T, 1, 8, U, FULL>, 8);
 }
 template <typename T, bool FULL>
 static hipError_t launch_parts(const LowArgs& a, int mt, hipStream_t stream) {
-  const hipError_t e = launch_low<T, false, FULL>(a, mt, stream);
+  const hipError_t e = launch_low<T, FULL>(a, mt, stream);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((k_adapt_parts<T>), dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, stream, a);
   return hipGetLastError();
+}
+
+// Single tokens: y = round(base + scale low B[a]^T), base the streaming product's
+// sums in fp32.  A block takes one token, a wavefront 64 outputs, whose rows of
+// B[a] lie one behind the other: a team of lanes takes a row, eight ranks each.
+// Bound by latency and the read of B.  In the streaming kernel's epilogue, whose
+// few blocks have to read all of it, the second term cost 48 tokens, 13824 ->
+// 5120, 25 adapters of rank 64, 28 us; here it takes 7.6.
+struct AddArgs {
+  const float *base, *low, *scale;  // low: [splits, N, rank]
+  const int32_t* ids;
+  const char* mat;  // [count, O, rank]
+  void* y;
+  float* out;  // low, kept, or NULL
+  int N, O, count, rank, splits, y_type;
+};
+template <typename T>
+__global__ void __launch_bounds__(256)
+k_adapt_add(AddArgs a) {
+  __shared__ float low[128], sums[4][64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int t = blockIdx.y, o0 = 64 * (4 * blockIdx.x + wave);
+  int id = a.ids[t];
+  if (id >= a.count) id = -1;
+  const int o = o0 + lane;
+  float v = o < a.O ? a.base[(size_t)t * a.O + o] : 0.0f;
+  if (tid < a.rank) {
+    float s = 0.0f;
+    if (id >= 0) {
+      float x[8];  // past the end the last piece's, not added
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = a.low[((size_t)min(k, a.splits - 1) * a.N + t) * a.rank + tid];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += k < a.splits ? x[k] : 0.0f;
+    }
+    if (a.out && blockIdx.x == 0) a.out[(size_t)t * a.rank + tid] = s;
+    low[tid] = id >= 0 ? s * a.scale[id] : 0.0f;
+  }
+  __syncthreads();
+  if (o0 >= a.O) return;
+  if (id >= 0) {
+    const int rb = a.rank >> 3, rows = min(64, a.O - o0);
+    int team = 1;
+    while (team < rb) team *= 2;
+    const int part = lane & (team - 1), first = lane / team, step = 64 / team;
+    const char* b = a.mat + ((int64_t)id * a.O + o0) * a.rank * 2 + 16 * min(part, rb - 1);
+    float u[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) u[k] = part < rb ? low[8 * part + k] : 0.0f;
+    for (int i0 = 0; i0 < 64; i0 += 4 * step) {
+      uint4 w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = *(const uint4*)(b + (int64_t)min(i0 + j * step + first, rows - 1) * a.rank * 2);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = i0 + j * step + first;
+        float s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          s = fmaf(u[k], to_f32(__builtin_bit_cast(T, (uint16_t)(word_of(w[j], k >> 1) >> (16 * (k & 1))))), s);
+        s = part < rb ? s : 0.0f;
+        for (int k = 1; k < team; k *= 2) s += __shfl_xor(s, k);
+        if (part == 0 && i < 64) sums[wave][i] = s;
+      }
+    }
+    // the wavefront's own writes
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    v += sums[wave][lane];
+  }
+  if (o >= a.O) return;
+  if (a.y_type == kF32)
+    ((float*)a.y)[(size_t)t * a.O + o] = v;
+  else
+    ((T*)a.y)[(size_t)t * a.O + o] = from_f32<T>(v);
 }
 
 // ------------------------------------------------------------ backward pass
@@ -647,14 +598,13 @@ struct AdaptPlan {
   bool skinny;
   int mt, splits, width, nparts, ldb, ranks, chunk, units;
   int64_t stride;
-  size_t off_low, off_v, off_parts, off_up, off_At, off_Bt, off_order, off_start, off_left, off_lup, off_pA, off_pB,
+  size_t off_low, off_base, off_v, off_parts, off_up, off_At, off_Bt, off_order, off_start, off_left, off_lup, off_pA, off_pB,
       bytes;
 };
 static AdaptPlan adapt_plan(const W4Args& a, const W4Adapt& d, bool backward) {
   AdaptPlan p{};
   size_t at = backward ? w4_input_grad_workspace(a) : w4_workspace(kOpLinear, a);
-  p.skinny = !backward && w4_skinny_fits_adapted(a, d.rank);
-  if (!backward && !p.skinny) at = w4_gemm_workspace(kOpLinear, a);
+  p.skinny = !backward && w4_skinny_fits(a);
   auto take = [&](size_t n) {
     const size_t r = align256(at);
     at = r + n;
@@ -662,14 +612,15 @@ static AdaptPlan adapt_plan(const W4Args& a, const W4Adapt& d, bool backward) {
   };
   p.splits = 1;
   if (p.skinny) {
-    // pieces of the sum of at least 256 columns, as many as give each unit a block;
-    // a kept low is written whole
-    const int64_t slots = (a.N + 15) / 16 * (a.N < 16 ? a.N : 16);
-    int64_t n = 2 * kCUs / slots, most = a.K / 256;
+    // pieces of the sum of at least 256 columns, until each unit has a block of
+    // them (they run beside the product's own)
+    const int64_t blocks = (a.N + 15) / 16 * (a.N < 16 ? a.N : 16) * ((d.rank + 15) / 16);
+    int64_t n = kCUs / blocks, most = a.K / 256;
     n = n > 8 ? 8 : n;
     n = n > most ? most : n;
-    p.splits = d.low || n < 1 ? 1 : (int)n;
-    p.off_low = take(d.low ? 0 : (size_t)p.splits * a.N * d.rank * 4);
+    p.splits = n < 1 ? 1 : (int)n;
+    p.off_low = take((size_t)p.splits * a.N * d.rank * 4);
+    p.off_base = take(a.y_type == kF32 ? 0 : (size_t)a.N * a.O * 4);
   } else {
     const LowPlan low = low_plan(a.N, backward ? a.O : a.K, d.rank);
     p.mt = low.mt;
@@ -722,25 +673,31 @@ static hipError_t forward(const W4Args& a, const W4Adapt& d, const AdaptPlan& p,
   l.A = (const uint16_t*)d.A;
   l.ids = d.ids;
   l.scale = d.scale;
-  l.low = d.low && p.skinny ? d.low : (float*)(ws + p.off_low);
+  l.low = (float*)(ws + p.off_low);
   l.out = d.low;
   l.N = (int)a.N;
   l.K = l.lda = (int)a.K;
   l.count = d.count;
   l.rank = d.rank;
   l.splits = p.splits;
+  if (p.skinny) {
+    LowBlocks low{l, 0, (int)((a.N + 15) / 16), (int)(a.N < 16 ? a.N : 16), (d.rank + 15) / 16};
+    W4Args b = a;
+    b.y_type = kF32;
+    if (a.y_type != kF32) b.out0 = ws + p.off_base;
+    const hipError_t e = launch_w4_skinny_low(b, low, stream);
+    if (e != hipSuccess) return e;
+    const AddArgs add{(const float*)b.out0, l.low, d.scale, d.ids, (const char*)d.B, a.out0, d.low,
+                      (int)a.N, (int)a.O, d.count, d.rank, p.splits, a.y_type};
+    hipLaunchKernelGGL((k_adapt_add<T>), dim3((unsigned)((a.O + 255) / 256), (unsigned)a.N), dim3(256), 0,
+                       stream, add);
+    return hipGetLastError();
+  }
   Adapters ad{};
   ad.ids = d.ids;
   ad.mat = (const char*)d.B;
-  ad.scale = d.scale;
   ad.count = d.count;
   ad.rank = d.rank;
-  if (p.skinny) {
-    ad.low = l.low;
-    ad.splits = p.splits;
-    const hipError_t e = launch_low<T, true, true>(l, 1, stream);
-    return e != hipSuccess ? e : launch_w4_skinny_adapted(a, ad, stream);
-  }
   l.parts = (uint16_t*)(ws + p.off_parts);
   l.up = a.type == kF16 ? (int*)(ws + p.off_up) : nullptr;
   l.width = ad.width = p.width;

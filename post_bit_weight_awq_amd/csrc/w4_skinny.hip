@@ -43,28 +43,24 @@ constexpr int kSkinnyLds = 160 * 1024;
 struct SkinnyPlan {
   int lds;       // bytes
   int off_ring;  // of the two stages, behind the (step, zero) pairs
-  int off_low;   // of the adapters' products
 };
-static SkinnyPlan skinny_plan(int64_t N, int64_t K, int group, int KS, int rank = 0) {
+static SkinnyPlan skinny_plan(int64_t N, int64_t K, int group, int KS) {
   const int WR = 8 / KS, rows = 32 * WR, MT = (int)((N + 15) / 16);
   const int64_t params = ((int64_t)rows * (K / group) * 4 + 1023) & ~1023;
   const int64_t sums = (int64_t)KS * 16 * MT * (rows + 1) * 4;
   const int64_t ring = params + 2 * (KS * (N <= 4 ? 1024 : MT * 4096) + 8 * 2048);
   SkinnyPlan p;
   p.off_ring = (int)params;
-  // low lies behind the sums, where the stages were
-  p.off_low = (int)sums;
-  const int64_t end = sums + 4 * N * rank;
-  p.lds = ring > kSkinnyLds || end > kSkinnyLds ? 0 : (int)(ring > end ? ring : end);
+  p.lds = ring > kSkinnyLds ? 0 : (int)(ring > sums ? ring : sums);
   return p;
 }
 
-// AD: Adapters, whose term each output adds in fp32, or none.
+// AD: LowBlocks, whose sums further blocks form beside the product, or none.
 template <typename T, int GROUP, bool GATED, int MT, int KS, bool FEW, typename AD>
 __global__ void __launch_bounds__(512, 2)
 k_w4_skinny(const T* __restrict__ X, int M, int K, int O, const char* __restrict__ qw,
             const _Float16* __restrict__ step16, const _Float16* __restrict__ zero16, Epilogue ep,
-            int off_ring, int off_low, AD ad) {
+            int off_ring, AD ad) {
   constexpr bool BF = !__is_same(T, _Float16);
   constexpr int WR = 8 / KS, R = 32 * WR;  // packed rows per block
   constexpr int GPB = 128 / GROUP;         // groups per block of 128 columns
@@ -76,6 +72,11 @@ k_w4_skinny(const T* __restrict__ X, int M, int K, int O, const char* __restrict
   // which every wavefront of the group issues
   constexpr int XW = FEW ? 1 : 4 * MT / WR;
   extern __shared__ __attribute__((aligned(16))) char smem[];
+  if constexpr (AD::on)
+    if ((int)blockIdx.x >= ad.first) {
+      ad.template run<T>(blockIdx.x - ad.first, (float*)smem);
+      return;
+    }
   uint32_t* const pairs = (uint32_t*)smem;  // [ng][R] (step, zero)
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -122,15 +123,6 @@ k_w4_skinny(const T* __restrict__ X, int M, int K, int O, const char* __restrict
       dma16((const char*)X + 256 * kb, ox[i], l + kg * XB + (FEW ? 0 : (wr + i * WR) * 1024));
   };
   load(0);
-  __shared__ int ids[AD::on ? 64 : 1];  // a token's adapter or -1, and its scale
-  __shared__ float scales[AD::on ? 64 : 1];
-  if constexpr (AD::on)
-    if (tid < M) {
-      const int id = ad.ids[tid];
-      const bool there = id >= 0 && id < ad.count;
-      ids[tid] = there ? id : -1;
-      scales[tid] = there ? ad.scale[id] : 0.0f;
-    }
   uint16_t part = 0;  // of the zeros: bits of what they have behind the point,
   _Float16 top = 0;   // and the largest magnitude
   const int di = 512 / ng, dg = 512 - di * ng;
@@ -271,63 +263,8 @@ k_w4_skinny(const T* __restrict__ X, int M, int K, int O, const char* __restrict
       for (int r = 0; r < 4; ++r)
         red[(kg * 16 * MT + 16 * m + 4 * q4 + r) * RP +
             (GATED ? u * (R / 2) + 16 * wr : 32 * wr + 16 * u) + r16] = acc[m][u][r];
-  if constexpr (AD::on) {
-    // scale low of every token, the splits of its sum in order
-    float* const low = (float*)(smem + off_low);
-    const int all = M * ad.rank;
-#pragma unroll 2
-    for (int e = tid; e < all; e += 512) {
-      const int t = e / ad.rank;
-      const bool mine = ids[t] >= 0;
-      float s = 0.0f, v[8];  // past the end the last split's, not added
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = mine ? ad.low[(size_t)min(k, ad.splits - 1) * all + e] : 0.0f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) s += k < ad.splits ? v[k] : 0.0f;
-      low[e] = s * scales[t];
-    }
-  }
   __syncthreads();
   constexpr int C = GATED ? R / 2 : R;
-  if constexpr (AD::on) {
-    // A wavefront per token: the block's rows of its adapter lie one behind the
-    // other, a team of lanes takes a row, eight ranks each.  (A thread per
-    // output and row: 48 tokens, 13824 -> 5120, rank 64, 31 us instead of
-    // PERF_TEAM.)
-    const float* const low = (const float*)(smem + off_low);
-    const int rb8 = ad.rank >> 3;
-    int team = 1;
-    while (team < rb8) team *= 2;
-    const int part = lane & (team - 1), first = lane / team, step = 64 / team;
-    for (int t = wave; t < M; t += 8) {
-      const int id = __builtin_amdgcn_readfirstlane(ids[t]);
-      if (id < 0) continue;
-      const char* b = ad.mat + ((int64_t)id * O + rb) * ad.rank * 2 + 16 * min(part, rb8 - 1);
-      float u[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) u[k] = part < rb8 ? low[t * ad.rank + 8 * part + k] : 0.0f;
-      for (int i0 = 0; i0 < C; i0 += 4 * step) {
-        uint4 w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int i = min(i0 + j * step + first, min(C, rows - rb) - 1);
-          w[j] = *(const uint4*)(b + (int64_t)i * ad.rank * 2);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float s = 0.0f;
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            s = fmaf(u[k], to_f32(__builtin_bit_cast(T, (uint16_t)(word_of(w[j], k >> 1) >> (16 * (k & 1))))), s);
-          s = part < rb8 ? s : 0.0f;
-          for (int k = 1; k < team; k *= 2) s += __shfl_xor(s, k);
-          const int i = i0 + j * step + first;
-          if (part == 0 && i < C) red[t * RP + i] += s;
-        }
-      }
-    }
-    __syncthreads();
-  }
   for (int e = tid; e < M * C; e += 512) {
     const int t = e / C, i = e - t * C;
     if (rb + i >= rows) continue;
@@ -352,12 +289,9 @@ k_w4_skinny(const T* __restrict__ X, int M, int K, int O, const char* __restrict
   }
 }
 
-inline int rank_of(const NoAdapters&) { return 0; }
-inline int rank_of(const Adapters& ad) { return ad.rank; }
-
 template <typename T, int GROUP, bool GATED, int MT, int KS, bool FEW, typename AD>
-static hipError_t launch(const W4Args& a, const AD& ad, hipStream_t stream) {
-  const SkinnyPlan p = skinny_plan(a.N, a.K, a.group, KS, rank_of(ad));
+static hipError_t launch(const W4Args& a, AD ad, hipStream_t stream) {
+  const SkinnyPlan p = skinny_plan(a.N, a.K, a.group, KS);
   const int per = GATED ? 16 * (8 / KS) : 32 * (8 / KS);
   const int64_t outs = GATED ? a.O / 2 : a.O;
   auto* kernel = &k_w4_skinny<T, GROUP, GATED, MT, KS, FEW, AD>;
@@ -367,9 +301,14 @@ static hipError_t launch(const W4Args& a, const AD& ad, hipStream_t stream) {
     if (e != hipSuccess) return e;
   }
   const Epilogue ep{nullptr, a.out0, a.out1, (int)a.N, (int)a.O, a.y_type, a.type, a.act};
-  hipLaunchKernelGGL(kernel, dim3((unsigned)((outs + per - 1) / per)), dim3(512), p.lds, stream,
+  unsigned blocks = (unsigned)((outs + per - 1) / per);
+  if constexpr (AD::on) {
+    ad.first = (int)blocks;
+    blocks += (unsigned)ad.blocks();
+  }
+  hipLaunchKernelGGL(kernel, dim3(blocks), dim3(512), p.lds, stream,
                      (const T*)a.in0, (int)a.N, (int)a.K, (int)a.O, (const char*)a.qweight,
-                     (const _Float16*)a.step16, (const _Float16*)a.zero16, ep, p.off_ring, p.off_low, ad);
+                     (const _Float16*)a.step16, (const _Float16*)a.zero16, ep, p.off_ring, ad);
   return hipGetLastError();
 }
 
@@ -380,8 +319,8 @@ static hipError_t launch(const W4Args& a, const AD& ad, hipStream_t stream) {
 // 5120 -> 15360 22.2 / 13.8 / 14.7, 16 tokens 5120 -> 5120 21.2 / 12.4 / 8.0,
 // gated 5120 -> 2 x 13824 29.2 / 24.5 / 36.0; 32 tokens, the same, 31.8 / 37.6,
 // 48 tokens 5120 -> 15360 32.5 / 22.2, gated 42.8 / 50.4.
-static int skinny_ks(const W4Args& a, int rank = 0) {
-  auto fits = [&](int ks) { return skinny_plan(a.N, a.K, a.group, ks, rank).lds > 0; };
+static int skinny_ks(const W4Args& a) {
+  auto fits = [&](int ks) { return skinny_plan(a.N, a.K, a.group, ks).lds > 0; };
   if (a.N > 64) return 0;
   int ks = 8;
   if (a.N > 16)
@@ -405,7 +344,7 @@ static int skinny_ks(const W4Args& a, int rank = 0) {
 // with 17 to 48 tokens and two with more.
 template <typename T, int GROUP, bool GATED, int MT, bool FEW, typename AD>
 static hipError_t by_ks(const W4Args& a, const AD& ad, hipStream_t stream) {
-  const int ks = skinny_ks(a, rank_of(ad));
+  const int ks = skinny_ks(a);
   if constexpr (MT == 1)
     if (ks == 8) return launch<T, GROUP, GATED, MT, 8, FEW>(a, ad, stream);
   if constexpr (!FEW && MT <= 3)
@@ -443,16 +382,14 @@ hipError_t launch_w4_skinny(W4Op op, const W4Args& a, hipStream_t stream) {
   return by_op<__bf16, 32>(op, a, stream);
 }
 
-bool w4_skinny_fits_adapted(const W4Args& a, int rank) { return skinny_ks(a, rank) != 0; }
-
 template <typename T>
-static hipError_t adapted(const W4Args& a, const Adapters& ad, hipStream_t stream) {
-  if (a.group == 128) return by_tokens<T, 128, false>(a, ad, stream);
-  if (a.group == 64) return by_tokens<T, 64, false>(a, ad, stream);
-  return by_tokens<T, 32, false>(a, ad, stream);
+static hipError_t with_low(const W4Args& a, const LowBlocks& low, hipStream_t stream) {
+  if (a.group == 128) return by_tokens<T, 128, false>(a, low, stream);
+  if (a.group == 64) return by_tokens<T, 64, false>(a, low, stream);
+  return by_tokens<T, 32, false>(a, low, stream);
 }
-hipError_t launch_w4_skinny_adapted(const W4Args& a, const Adapters& ad, hipStream_t stream) {
-  return a.type == kF16 ? adapted<_Float16>(a, ad, stream) : adapted<__bf16>(a, ad, stream);
+hipError_t launch_w4_skinny_low(const W4Args& a, const LowBlocks& low, hipStream_t stream) {
+  return a.type == kF16 ? with_low<_Float16>(a, low, stream) : with_low<__bf16>(a, low, stream);
 }
 
 }  // namespace awq
