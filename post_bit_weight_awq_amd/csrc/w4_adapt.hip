@@ -424,148 +424,156 @@ k_adapt_left(GradArgs g) {
   }
   uint16_t* d = g.left + ((int64_t)side * P * g.ranks + r0 + r) * g.stride + left_place(g, u);
   const int n = u.p1 - u.p0;
-  for (int b = 128 * blockIdx.z; b < 128 * (int)blockIdx.z + 128; b += 64) {
-    const floatx4 v = load(b + ti);
-    __syncthreads();
+  const int b = 64 * blockIdx.z;
+  const floatx4 v = load(b + ti);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) tile[tr + i][ti] = v[i];
-    __syncthreads();
-    uint16_t h[4][P];
+  for (int i = 0; i < 4; ++i) tile[tr + i][ti] = v[i];
+  __syncthreads();
+  uint16_t h[4][P];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) split_parts<T>(ldexpf(tile[r][i4 + i], -e), h[i]);
-    // up to seven places behind the last token are this adapter's too
-    if (b + i4 < n)
+  for (int i = 0; i < 4; ++i) split_parts<T>(ldexpf(tile[r][i4 + i], -e), h[i]);
+  // up to seven places behind the last token are this adapter's too
+  if (b + i4 < n)
 #pragma unroll
-      for (int p = 0; p < P; ++p)
-        *(uint2*)(d + (int64_t)p * g.ranks * g.stride + b + i4) =
-            make_uint2(h[0][p] | (uint32_t)h[1][p] << 16, h[2][p] | (uint32_t)h[3][p] << 16);
-  }
+    for (int p = 0; p < P; ++p)
+      *(uint2*)(d + (int64_t)p * g.ranks * g.stride + b + i4) =
+          make_uint2(h[0][p] | (uint32_t)h[1][p] << 16, h[2][p] | (uint32_t)h[3][p] << 16);
 }
 
 constexpr int kGradWaves = 4, kGradCols = 128;
 
-// 16 RT ranks from 64 z on by 128 columns of X, then of dY; each wavefront takes
-// every fourth 32 tokens of the unit.
+// 16 RT ranks from 64 z on by 4 x 128 columns of X, then of dY, all tokens of a
+// unit, 32 at a time.  A wavefront takes 128 columns; the left operands' fragments
+// come through LDS, each wavefront brings a quarter of them by direct loads: a
+// compute unit gets about 30 bytes a ns from L2, and read by each wavefront they
+// were 60 % of that (4096 tokens, 5120 and 15360 columns, rank 64: 92 us instead of
+// 72; with the tokens divided among the wavefronts and their sums added
+// through LDS, 95).  The next step's operands are on the way while one is used.
 template <typename T, int RT>
 __global__ void __launch_bounds__(64 * kGradWaves, 2)
 k_adapt_grad(GradArgs g) {
-  constexpr int R = 16 * RT, P = kLeftParts<T>, CP = kGradCols + 4;
-  extern __shared__ float red[];  // [2][R][CP]
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  constexpr int P = kLeftParts<T>, F = RT * P;
+  __shared__ __attribute__((aligned(16))) char smem[2 * F * 1024];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, q4 = lane >> 4;
   const int unit = blockIdx.y, r0 = 64 * blockIdx.z;
   GradUnit u;
   if (!grad_unit(g, unit, &u)) return;
-  const int ka = g.K / kGradCols;
-  const bool right = (int)blockIdx.x >= ka;  // dB
-  const int C = right ? g.O : g.K, c0 = kGradCols * (right ? blockIdx.x - ka : blockIdx.x);
-  const uint16_t* Y = (right ? g.dY : g.X) + c0 + 8 * r16;
-  const uint16_t* L = g.left + ((int64_t)right * P * g.ranks + r0 + r16) * g.stride + left_place(g, u) + 8 * q4;
+  const int ba = (g.K / kGradCols + kGradWaves - 1) / kGradWaves;
+  const bool right = (int)blockIdx.x >= ba;  // dB
+  const int C = right ? g.O : g.K;
+  const int c0 = kGradCols * (kGradWaves * (blockIdx.x - (right ? ba : 0)) + wave);
+  const bool live = c0 < C;  // else it only brings its fragments
+  const uint16_t* Y = (right ? g.dY : g.X) + (live ? c0 + 8 * r16 : 0);
+  const char* L = (const char*)(g.left + ((int64_t)right * P * g.ranks + r0) * g.stride + left_place(g, u));
+  const uint32_t at = (uint32_t)(r16 * g.stride * 2) + 16 * q4;
   const int m_last = (g.ranks - r0) / 16 - 1;  // tiles of ranks behind it repeat it
   floatx4 acc[RT][8];
 #pragma unroll
   for (int m = 0; m < RT; ++m)
 #pragma unroll
     for (int n = 0; n < 8; ++n) acc[m][n] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-  const int left = C - c0 - 8 * r16;  // columns from the lane's first on
-  const bool plain = C - c0 >= kGradCols && C % 8 == 0;
+  const int left = live ? C - c0 - 8 * r16 : 0;  // columns from the lane's first on
+  const bool plain = live && C - c0 >= kGradCols && C % 8 == 0;
   int token[8];
   auto tokens = [&](int s) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) token[i] = g.order[min(s + 8 * q4 + i, u.p1 - 1)];
   };
-  if (u.p0 + 32 * wave < u.p1) tokens(u.p0 + 32 * wave);
-  for (int s = u.p0 + 32 * wave; s < u.p1; s += 32 * kGradWaves) {
-    uint4 y[8], lp[RT][P];
+  uint4 y[8], yn[8];
+  const uint32_t lds = (uint32_t)(uintptr_t)smem;
+  auto request = [&](int s, int stage) {
+    // fragment f = m P + p
+#pragma unroll
+    for (int f = 0; f < F; f += kGradWaves)
+      if (f + wave < F) {
+        const int m = (f + wave) / P, p = (f + wave) % P;
+        dma16(L + ((int64_t)(p * g.ranks + 16 * min(m, m_last)) * g.stride + (s - u.p0)) * 2, at,
+              lds + stage * F * 1024 + (f + wave) * 1024);
+      }
     if (plain) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = *(const uint4*)(Y + (int64_t)token[i] * C);
+      for (int i = 0; i < 8; ++i) yn[i] = *(const uint4*)(Y + (int64_t)token[i] * C);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = load8(Y + (int64_t)token[i] * C, left);
+      for (int i = 0; i < 8; ++i) yn[i] = load8(Y + (int64_t)token[i] * C, left);
     }
+  };
+  tokens(u.p0);
+  request(u.p0, 0);
+  if (u.p0 + 32 < u.p1) tokens(u.p0 + 32);
+  int stage = 0;
+  for (int s = u.p0; s < u.p1; s += 32) {
+    // this step's fragments have landed, and nobody reads the other stage
+    wait_vm<0>();
+    __syncthreads();
 #pragma unroll
-    for (int m = 0; m < RT; ++m)
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-        lp[m][p] = *(const uint4*)(L + (int64_t)(p * g.ranks + 16 * min(m, m_last)) * g.stride + (s - u.p0));
-    if (s + 32 * kGradWaves < u.p1) tokens(s + 32 * kGradWaves);
-    if (s + 32 > u.p1) {
-      // behind the unit's last token both sides are 0
-      const int n = u.p1 - s - 8 * q4;
+    for (int i = 0; i < 8; ++i) y[i] = yn[i];
+    if (s + 32 < u.p1) request(s + 32, stage ^ 1);
+    if (s + 64 < u.p1) tokens(s + 64);
+    const char* st = smem + stage * F * 1024 + 16 * lane;
+    // behind the unit's last token both sides are 0
+    const int n_in = u.p1 - s - 8 * q4;
+    const bool edge = s + 32 > u.p1;
+    if (edge)
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (i >= n) y[i] = make_uint4(0, 0, 0, 0);
-      uint32_t k[4];
+        if (i >= n_in) y[i] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) k[i] = 2 * i >= n ? 0u : 2 * i + 1 >= n ? 0xffffu : 0xffffffffu;
+    for (int m = 0; m < RT; ++m) {
+      uint4 lp[P];
 #pragma unroll
-      for (int m = 0; m < RT; ++m)
+      for (int p = 0; p < P; ++p) {
+        lp[p] = *(const uint4*)(st + (m * P + p) * 1024);
+        if (edge) {
+          lp[p].x &= 0 >= n_in ? 0u : 1 >= n_in ? 0xffffu : 0xffffffffu;
+          lp[p].y &= 2 >= n_in ? 0u : 3 >= n_in ? 0xffffu : 0xffffffffu;
+          lp[p].z &= 4 >= n_in ? 0u : 5 >= n_in ? 0xffffu : 0xffffffffu;
+          lp[p].w &= 6 >= n_in ? 0u : 7 >= n_in ? 0xffffu : 0xffffffffu;
+        }
+      }
 #pragma unroll
-        for (int p = 0; p < P; ++p)
-          lp[m][p] = make_uint4(lp[m][p].x & k[0], lp[m][p].y & k[1], lp[m][p].z & k[2], lp[m][p].w & k[3]);
+      for (int n = 0; n < 8; ++n) {
+        const uint32_t sel = n & 1 ? 0x07060302u : 0x05040100u;
+        const uint4 b = make_uint4(__builtin_amdgcn_perm(word_of(y[1], n >> 1), word_of(y[0], n >> 1), sel),
+                                   __builtin_amdgcn_perm(word_of(y[3], n >> 1), word_of(y[2], n >> 1), sel),
+                                   __builtin_amdgcn_perm(word_of(y[5], n >> 1), word_of(y[4], n >> 1), sel),
+                                   __builtin_amdgcn_perm(word_of(y[7], n >> 1), word_of(y[6], n >> 1), sel));
+#pragma unroll
+        for (int p = 0; p < P; ++p) acc[m][n] = mfma16<T>(lp[p], b, acc[m][n]);
+      }
     }
-#pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      const uint32_t sel = n & 1 ? 0x07060302u : 0x05040100u;
-      const uint4 b = make_uint4(__builtin_amdgcn_perm(word_of(y[1], n >> 1), word_of(y[0], n >> 1), sel),
-                                 __builtin_amdgcn_perm(word_of(y[3], n >> 1), word_of(y[2], n >> 1), sel),
-                                 __builtin_amdgcn_perm(word_of(y[5], n >> 1), word_of(y[4], n >> 1), sel),
-                                 __builtin_amdgcn_perm(word_of(y[7], n >> 1), word_of(y[6], n >> 1), sel));
-#pragma unroll
-      for (int m = 0; m < RT; ++m)
-#pragma unroll
-        for (int p = 0; p < P; ++p) acc[m][n] = mfma16<T>(lp[m][p], b, acc[m][n]);
-    }
+    stage ^= 1;
   }
-  // tile n, lane l: ranks 4 (l / 16) + r, column 8 (l % 16) + n; the
-  // wavefronts' sums in a tree of fixed order
-  auto put = [&](float* p) {
-#pragma unroll
-    for (int m = 0; m < RT; ++m)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int n = 0; n < 8; ++n) p[(16 * m + 4 * q4 + r) * CP + 8 * r16 + n] = acc[m][n][r];
-  };
-  auto add = [&](const float* p) {
-#pragma unroll
-    for (int m = 0; m < RT; ++m)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int n = 0; n < 8; ++n) acc[m][n][r] += p[(16 * m + 4 * q4 + r) * CP + 8 * r16 + n];
-  };
-  if (wave >= 2) put(red + (wave - 2) * R * CP);
-  __syncthreads();
-  if (wave < 2) add(red + wave * R * CP);
-  __syncthreads();
-  if (wave == 1) put(red);
-  __syncthreads();
-  if (wave == 0) {
-    add(red);
-    put(red);
-  }
-  __syncthreads();
-  const int rows = min(R, g.rank - r0), cols = min(kGradCols, C - c0);
+  if (!live) return;
+  // tile n, lane l: ranks 4 (l / 16) + r, column 8 (l % 16) + n
   const bool whole = u.all <= g.chunk;
   const float f = right && whole ? g.scale[u.a] : 1.0f;
   const int64_t to = whole ? u.a : part_of(g, u.a) + u.piece;
-  const int* up = g.up ? g.up + (unit * 2 + right) * g.ranks + r0 : nullptr;
-  if (right) {
-    float* d = (whole ? g.dB : g.pB) + (to * g.O + c0) * g.rank + r0;
-    for (int e = tid; e < cols * rows; e += 64 * kGradWaves) {
-      const int c = e / rows, r = e - c * rows;
-      const float v = red[r * CP + c];
-      d[(int64_t)c * g.rank + r] = (up ? ldexpf(v, up[r]) : v) * f;
-    }
-  } else {
-    float* d = (whole ? g.dA : g.pA) + (to * g.rank + r0) * g.K + c0;
-    for (int e = tid; e < rows * kGradCols; e += 64 * kGradWaves) {
-      const int r = e / kGradCols, c = e % kGradCols;
-      const float v = red[r * CP + c];
-      d[(int64_t)r * g.K + c] = up ? ldexpf(v, up[r]) : v;
+#pragma unroll
+  for (int m = 0; m < RT; ++m) {
+    const int r = r0 + 16 * m + 4 * q4;  // four ranks; rank is a multiple of 8
+    if (r >= g.rank) continue;
+    if (g.up)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int up = g.up[(unit * 2 + right) * g.ranks + r + i];
+#pragma unroll
+        for (int n = 0; n < 8; ++n) acc[m][n][i] = ldexpf(acc[m][n][i], up);
+      }
+    if (right) {
+      float* d = (whole ? g.dB : g.pB) + (to * g.O + c0 + 8 * r16) * g.rank + r;
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+        if (n < left) *(floatx4*)(d + (int64_t)n * g.rank) = acc[m][n] * f;
+    } else {
+      float* d = (whole ? g.dA : g.pA) + (to * g.rank + r) * g.K + c0 + 8 * r16;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        *(floatx4*)(d + (int64_t)i * g.K) = floatx4{acc[m][0][i], acc[m][1][i], acc[m][2][i], acc[m][3][i]};
+        *(floatx4*)(d + (int64_t)i * g.K + 4) = floatx4{acc[m][4][i], acc[m][5][i], acc[m][6][i], acc[m][7][i]};
+      }
     }
   }
 }
@@ -639,13 +647,12 @@ static AdaptPlan adapt_plan(const W4Args& a, const W4Adapt& d, bool backward) {
     p.off_order = take((size_t)a.N * 4);
     p.off_start = take((size_t)(d.count + 1) * 4);
     // A chunk's sums are written and read in fp32: from eight tokens per rank on
-    // they are at most half of what it reads; beyond that about four blocks per
-    // unit.
-    const int64_t tiles = (a.K + a.O + kGradCols - 1) / kGradCols * (d.rank > 64 ? 2 : 1);
-    int64_t chunk = a.N * tiles / (4 * kCUs);
+    // they are at most half of what it reads; beyond that two blocks per unit.
+    const int64_t tiles = (a.K + a.O + 4 * kGradCols - 1) / (4 * kGradCols) * (d.rank > 64 ? 2 : 1);
+    int64_t chunk = a.N * tiles / (2 * kCUs);
     if (chunk < 8 * d.rank) chunk = 8 * d.rank;
     if (chunk > a.N) chunk = a.N;
-    p.chunk = (int)((chunk + 127) & ~(int64_t)127);
+    p.chunk = (int)((chunk + 63) & ~(int64_t)63);
     p.units = (int)(a.N / p.chunk) + d.count;
     p.ranks = (d.rank + 15) & ~15;
     // the adapters' tokens, each from a multiple of eight on, and what a last
@@ -780,21 +787,16 @@ static hipError_t backward(const W4Args& a, const W4Adapt& d, const AdaptPlan& p
   g.stride = p.stride;
   g.left = (uint16_t*)(ws + p.off_left);
   g.up = a.type == kF16 ? (int*)(ws + p.off_lup) : nullptr;
-  hipLaunchKernelGGL((k_adapt_left<T>), dim3(p.units, 2 * p.ranks / 16, p.chunk / 128), dim3(256), 0, stream, g);
-  auto go = [&](auto* kernel, int rt, int z) {
-    const int lds = 2 * 16 * rt * (kGradCols + 4) * 4;
-    if (lds > 65536) {
-      const hipError_t e =
-          hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-      if (e != hipSuccess) return e;
-    }
-    const dim3 grid((unsigned)(a.K / kGradCols + (a.O + kGradCols - 1) / kGradCols), p.units, z);
-    hipLaunchKernelGGL(kernel, grid, dim3(64 * kGradWaves), lds, stream, g);
+  hipLaunchKernelGGL((k_adapt_left<T>), dim3(p.units, 2 * p.ranks / 16, p.chunk / 64), dim3(256), 0, stream, g);
+  auto go = [&](auto* kernel, int z) {
+    const int64_t wide = kGradCols * kGradWaves;
+    const dim3 grid((unsigned)((a.K + wide - 1) / wide + (a.O + wide - 1) / wide), p.units, z);
+    hipLaunchKernelGGL(kernel, grid, dim3(64 * kGradWaves), 0, stream, g);
     return hipGetLastError();
   };
-  e = d.rank <= 16   ? go(&k_adapt_grad<T, 1>, 1, 1)
-      : d.rank <= 32 ? go(&k_adapt_grad<T, 2>, 2, 1)
-                     : go(&k_adapt_grad<T, 4>, 4, d.rank > 64 ? 2 : 1);
+  e = d.rank <= 16   ? go(&k_adapt_grad<T, 1>, 1)
+      : d.rank <= 32 ? go(&k_adapt_grad<T, 2>, 1)
+                     : go(&k_adapt_grad<T, 4>, d.rank > 64 ? 2 : 1);
   if (e != hipSuccess) return e;
   const int64_t quads = d.rank * (a.K + a.O) / 4;
   hipLaunchKernelGGL(k_adapt_join, dim3((unsigned)((quads + 255) / 256), d.count), dim3(256), 0, stream,
