@@ -100,6 +100,14 @@ bool w4_skinny_fits(const W4Args& a);
 hipError_t launch_w4_skinny(W4Op op, const W4Args& a, hipStream_t stream);
 hipError_t launch_w4(W4Op op, const W4Args& a, hipStream_t stream);
 
+// Blocks of a launch whose number may pass what one dimension takes (2^32 threads
+// along x): the rest lie along y, and those behind the last find nothing to do.
+constexpr int64_t kGridRow = (int64_t)1 << 22;
+inline dim3 grid_of(int64_t blocks, unsigned z = 1) {
+  return blocks <= kGridRow ? dim3((unsigned)blocks, 1, z)
+                            : dim3((unsigned)kGridRow, (unsigned)((blocks + kGridRow - 1) / kGridRow), z);
+}
+
 // The same with adapters (w4_adapt.hip): a.O and a.K are the packed matrix's,
 // in0 X or dY, in1 X of the backward pass, out0 Y or dX.
 struct W4Adapt {

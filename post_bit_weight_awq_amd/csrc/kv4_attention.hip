@@ -49,9 +49,9 @@ struct AttnArgs {
   float scale, slack;  // scale: |scale| log2(e); slack: 8 / scale
   int flip;            // the scale is negative: Q changes sign
   int splits, per;    // blocks of a unit, the keys of each
-  int tiles;          // of rows, over all sequences
+  uint32_t units;     // tiles of rows over all sequences, by kv heads
   int rows;           // of a tile that k_kv4_join looks at
-  float* parts;  // [unit][split][16][D + 2]
+  float* parts;  // [unit][split][row][D + 4]: the sums, maximum, sum of weights
 };
 
 // Rows row0 .. of one sequence and kv head, `rows` of them in the sequence.
@@ -555,7 +555,8 @@ k_kv4_decode(AttnArgs a) {
   __shared__ float sm[kDecodeWaves][16], sl[kDecodeWaves][16];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int split = blockIdx.x % a.splits, id = blockIdx.x / a.splits;
+  const uint32_t block = grid_block(), split = block % a.splits, id = block / a.splits;
+  if (id >= a.units) return;
   const Unit u = unit_of<kDecodeRows>(a, id / a.c.heads, id % a.c.heads);
   if (u.row0 >= u.rows) return;
   const int count = min(u.rows - u.row0, 16);
@@ -607,7 +608,7 @@ k_kv4_decode(AttnArgs a) {
       for (int k = 0; k < 8; ++k) v[k] = fmaf(f, so[k], v[k]);
     }
     if (a.splits > 1) {
-      float* p = a.parts + ((int64_t)blockIdx.x * 16 + row) * (D + 4);
+      float* p = a.parts + ((int64_t)block * 16 + row) * (D + 4);
       *(float4*)(p + c) = make_float4(v[0], v[1], v[2], v[3]);
       *(float4*)(p + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
       if (c == 0) {
@@ -762,7 +763,8 @@ k_kv4_chunk(AttnArgs a) {
   __shared__ __attribute__((aligned(16))) char smem[2 * S::kBytes];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int split = blockIdx.x % a.splits, id = blockIdx.x / a.splits;
+  const uint32_t block = grid_block(), split = block % a.splits, id = block / a.splits;
+  if (id >= a.units) return;
   const Unit u = unit_of<kChunkRows>(a, id / a.c.heads, id % a.c.heads);
   if (u.row0 >= u.rows) return;
   auto seen_by = [&](int row) { return min(max(u.len - u.run + row / a.per_kv + 1, 0), u.len); };
@@ -823,7 +825,7 @@ k_kv4_chunk(AttnArgs a) {
   if (row >= u.rows) return;
   constexpr int TG = G / 16;
   if (a.splits > 1) {
-    float* x = a.parts + ((int64_t)blockIdx.x * kChunkRows + row - u.row0) * (D + 4);
+    float* x = a.parts + ((int64_t)block * kChunkRows + row - u.row0) * (D + 4);
 #pragma unroll
     for (int n = 0; n < D / 16; n += 2)
 #pragma unroll
@@ -909,9 +911,10 @@ static hipError_t run(const Kv4Attention& k, hipStream_t stream) {
   const Split split = split_of(k);
   a.splits = split.splits;
   a.per = split.per;
-  a.tiles = (int)row_tiles(k, split.rows);
-  const int64_t units = (int64_t)a.tiles * a.c.heads;
-  const dim3 grid((unsigned)(units * a.splits));
+  // below 2^31, with splits below 2^18
+  const int64_t units = row_tiles(k, split.rows) * a.c.heads;
+  a.units = (uint32_t)units;
+  const dim3 grid = grid_of(units * a.splits);
   // rows of a tile at most
   a.rows = k.starts == nullptr && a.per_kv < split.rows ? a.per_kv : split.rows;
   if (!takes_decode(k))

@@ -244,8 +244,9 @@ k_adapt_order(OrderArgs a) {
   __shared__ __attribute__((aligned(16))) uint16_t tile[64 * kTileRow];
   __shared__ int wsum[kOrder / 64][2];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  if ((int)blockIdx.x < a.count) {
-    const int me = blockIdx.x;
+  const uint32_t block = grid_block();
+  if (block < (uint32_t)a.count) {
+    const int me = block;
     int less = 0, mine = 0;
     for (int t = tid; t < a.N; t += kOrder) {
       const int id = a.ids[t];
@@ -302,9 +303,10 @@ k_adapt_order(OrderArgs a) {
     return;
   }
   const int ka = a.K / 64, kb = (a.ldb + 63) / 64, rb = a.rank >> 3;
-  const int64_t id = (int64_t)blockIdx.x - a.count;
+  const int64_t id = (int64_t)block - a.count;
   const int which = (int)(id % (ka + kb));
   const int64_t ad = id / (ka + kb);
+  if (ad >= a.count) return;
   if (which < ka) {
     const int c0 = 64 * which;
     const uint16_t* s = a.A + ad * a.rank * a.K + c0;
@@ -733,7 +735,7 @@ static hipError_t backward(const W4Args& a, const W4Adapt& d, const AdaptPlan& p
   o.count = d.count;
   o.rank = d.rank;
   const int64_t blocks = d.count * (1 + (a.K + 63) / 64 + (p.ldb + 63) / 64);
-  hipLaunchKernelGGL(k_adapt_order, dim3((unsigned)blocks), dim3(kOrder), 0, stream, o);
+  hipLaunchKernelGGL(k_adapt_order, grid_of(blocks), dim3(kOrder), 0, stream, o);
   LowArgs l{};
   l.X = (const uint16_t*)a.in0;
   l.A = o.Bt;

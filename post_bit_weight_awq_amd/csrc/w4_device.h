@@ -17,6 +17,9 @@ __device__ __forceinline__ T from_f32(float v) {
   return (T)v;
 }
 
+// The block's place in a grid_of() launch.
+__device__ __forceinline__ uint32_t grid_block() { return blockIdx.y * gridDim.x + blockIdx.x; }
+
 // act(g): silu g / (1 + e^-g), or the tanh form of gelu,
 // g/2 (1 + tanh(c (g + a g^3))) = g / (1 + e^-2c(g + a g^3)).  Both are
 // g * sigmoid(y); *slope gets the derivative p + g y' p (1 - p).  With

@@ -358,3 +358,48 @@ def test_streams_workspaces_and_graphs(runs):
         step()
         assert torch.equal(got, out)
         torch.cuda.synchronize()
+
+
+def test_more_blocks_than_one_dimension_takes():
+    """Launches of more than 2^32 threads: the last tokens, heads and sequences are reached."""
+    d, page, n = 64, 16, 2 ** 20
+    hold = K.make_cache(4, 130, page, d, 32, 1)
+    c = on_gpu(hold)
+    k = torch.randn(4099, 1, d, generator=torch.Generator().manual_seed(2)).to(B)
+    kd = k.cuda()[torch.arange(n, device="cuda") % 4099].expand(n, 130, d)
+    slots = torch.full((n,), -1, dtype=torch.int32)
+    tail = torch.arange(n - 60, n)
+    slots[tail] = torch.arange(60, dtype=torch.int32)
+    slots[5] = 61
+    awq.awq_kv4_append(kd, kd, c, slots.cuda())
+    at = torch.cat([tail, torch.tensor([5])])
+    x = k[at % 4099].expand(61, 130, d)
+    want = append_plain(hold, x, x, slots[at], 32)
+    assert same(back(c), want)
+    every = torch.arange(n, dtype=torch.int32, device="cuda") % 64
+    few = awq.awq_kv4_gather(c, every[:64], dtype=B)
+    for got, part in zip(awq.awq_kv4_gather(c, every, dtype=B), few):
+        assert bool((got.view(-1, 64, 130, d) == part).all())
+
+
+@pytest.mark.parametrize("heads,run", [(17, None), (114, 17)])
+def test_more_units_than_one_dimension_takes(heads, run):
+    d, page = 64, 16
+    c = on_gpu(K.make_cache(3, heads, page, d, 32, 1))
+    q = torch.randn(1, heads, d, generator=torch.Generator().manual_seed(2)).half().cuda()
+    if run is None:
+        seqs, few = 2 ** 20, 17
+        lens = torch.arange(seqs, dtype=torch.int32) % few
+        starts = lambda s: None
+        n = 1
+    else:
+        seqs, few = 2 ** 15 + 5, 1
+        lens = torch.full((seqs,), 16, dtype=torch.int32)
+        starts = lambda s: torch.arange(s + 1, dtype=torch.int32) * run
+        n = run
+    table = torch.full((seqs, 1), 2, dtype=torch.int32)
+    part = attend(c, q.expand(few * n, heads, d), table[:few], lens[:few], starts(few))
+    got = attend(c, q.expand(seqs * n, heads, d), table, lens, starts(seqs))
+    whole = seqs // few * few * n
+    assert bool((got[:whole].view(-1, few * n, heads, d) == part).all())
+    assert torch.equal(got[whole:], part[:seqs * n - whole])

@@ -251,3 +251,24 @@ def test_two_layers_under_autograd():
         # half a step of 2^-10; they add like independent errors of a norm
         rel = float((got.grad.double().cpu() - want.grad).norm() / want.grad.norm())
         assert rel <= 6 * 2.0 ** -11, rel
+
+
+def test_more_blocks_than_one_dimension_takes():
+    """So many adapters that the launch that lays them out has more than 2^32 threads: the last ones too."""
+    n, k, o, count = 5, 8192, 8192, 32768
+    layer, x, dy, _, _, _, _ = make(n, k, o, 128, B, 8, 1, 3)
+    ids = torch.tensor([count - 1, 0, -1, count - 1, 20000], dtype=torch.int32)
+    used = [0, 20000, count - 1]
+    g = torch.Generator().manual_seed(4)
+    few_a, few_b = (0.05 * torch.randn(3, 8, k, generator=g)).to(B), (0.05 * torch.randn(3, o, 8, generator=g)).to(B)
+    a, b = torch.zeros(count, 8, k, dtype=B, device="cuda"), torch.zeros(count, o, 8, dtype=B, device="cuda")
+    a[used], b[used] = few_a.cuda(), few_b.cuda()
+    scale = torch.linspace(0.5, 1.5, count)
+    low = torch.randn(n, 8, generator=g)
+    dx, da, db = awq.awq_w4a16_adapted_backward(dy.cuda(), x.cuda(), low.cuda(), *gpu(layer), a, b, scale.cuda(), ids.cuda())
+    few_ids = torch.tensor([2, 0, -1, 2, 1], dtype=torch.int32)
+    want = AP.backward_bounds(dy, x, low, layer, few_a, few_b, scale[used], few_ids)
+    inside(dx, want[0][0], AP.rounded(*want[0], B), "dx")
+    inside(da[used], want[1][0], AP.rounded(*want[1], F32), "da")
+    inside(db[used], want[2][0], AP.rounded(*want[2], F32), "db")
+    assert int(da.count_nonzero(dim=(1, 2)).count_nonzero()) == 3 == int(db.count_nonzero(dim=(1, 2)).count_nonzero())
