@@ -27,12 +27,14 @@
 // and k_kv4_join joins the splits in order.  Bound by the stream of codes on long
 // caches (64 ragged sequences of up to 4096 keys, 40 heads of 128: 183 us, 4.4
 // TB/s; with the tiles in registers, at half the wavefronts in flight, 200), by
-// the way to the first keys and the join on short ones (one sequence of 777: 9.5
+// the way to the first keys and the join on short ones (one sequence of 777: 10.8
 // us).  Runs of tokens (k_kv4_chunk): a block of eight wavefronts takes 128 rows;
 // they prepare a tile's operands in LDS together, each an eighth.  Bound by VALU
-// issue and the barrier of each tile: 4 x 256 to 512 tokens behind up to 4096
-// keys, 32 heads on 8: 202 us, 304 TFLOP/s (each wavefront by itself, for two row
-// tiles: 268; four wavefronts of two row tiles: 204; products a tile ahead: 255).
+// issue and the barrier of each tile and, with few sequences, by the longest one:
+// 4 x 256 to 512 tokens behind 512 to 4096 keys, 32 heads on 8: 165 us, 372
+// TFLOP/s, 16 such sequences 464 us, 507 TFLOP/s (in whole units, 4 sequences: 200
+// us; each wavefront by itself, for two row tiles, then 268; four wavefronts of two
+// row tiles 204; of 64 rows 197, and 16 sequences 509; products a tile ahead 255).
 #include "kv4_device.h"
 #include "w4_internal.h"
 
@@ -84,11 +86,29 @@ __device__ __forceinline__ Unit unit_of(const AttnArgs& a, int tile, int head) {
     u.seq = lo;
     u.first = start(lo);
     u.run = max(start(lo + 1) - u.first, 0);
-    u.row0 = max(tile - base(lo), 0) * R;
+    // the last rows, which see the most keys, begin first
+    const int at = max(tile - base(lo), 0), tiles = (u.run * a.per_kv + R - 1) / R;
+    u.row0 = (at < tiles ? tiles - 1 - at : at) * R;
   }
   u.rows = u.run * a.per_kv;
   u.len = min(max(a.lens[u.seq], 0), a.per_seq << a.c.shift);
   return u;
+}
+
+// The keys of a unit: `end` that its last row sees, in parts of `per` each.
+// One part alone goes to the output, more meet in the join.
+struct Keys {
+  int end, per;
+  __device__ __forceinline__ bool one() const { return end <= per; }
+  __device__ __forceinline__ int parts() const { return (end + per - 1) / per; }
+};
+template <int R>
+__device__ __forceinline__ Keys keys_of(const AttnArgs& a, const Unit& u) {
+  constexpr int kStep = R == 16 ? 128 : 32;  // what a block takes at a time
+  Keys k;
+  k.end = min(max(u.len - u.run + (min(u.row0 + R, u.rows) - 1) / a.per_kv + 1, 0), u.len);
+  k.per = max(((k.end + a.splits - 1) / a.splits + kStep - 1) & -kStep, a.per);
+  return k;
 }
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -540,7 +560,7 @@ __device__ __forceinline__ T* out_row(const AttnArgs& a, const Unit& u, int row)
   return (T*)a.out + ((int64_t)(u.first + t) * a.heads + u.head * a.per_kv + row - t * a.per_kv) * D;
 }
 
-constexpr int kDecodeRows = 16, kDecodeWaves = 4, kSplitKeys = 256;
+constexpr int kDecodeRows = 16, kDecodeWaves = 4;
 
 template <typename T, int D, int G, bool PAIR>
 __global__ void __launch_bounds__(64 * kDecodeWaves, D / G == 4 ? 3 : 4)
@@ -560,13 +580,12 @@ k_kv4_decode(AttnArgs a) {
   const Unit u = unit_of<kDecodeRows>(a, id / a.c.heads, id % a.c.heads);
   if (u.row0 >= u.rows) return;
   const int count = min(u.rows - u.row0, 16);
-  // the last row sees the most keys
-  const int end = min(max(u.len - u.run + (u.row0 + count - 1) / a.per_kv + 1, 0), u.len);
-  const int per = max(((end + a.splits - 1) / a.splits + 127) & ~127, a.per);
-  const int from = (int)min((int64_t)split * per, (int64_t)end), to = min(from + per, end);
+  const Keys keys = keys_of<kDecodeRows>(a, u);
+  const int from = (int)min((int64_t)split * keys.per, (int64_t)keys.end), to = min(from + keys.per, keys.end);
   Rows<D, G> w;
   // PAIR: rows of lanes 8 to 15 are those of 0 to 7
   const int low = load_rows<T>(a, u, PAIR ? u.row0 - (lane & 8) : u.row0, lane, w);
+  if (split && from >= keys.end) return;  // not before Q is on its way
   walk<T, D, G, PAIR>(a, u, w, low, from + 32 * wave, to, 32 * kDecodeWaves, lane, smem + wave * kOwn);
   finish_sums(w);
   const int r16 = lane & 15, q4 = lane >> 4;
@@ -607,7 +626,7 @@ k_kv4_decode(AttnArgs a) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] = fmaf(f, so[k], v[k]);
     }
-    if (a.splits > 1) {
+    if (!keys.one()) {
       float* p = a.parts + ((int64_t)block * 16 + row) * (D + 4);
       *(float4*)(p + c) = make_float4(v[0], v[1], v[2], v[3]);
       *(float4*)(p + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
@@ -624,9 +643,9 @@ k_kv4_decode(AttnArgs a) {
   }
 }
 
-// A row per block: thread groups take every 256 / (D / 8)-th split each, with
-// four in flight, and are joined through LDS, all in fixed order.
-template <typename T, int D, int R>
+// Single tokens: a row per block: thread groups take every 256 / (D / 8)-th part
+// each, with four in flight, and are joined through LDS, all in fixed order.
+template <typename T, int D>
 __global__ void __launch_bounds__(256)
 k_kv4_join(AttnArgs a) {
   constexpr int C = D / 8, N = 256 / C;  // threads of a row's columns, groups
@@ -634,14 +653,20 @@ k_kv4_join(AttnArgs a) {
   const int tid = threadIdx.x, c = 8 * (tid % C), part = tid / C;
   const int row = blockIdx.x % a.rows;
   const int id = blockIdx.x / a.rows;
+  constexpr int R = kDecodeRows;
   const Unit u = unit_of<R>(a, id / a.c.heads, id % a.c.heads);
   if (u.row0 + row >= u.rows) return;
   const float* p = a.parts + ((int64_t)id * a.splits * R + row) * (D + 4);
   constexpr int64_t S = R * (D + 4);
-  if (tid < a.splits) sm[tid] = p[tid * S + D];
+  // requested before it is known how many of them were written
+  const float top = p[min(tid, a.splits - 1) * S + D];
+  const Keys keys = keys_of<R>(a, u);
+  if (keys.one()) return;
+  const int parts = keys.parts();
+  if (tid < 128) sm[tid] = tid < parts ? top : -INFINITY;
   __syncthreads();
   float m = -INFINITY;
-  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, sm[s]);
+  for (int s = 0; s < parts; ++s) m = fmaxf(m, sm[s]);
   float l = 0.0f, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   for (int s = part; s < a.splits; s += 4 * N) {
     float4 y[4], z[4];
@@ -656,7 +681,7 @@ k_kv4_join(AttnArgs a) {
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (s + i * N >= a.splits) break;
+      if (s + i * N >= parts) break;
       l = fmaf(f[i], w[i], l);
       v[0] = fmaf(f[i], y[i].x, v[0]), v[1] = fmaf(f[i], y[i].y, v[1]);
       v[2] = fmaf(f[i], y[i].z, v[2]), v[3] = fmaf(f[i], y[i].w, v[3]);
@@ -677,6 +702,56 @@ k_kv4_join(AttnArgs a) {
     o += so[i][tid];
   }
   out_row<T, D>(a, u, u.row0 + row)[tid] = from_f32<T>(l == 0.0f ? 0.0f : o * (1.0f / l));
+}
+
+// Runs: eight columns of a row per thread, part after part, four in flight.
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(256)
+k_kv4_join_runs(AttnArgs a) {
+  constexpr int C = D / 8, N = 256 / C;  // rows of a block
+  const uint32_t block = grid_block(), id = block / (R / N);
+  const int c = 8 * (threadIdx.x % C), row = block % (R / N) * N + threadIdx.x / C;
+  if (id >= a.units) return;
+  const Unit u = unit_of<R>(a, id / a.c.heads, id % a.c.heads);
+  if (u.row0 + row >= u.rows) return;
+  const Keys keys = keys_of<R>(a, u);
+  if (keys.one()) return;
+  const int parts = keys.parts();
+  const float* p = a.parts + ((int64_t)id * a.splits * R + row) * (D + 4);
+  constexpr int64_t S = R * (D + 4);
+  float m = -INFINITY, l = 0.0f, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int s = 0; s < parts; s += 4) {
+    float4 y[4], z[4];
+    float2 w[4];  // maximum, sum of weights
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float* x = p + min(s + i, parts - 1) * S;
+      y[i] = *(const float4*)(x + c), z[i] = *(const float4*)(x + c + 4);
+      w[i] = *(const float2*)(x + D);
+    }
+    const float was = m;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, w[i].x);
+    // -inf has no keys, or sums that are NaN: they keep their weight
+    const float f = was == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((was - m) * a.scale);
+    l *= f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] *= f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (s + i >= parts) break;
+      const float g = w[i].x == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((w[i].x - m) * a.scale);
+      l = fmaf(g, w[i].y, l);
+      v[0] = fmaf(g, y[i].x, v[0]), v[1] = fmaf(g, y[i].y, v[1]);
+      v[2] = fmaf(g, y[i].z, v[2]), v[3] = fmaf(g, y[i].w, v[3]);
+      v[4] = fmaf(g, z[i].x, v[4]), v[5] = fmaf(g, z[i].y, v[5]);
+      v[6] = fmaf(g, z[i].z, v[6]), v[7] = fmaf(g, z[i].w, v[7]);
+    }
+  }
+  const float f = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] *= f;
+  store8(out_row<T, D>(a, u, u.row0 + row) + c, v, 8, true);
 }
 
 constexpr int kChunkWaves = 8, kChunkRows = 16 * kChunkWaves;
@@ -768,9 +843,9 @@ k_kv4_chunk(AttnArgs a) {
   const Unit u = unit_of<kChunkRows>(a, id / a.c.heads, id % a.c.heads);
   if (u.row0 >= u.rows) return;
   auto seen_by = [&](int row) { return min(max(u.len - u.run + row / a.per_kv + 1, 0), u.len); };
-  const int end = seen_by(min(u.row0 + kChunkRows, u.rows) - 1);
-  const int per = max(((end + a.splits - 1) / a.splits + 31) & ~31, a.per);
-  const int from = (int)min((int64_t)split * per, (int64_t)end), to = min(from + per, end);
+  const Keys keys = keys_of<kChunkRows>(a, u);
+  const int from = (int)min((int64_t)split * keys.per, (int64_t)keys.end), to = min(from + keys.per, keys.end);
+  if (split && from >= keys.end) return;
   // a wavefront behind the sequence's rows prepares its share alone
   const int row0 = u.row0 + 16 * wave;
   const bool live = row0 < u.rows;
@@ -824,7 +899,7 @@ k_kv4_chunk(AttnArgs a) {
   const int row = row0 + (lane & 15);
   if (row >= u.rows) return;
   constexpr int TG = G / 16;
-  if (a.splits > 1) {
+  if (!keys.one()) {
     float* x = a.parts + ((int64_t)block * kChunkRows + row - u.row0) * (D + 4);
 #pragma unroll
     for (int n = 0; n < D / 16; n += 2)
@@ -874,8 +949,11 @@ static Split split_of(const Kv4Attention& a) {
   // Single tokens: four blocks of four wavefronts fit a compute unit.  Where the
   // units fill them by themselves a part costs more than it hides: 64 x 500 keys,
   // 8 kv heads: 12.0 us whole, 16.6 in two; one sequence of 8192, 8 kv heads: 10.5
-  // us in parts of 256, 12.4 of 192 and 11.9 of 512.  Runs: two blocks of eight.
-  const int64_t target = decode ? 4 * kCUs : 2 * kCUs;
+  // us in parts of 256, 12.4 of 192 and 11.9 of 512.  Runs: two blocks of eight fit;
+  // half as many again even out sequences of different lengths (4 x 256 to 512
+  // tokens behind 512 to 4096 keys, 32 heads on 8: 165 us, 200 in whole; 8 x 256
+  // behind up to 8192: 310 and 393), parts of 1024 keys too few (217).
+  const int64_t target = decode ? 4 * kCUs : 3 * kCUs;
   s.per = !decode ? 512 : units < kCUs ? 256 : 320;
   int64_t n = (target + units / 2) / units, most = keys / s.per;
   if (n > most) n = most;
@@ -923,13 +1001,11 @@ static hipError_t run(const Kv4Attention& k, hipStream_t stream) {
     hipLaunchKernelGGL((k_kv4_decode<T, D, G, true>), grid, dim3(64 * kDecodeWaves), 0, stream, a);
   else
     hipLaunchKernelGGL((k_kv4_decode<T, D, G, false>), grid, dim3(64 * kDecodeWaves), 0, stream, a);
-  if (a.splits > 1) {
-    const dim3 rows((unsigned)(units * a.rows));
-    if (split.rows == kDecodeRows)
-      hipLaunchKernelGGL((k_kv4_join<T, D, kDecodeRows>), rows, dim3(256), 0, stream, a);
-    else
-      hipLaunchKernelGGL((k_kv4_join<T, D, kChunkRows>), rows, dim3(256), 0, stream, a);
-  }
+  if (a.splits > 1 && takes_decode(k))
+    hipLaunchKernelGGL((k_kv4_join<T, D>), dim3((unsigned)(units * a.rows)), dim3(256), 0, stream, a);
+  else if (a.splits > 1)
+    hipLaunchKernelGGL((k_kv4_join_runs<T, D, kChunkRows>), grid_of(units * (kChunkRows * D / 2048)), dim3(256), 0,
+                       stream, a);
   return hipGetLastError();
 }
 template <typename T>

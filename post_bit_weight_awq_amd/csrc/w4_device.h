@@ -18,7 +18,7 @@ __device__ __forceinline__ T from_f32(float v) {
 }
 
 // The block's place in a grid_of() launch.
-__device__ __forceinline__ uint32_t grid_block() { return blockIdx.y * gridDim.x + blockIdx.x; }
+__device__ __forceinline__ uint32_t grid_block() { return blockIdx.y * (uint32_t)kGridRow + blockIdx.x; }
 
 // act(g): silu g / (1 + e^-g), or the tanh form of gelu,
 // g/2 (1 + tanh(c (g + a g^3))) = g / (1 + e^-2c(g + a g^3)).  Both are
