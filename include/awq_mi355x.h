@@ -483,7 +483,7 @@ int awq_kv4_gather(const awq_kv4_cache* cache, const int32_t* slots, int64_t n_t
  *   table:  [n_seqs, max_pages] int32; the keys of a page outside 0..n_pages - 1
  *           are not seen.  Pages may be shared
  *   lens:   [n_seqs] int32; taken as at least 0 and at most max_pages * page_size
- *   scale:  finite
+ *   scale:  from -2^32 to 2^32; scores are to stay in binary32's range
  *   out:    [n_tokens, n_heads, head_dim] dtype, dense
  *   n_heads: a multiple of cache->n_heads, up to 1024 times; n_tokens, n_seqs:
  *           1..2^20, n_tokens * n_heads < 2^31; max_pages * page_size: up to 2^30

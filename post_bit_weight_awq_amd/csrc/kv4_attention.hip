@@ -288,9 +288,11 @@ struct Sixteen {
   }
 };
 
-// Scores of 32 keys, in units of the scale, in two steps: the groups' products,
-// whose sums begin at -16 sum Q, which takes the codes' 16 back, and what steps
-// and offsets make of them.  kf(u, j): columns 32 j .. of keys 16 u ..
+// Scores of 32 keys, in units of the scale and less the row's maximum so far, in
+// two steps: the groups' products, whose sums begin at -16 sum Q, which takes the
+// codes' 16 back, and what steps and offsets make of them.  The maximum is taken
+// off before the scale: its own product with it would be rounded, by more than
+// exp2 holds where scores are beyond 2^30.  kf(u, j): columns 32 j .. of keys 16 u ..
 template <typename T, int D, int G, typename KF>
 __device__ __forceinline__ void products(const Rows<D, G>& w, KF kf, floatx4 (&acc)[2][D / G]) {
   using R = Rows<D, G>;
@@ -309,6 +311,7 @@ template <int D, int G>
 __device__ __forceinline__ void scores(const Rows<D, G>& w, const uint32_t (&p)[2][4 * (D / G)],
                                        const floatx4 (&acc)[2][D / G], float (&s)[8]) {
   constexpr int NG = D / G;
+  const float base = w.m == -INFINITY ? 0.0f : -w.m;
 #pragma unroll
   for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -317,7 +320,7 @@ __device__ __forceinline__ void scores(const Rows<D, G>& w, const uint32_t (&p)[
       for (int r = 0; r < 4; ++r) {
         const uint32_t x = p[u][r * NG + g];
         float& y = s[4 * u + r];
-        y = fmaf(f16_hi(x), w.qs[g], g == 0 ? 0.0f : y);  // one operation of mixed types
+        y = fmaf(f16_hi(x), w.qs[g], g == 0 ? base : y);  // one operation of mixed types
         y = fmaf(f16_lo(x), acc[u][g][r], y);
       }
 }
@@ -350,14 +353,15 @@ template <int D, int G>
 __device__ __forceinline__ void weigh(Rows<D, G>& w, float scale, float slack, float (&s)[8]) {
   using R = Rows<D, G>;
   float top = fmaxf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])), fmaxf(fmaxf(s[4], s[5]), fmaxf(s[6], s[7])));
-  if (__any(top > w.m + slack)) {
+  const bool first = w.m == -INFINITY;
+  if (__any(top > (first ? -INFINITY : slack))) {
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
-    const float now = fmaxf(w.m, top);
-    const float a = w.m == now         ? 1.0f
-                    : w.m == -INFINITY ? 0.0f
-                                       : __builtin_amdgcn_exp2f((w.m - now) * scale);
-    w.m = now;
+    const float up = first ? (top == -INFINITY ? 0.0f : top) : fmaxf(top, 0.0f);
+    const float a = first ? (top == -INFINITY ? 1.0f : 0.0f) : __builtin_amdgcn_exp2f(-up * scale);
+    w.m = first ? top : w.m + up;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] -= up;
     w.l *= a;
 #pragma unroll
     for (int g = 0; g < R::NG; ++g) {
@@ -370,10 +374,9 @@ __device__ __forceinline__ void weigh(Rows<D, G>& w, float scale, float slack, f
 #pragma unroll
       for (int r = 0; r < 4; ++r) w.o[n][r] *= a;
   }
-  const float base = w.m == -INFINITY ? 0.0f : -w.m * scale;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], scale, base));
+    s[i] = __builtin_amdgcn_exp2f(s[i] * scale);
     w.l += s[i];
   }
 }

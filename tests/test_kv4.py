@@ -176,3 +176,8 @@ def test_plain_quantize_bounds():
     x[0, 5] = math.inf
     c, p = K.quantize(x.half(), 32)
     assert bool(K.value(c, p)[0, :32].isnan().all()) and bool((K.value(c, p)[0, 32:] == 0).all())
+
+
+def test_attention_refuses_scales_that_leave_the_range(lib):
+    for scale in (2.0 ** 33, -1e38, 3e38):
+        assert attend(lib, cache(), scale=scale) == BAD

@@ -403,3 +403,30 @@ def test_more_units_than_one_dimension_takes(heads, run):
     whole = seqs // few * few * n
     assert bool((got[:whole].view(-1, few * n, heads, d) == part).all())
     assert torch.equal(got[whole:], part[:seqs * n - whole])
+
+
+@pytest.mark.parametrize("runs", [None, [40, 33]])
+@pytest.mark.parametrize("scale", [2.0 ** 32, -2.0 ** 32])
+def test_largest_scales(scale, runs):
+    """All weight is on one key: its values, off by their two bf16 parts (2^-17), the
+    quotient of the sums (a few 2^-24) and the output's rounding."""
+    lens, h, d = [50, 700], 2, 128
+    hold = K.make_cache(50, h, 16, d, 64, 3)
+    g = torch.Generator().manual_seed(5)
+    table = torch.randperm(50, generator=g)[:44 + 4].view(1, -1)[:, :44].repeat(2, 1).to(torch.int32)
+    n = len(lens) if runs is None else sum(runs)
+    q = torch.randn(n, 2 * h, d, generator=g).half()
+    starts = None if runs is None else torch.tensor([0, runs[0], n], dtype=torch.int32)
+    got = attend(on_gpu(hold), q.cuda(), table, torch.tensor(lens, dtype=torch.int32), starts, scale=scale).cpu().to(K.F64)
+    k, v = K.read(hold)
+    size = K.size_of(d, hold[3])
+    for s in range(2):
+        a, b = (s, s + 1) if runs is None else (int(starts[s]), int(starts[s + 1]))
+        for t in range(a, b):
+            j = torch.arange(lens[s] - (b - 1 - t))
+            p, i = table[s, j // 16].long(), j % 16
+            for x in range(2 * h):
+                best = int((scale * (k[p, x // 2, i] @ q[t, x].to(K.F64))).argmax())
+                one, big = v[p[best], x // 2, i[best]], size[p[best], x // 2, i[best]]
+                bound = 2.0 ** -16 * big
+                assert bool(((got[t, x] - one).abs() <= bound + K.half_step(H) * (one.abs() + bound) + K.tiny(H)).all()), (t, x)
