@@ -483,7 +483,7 @@ int awq_kv4_gather(const awq_kv4_cache* cache, const int32_t* slots, int64_t n_t
  *   table:  [n_seqs, max_pages] int32; the keys of a page outside 0..n_pages - 1
  *           are not seen.  Pages may be shared
  *   lens:   [n_seqs] int32; taken as at least 0 and at most max_pages * page_size
- *   scale:  from -2^32 to 2^32; scores are to stay in binary32's range
+ *   scale:  from -2^32 to 2^32
  *   out:    [n_tokens, n_heads, head_dim] dtype, dense
  *   n_heads: a multiple of cache->n_heads, up to 1024 times; n_tokens, n_seqs:
  *           1..2^20, n_tokens * n_heads < 2^31; max_pages * page_size: up to 2^30
@@ -493,7 +493,9 @@ int awq_kv4_gather(const awq_kv4_cache* cache, const int32_t* slots, int64_t n_t
  * key times the step of its values is held in 16 bits (two bf16 parts), the
  * output rounds once.  Sums have a fixed order for given sizes.  NaN and
  * infinities at keys that a row does not see do not reach it; a query with an
- * infinity or a NaN gets NaN.
+ * infinity or a NaN gets NaN.  Finite queries may have any size: bf16's enter in
+ * units of 2^32, in which no sum leaves binary32 (what is cut below 2^-94 costs
+ * less than 2^-34 of a weight); weights of keys far below the row's best are 0.
  * Errors: as awq_kv4_append; AWQ_ERR_WORKSPACE for a short workspace. */
 size_t awq_kv4_attention_workspace_size(const awq_kv4_cache* cache, int64_t n_tokens,
                                         int64_t n_heads, int64_t n_seqs, int64_t max_pages,

@@ -782,7 +782,7 @@ int awq_kv4_attention(const awq_kv4_cache* cache, const void* q, int dtype, int6
       (rc = check_stride(q_token_stride, "q_token_stride")) ||
       (rc = check_stride(q_head_stride, "q_head_stride")))
     return rc;
-  // scores of 16-bit values times it stay in binary32
+  // up to it what the kernels cut of bf16 queries (below 2^-94) costs less than 2^-34 of a weight
   if (!(scale >= -0x1p32f && scale <= 0x1p32f))
     return fail(AWQ_ERR_INVALID_ARG, "scale=%g outside -2^32..2^32", (double)scale);
   const size_t need = awq::kv4_attention_workspace(a);

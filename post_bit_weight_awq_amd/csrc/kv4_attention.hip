@@ -48,7 +48,7 @@ struct AttnArgs {
   int64_t q_token, q_head;
   int tokens, seqs, per_seq;
   const int32_t *starts, *table, *lens;
-  float scale, slack;  // scale: |scale| log2(e); slack: 8 / scale
+  float scale, slack;  // scale: |scale| log2(e) (bf16: times kUnit); slack: 8 / scale
   int flip;            // the scale is negative: Q changes sign
   int splits, per;    // blocks of a unit, the keys of each
   uint32_t units;     // tiles of rows over all sequences, by kv heads
@@ -137,6 +137,16 @@ __device__ __forceinline__ int column(int n, int i) {
   return (n / TG) * G + 8 * (i % WG) + TG * (i / WG) + n % TG;
 }
 
+// Two bf16 values in units of 2^32: any finite query is then below 2^96, and
+// neither 16 + code times a row's sum nor a score (codes 15 and steps and offsets of
+// fp16's largest: below 2^126) leaves binary32.  A power of two changes no bit above
+// 2^-94; what is cut below costs less than 2^-34 of a weight at the largest scale.
+constexpr float kUnit = 0x1p32f;
+__device__ __forceinline__ uint32_t lower(uint32_t w) {
+  return __builtin_amdgcn_perm(__float_as_uint(__uint_as_float(w & 0xffff0000u) * (1.0f / kUnit)),
+                               __float_as_uint(__uint_as_float(w << 16) * (1.0f / kUnit)), 0x07060302u);
+}
+
 // Returns the keys that all 16 rows see.
 template <typename T, int D, int G>
 __device__ __forceinline__ int load_rows(const AttnArgs& a, const Unit& u, int row0, int lane, Rows<D, G>& w) {
@@ -152,6 +162,7 @@ __device__ __forceinline__ int load_rows(const AttnArgs& a, const Unit& u, int r
   for (int j = 0; j < R::J; ++j) {
     uint4 v = *(const uint4*)(p + 32 * j + 8 * q4);
     v.x ^= sign, v.y ^= sign, v.z ^= sign, v.w ^= sign;
+    if constexpr (!__is_same(T, _Float16)) v.x = lower(v.x), v.y = lower(v.y), v.z = lower(v.z), v.w = lower(v.w);
     // columns 0 4, 1 5, 2 6, 3 7, as the words' nibbles come
     w.q[j] = make_uint4(__builtin_amdgcn_perm(v.z, v.x, 0x05040100u),
                         __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
@@ -984,8 +995,9 @@ static hipError_t run(const Kv4Attention& k, hipStream_t stream) {
   a.starts = k.starts;
   a.table = k.table;
   a.lens = k.lens;
-  // below 1e-30 all weights are 1, and -inf, a hidden key's score, keeps its product
-  a.scale = fmaxf(fabsf(k.scale) * 1.4426950408889634f, 1e-30f);
+  // at the least value scores' products are below 2^-23 (so all weights 1 at scale 0),
+  // and -inf, a hidden key's score, keeps its product
+  a.scale = fmaxf(fabsf(k.scale) * (__is_same(T, _Float16) ? 1.0f : kUnit) * 1.4426950408889634f, 0x1p-149f);
   a.slack = 8.0f / a.scale;
   a.flip = k.scale < 0.0f;
   a.parts = (float*)k.ws;
