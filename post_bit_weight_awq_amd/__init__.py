@@ -15,6 +15,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import operator
 from dataclasses import dataclass
 from typing import Optional
 
@@ -550,9 +551,20 @@ class Kv4Cache:
     v_params [n_pages, n_heads, page_size, head_dim / group_size, 2] fp16.
     awq_kv4_cache makes one; a program may bring its own memory.  Place
     p * page_size + i is token i of page p.  The arrays are checked here and not
-    by each call: they are not resized or moved while the object lives."""
-    __slots__ = ("k_codes", "v_codes", "k_params", "v_params", "n_pages", "n_heads", "page_size",
-                 "head_dim", "group_size", "_device", "_ref")
+    by each call, so they and the sizes are read-only: a larger cache is another
+    object.  Arrays that were resized or replaced in place are refused."""
+    __slots__ = ("_k_codes", "_v_codes", "_k_params", "_v_params", "_n_pages", "_n_heads", "_page_size",
+                 "_head_dim", "_group_size", "_device", "_ref", "_at")
+
+    k_codes = property(operator.attrgetter("_k_codes"))
+    v_codes = property(operator.attrgetter("_v_codes"))
+    k_params = property(operator.attrgetter("_k_params"))
+    v_params = property(operator.attrgetter("_v_params"))
+    n_pages = property(operator.attrgetter("_n_pages"))
+    n_heads = property(operator.attrgetter("_n_heads"))
+    page_size = property(operator.attrgetter("_page_size"))
+    head_dim = property(operator.attrgetter("_head_dim"))
+    group_size = property(operator.attrgetter("_group_size"))
 
     def __init__(self, k_codes: torch.Tensor, v_codes: torch.Tensor, k_params: torch.Tensor,
                  v_params: torch.Tensor):
@@ -573,12 +585,12 @@ class Kv4Cache:
                 raise ValueError(f"{name} must be contiguous")
             if t.device != device:
                 raise ValueError(f"{name} is on {t.device}, k_codes on {device}")
-        self.k_codes, self.v_codes, self.k_params, self.v_params = k_codes, v_codes, k_params, v_params
-        self.n_pages, self.n_heads, self.page_size = p, h, s
-        self.head_dim, self.group_size = 8 * w, 8 * w // g
+        self._k_codes, self._v_codes, self._k_params, self._v_params = k_codes, v_codes, k_params, v_params
+        self._n_pages, self._n_heads, self._page_size = p, h, s
+        self._head_dim, self._group_size = 8 * w, 8 * w // g
         self._device = device.index if device.type == "cuda" else -1
-        self._ref = ctypes.byref(AwqKv4Cache(k_codes.data_ptr(), v_codes.data_ptr(), k_params.data_ptr(),
-                                             v_params.data_ptr(), p, h, s, 8 * w, 8 * w // g))
+        self._at = (k_codes.data_ptr(), v_codes.data_ptr(), k_params.data_ptr(), v_params.data_ptr())
+        self._ref = ctypes.byref(AwqKv4Cache(*self._at, p, h, s, 8 * w, 8 * w // g))
 
 
 def awq_kv4_cache(n_pages: int, n_heads: int, page_size: int, head_dim: int, group_size: int = 64,
@@ -607,6 +619,9 @@ def _kv4(cache: Kv4Cache, dev: int):
         if cache._device < 0:
             raise ValueError("cache must be on the GPU")
         raise ValueError(f"cache is on cuda:{cache._device}, the current device is cuda:{dev}")
+    if (cache._k_codes.data_ptr(), cache._v_codes.data_ptr(), cache._k_params.data_ptr(),
+            cache._v_params.data_ptr()) != cache._at:
+        raise ValueError("the cache's arrays have moved since it was made: make another Kv4Cache of them")
     return cache._ref
 
 
