@@ -378,8 +378,8 @@ int awq_w4a16_param_grad(const void* dY, const void* X, int dtype, int64_t n_tok
  *   rank: a multiple of 8 from 8 to 128; n_adapters: 1..32768,
  *      n_adapters * rank * in_features (out_features) at most 2^34
  *   Y: [n_tokens, out_features] y_dtype, as awq_w4a16_linear's
- *   low: [n_tokens, rank] fp32 or NULL: what the backward pass reads.  The
- *      workspace's size is asked for with keep_low 1 where it is given (0: NULL)
+ *   low: [n_tokens, rank] fp32 or NULL: what the backward pass reads
+ *   keep_low: whether low will be given; reserved, the size is the same with any
  * low is held in binary32; the second sum takes it in binary32 or as 16-bit parts
  * that keep 16 bits or more (22 in fp16, 24 for AWQ_F32 outputs in bf16), fp16's
  * down to 2^-39 of a token's largest.  The two sums are added in binary32. */

@@ -634,7 +634,7 @@ int awq_w4a16_param_grad(const void* dY, const void* X, int dtype, int64_t n_tok
 
 size_t awq_w4a16_adapted_workspace_size(int64_t n_tokens, int64_t in_features, int64_t out_features,
                                         int group_size, int dtype, int y_dtype, int64_t n_adapters,
-                                        int rank, int keep_low) {
+                                        int rank, int /* keep_low */) {
   if (check_w4(n_tokens, in_features, out_features, group_size, dtype) ||
       check_y_type(dtype, y_dtype) || check_adapters(n_adapters, rank, in_features, out_features))
     return (size_t)-1;
@@ -642,10 +642,7 @@ size_t awq_w4a16_adapted_workspace_size(int64_t n_tokens, int64_t in_features, i
   awq::W4Args a = w4_args(n_tokens, in_features, out_features, group_size, dtype, 0, nullptr, nullptr,
                           nullptr);
   a.y_type = y_dtype;
-  awq::W4Adapt d = adapt_args(nullptr, nullptr, nullptr, n_adapters, rank, nullptr);
-  float kept;
-  d.low = keep_low ? &kept : nullptr;
-  return awq::w4_adapt_workspace(a, d, false);
+  return awq::w4_adapt_workspace(a, adapt_args(nullptr, nullptr, nullptr, n_adapters, rank, nullptr), false);
 }
 
 int awq_w4a16_adapted(const void* X, int dtype, int64_t n_tokens, int64_t in_features,

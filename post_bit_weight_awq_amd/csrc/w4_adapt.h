@@ -1,7 +1,8 @@
 // Adapters of rank R beside a packed product: for each token t of adapter a
 //   low[t, r] = sum_k X[t, k] A[a, r, k],   Y[t, o] += scale[a] low[t] . B[a, o]
-// low comes from k_adapt_low (w4_adapt.hip); the products add the second term to
-// their sums before they leave a block.
+// Tiled products: low comes from k_adapt_low (w4_adapt.hip), and they add the
+// second term to their sums before they leave a block.  Streaming product: further
+// blocks of its launch sum low, and k_adapt_add adds the second term behind it.
 #pragma once
 
 #include <type_traits>
