@@ -25,16 +25,23 @@
 // wavefront every fourth 32 keys through two stages of LDS of its own, filled by
 // direct loads; they are joined through LDS.  A long axis is split over blocks
 // and k_kv4_join joins the splits in order.  Bound by the stream of codes on long
-// caches (64 ragged sequences of up to 4096 keys, 40 heads of 128: 183 us, 4.4
-// TB/s; with the tiles in registers, at half the wavefronts in flight, 200), by
-// the way to the first keys and the join on short ones (one sequence of 777: 10.8
-// us).  Runs of tokens (k_kv4_chunk): a block of eight wavefronts takes 128 rows;
-// they prepare a tile's operands in LDS together, each an eighth.  Bound by VALU
-// issue and the barrier of each tile and, with few sequences, by the longest one:
-// 4 x 256 to 512 tokens behind 512 to 4096 keys, 32 heads on 8: 165 us, 372
-// TFLOP/s, 16 such sequences 464 us, 507 TFLOP/s (in whole units, 4 sequences: 200
-// us; each wavefront by itself, for two row tiles, then 268; four wavefronts of two
-// row tiles 204; of 64 rows 197, and 16 sequences 509; products a tile ahead 255).
+// caches (64 ragged sequences of up to 4096 keys, 40 heads of 128: 182 us, 4.4
+// TB/s, with 82 % of the busy cycles issuing vector operations; with the tiles in
+// registers, at half the wavefronts in flight, 200), by the way to the first keys and
+// the join on short ones (one sequence of 777: 10.3 us).  Heads of 128 in groups of 64
+// take 198 us and in groups of 32 257 (4.3 and 3.7 TB/s): more parameters to work
+// off, and in groups of 32 four to eight registers are spilled, whose reload in a tile
+// waits for the stages asked for ahead as well.
+// Runs of tokens (k_kv4_chunk): a block of eight wavefronts takes 128 rows; they
+// prepare a tile's operands in LDS together, each an eighth.  Bound by VALU issue
+// (about 175 vector operations for a tile's 26 MFMAs: 62 % of the busy cycles issue one,
+// in 35 % the matrix units work) and the barrier of each tile and, with few sequences,
+// by the longest one: 4 x 256 to 512 tokens behind 512 to 4096 keys, 32
+// heads on 8: 149 us, 411 TFLOP/s, 16 such sequences 458 us, 513 TFLOP/s; heads of 128
+// in groups of 64 215 and 725 us, of 32 289 and 985: their registers leave one block a
+// unit.  (On the card where parts took 165 us, whole units: 200 us; each wavefront by
+// itself, for two row tiles, then 268; four wavefronts of two row tiles 204; of 64 rows
+// 197, and 16 sequences 509 for 464; products a tile ahead 255.)
 #include "kv4_device.h"
 #include "w4_internal.h"
 
@@ -960,13 +967,16 @@ static Split split_of(const Kv4Attention& a) {
   s.rows = decode ? kDecodeRows : kChunkRows;
   const int64_t units = row_tiles(a, s.rows) * a.cache.heads;
   const int64_t keys = a.per_seq << a.cache.shift;
-  // Single tokens: four blocks of four wavefronts fit a compute unit.  Where the
+  // Single tokens: four blocks of four wavefronts fit a compute unit (three with four
+  // groups a head).  Where the
   // units fill them by themselves a part costs more than it hides: 64 x 500 keys,
   // 8 kv heads: 12.0 us whole, 16.6 in two; one sequence of 8192, 8 kv heads: 10.5
-  // us in parts of 256, 12.4 of 192 and 11.9 of 512.  Runs: two blocks of eight fit;
-  // half as many again even out sequences of different lengths (4 x 256 to 512
-  // tokens behind 512 to 4096 keys, 32 heads on 8: 165 us, 200 in whole; 8 x 256
-  // behind up to 8192: 310 and 393), parts of 1024 keys too few (217).
+  // us in parts of 256, 12.4 of 192 and 11.9 of 512.  Runs: two blocks of eight fit
+  // with heads of 64 and with groups of 128 (147 and 192 registers leave one with heads
+  // of 128 in groups of 64 and 32, where nothing else was measured); half as many again even
+  // out sequences of different lengths (4 x 256 to 512 tokens behind 512 to 4096 keys,
+  // 32 heads on 8 in groups of 128: 165 us, 200 in whole; 8 x 256 behind up to 8192: 310
+  // and 393), parts of 1024 keys too few (217).
   const int64_t target = decode ? 4 * kCUs : 3 * kCUs;
   s.per = !decode ? 512 : units < kCUs ? 256 : 320;
   int64_t n = (target + units / 2) / units, most = keys / s.per;

@@ -14,10 +14,11 @@
 // 8 threads a group.  The codes of V pass through LDS, so that 16 tokens that fill
 // a tile of the cache write (or read) its words in whole lines; a prompt's tokens
 // do.  A code is rint of the product with 1 / step, which is within 2^-18 of the
-// quotient, and where that lies so near a tie the quotient itself.  Bound by the
-// bytes moved (4095 tokens, 40 heads of 128 in groups of 32: append 36,
-// gather 23 us) and by the launch for a step of decoding (32 tokens, 8
-// heads: 3.5 and 2.9 us).
+// quotient, and where that lies so near a tie the quotient itself.  4095 tokens, 40
+// heads of 128 in groups of 32 are 84 MB of rows and 26 MB of cache: gather, bound
+// by these bytes, takes 23 us (4.7 TB/s); append, bound by VALU issue (about 25
+// operations a value; 96 % of the busy cycles issue one, in groups of 128 too), 36 us (3.1
+// TB/s).  A step of decoding (32 tokens, 8 heads) is a launch: 3.3 and 2.9 us.
 #include "kv4_device.h"
 #include "w4_internal.h"
 
