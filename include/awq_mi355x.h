@@ -424,8 +424,8 @@ int awq_w4a16_adapted_backward(const void* dY, const void* X, const float* low, 
  *   value = step * code + offset
  * in binary32 with IEEE division.  Finite x beyond +-65504 count as that; a
  * group with an infinity or a NaN reads as NaN.  By the roundings of step and
- * offset a value may lie past 65504, below 65600: fp16 outputs round it as such.  Place p * page_size + i is
- * token i of page p.
+ * offset a value may lie past 65504, below 65600: fp16 outputs round it as such.
+ * Place p * page_size + i is token i of page p.
  *   k_codes:  [n_pages, n_heads, page_size, head_dim / 8] uint32.  Word J q + j,
  *             J = head_dim / 32, q = 0..3, holds columns c = 8 (4 j + q) ..
  *             c + 7, column c + i in bits 4i .. 4i + 3
