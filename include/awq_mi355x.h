@@ -382,7 +382,9 @@ int awq_w4a16_param_grad(const void* dY, const void* X, int dtype, int64_t n_tok
  *   keep_low: whether low will be given; reserved, the size is the same with any
  * low is held in binary32; the second sum takes it in binary32 or as 16-bit parts
  * that keep 16 bits or more (22 in fp16, 24 for AWQ_F32 outputs in bf16), fp16's
- * down to 2^-39 of a token's largest.  The two sums are added in binary32. */
+ * down to 2^-39 of a token's largest.  The two sums are added in binary32.  Here
+ * and in the backward pass a sum is off by steps of its terms' magnitudes, in which
+ * fp16 values below 2^-14, the subnormal ones, count as that. */
 size_t awq_w4a16_adapted_workspace_size(int64_t n_tokens, int64_t in_features, int64_t out_features,
                                         int group_size, int dtype, int y_dtype, int64_t n_adapters,
                                         int rank, int keep_low);
@@ -403,7 +405,8 @@ int awq_w4a16_adapted(const void* X, int dtype, int64_t n_tokens, int64_t in_fea
  *   dA, dB: A's and B's shapes in fp32, overwritten; zeros for an adapter without
  *      tokens
  * v and low are held in binary32; the gradients take them as parts of 22 bits
- * (fp16: down to 2^-39 of the largest among the tokens taken together) or 24. */
+ * (fp16: down to 2^-39 of the largest among the tokens taken together) or 24 (bf16,
+ * above 2^-110). */
 size_t awq_w4a16_adapted_backward_workspace_size(int64_t n_tokens, int64_t in_features,
                                                  int64_t out_features, int group_size, int dtype,
                                                  int64_t n_adapters, int rank);
@@ -490,7 +493,8 @@ int awq_kv4_gather(const awq_kv4_cache* cache, const int32_t* slots, int64_t n_t
  *           1..2^20, n_tokens * n_heads < 2^31; max_pages * page_size: up to 2^30
  *   workspace: as the packed-weight operators'; its size depends on the sizes
  *           alone, not on lens
- * Codes meet Q without rounding, scores and sums are binary32, the weight of a
+ * Codes meet Q without rounding, scores and sums are binary32 (off by steps of
+ * their terms, in which fp16 queries below 2^-14 count as that), the weight of a
  * key times the step of its values is held in 16 bits (two bf16 parts), the
  * output rounds once.  Sums have a fixed order for given sizes.  NaN and
  * infinities at keys that a row does not see do not reach it; a query with an
